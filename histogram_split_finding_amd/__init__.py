@@ -75,6 +75,18 @@ class Params(ctypes.Structure):
                 ("min_samples_leaf", i32), ("max_depth", i32), ("objective", i32), ("pad", i32)]
 
 
+class Scores(ctypes.Structure):
+    _fields_ = [("data", vp), ("n_rows", i64), ("row_stride", i64), ("n_classes", i32), ("dtype", i32)]
+
+
+class Teacher(ctypes.Structure):
+    _fields_ = [("values", vp), ("classes", vp), ("rest", vp), ("k", i32), ("pad", i32)]
+
+
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", vp), ("top_k", vp), ("top_p", vp), ("min_p", vp)]
+
+
 class GrowBuffers(ctypes.Structure):
     _fields_ = [("pp", Rows * 2), ("q", vp), ("hist_g", vp), ("hist_cnt", vp), ("splits", vp),
                 ("lists", vp), ("ctrl", vp), ("ws", vp), ("ws_bytes", ctypes.c_size_t),
@@ -137,6 +149,16 @@ def load():
         "gbdt_column_major": (ctypes.c_int, [P(Matrix), vp, vp]),
         "gbdt_grow_tree": (ctypes.c_int, [P(Matrix), P(Features), vp, vp, P(Params), vp, vp,
                                           P(GrowBuffers), vp]),
+        "gbdt_scores_workspace_bytes": (ctypes.c_size_t, [i64, i32]),
+        "gbdt_top_scores": (ctypes.c_int, [P(Scores), i32, ctypes.c_float, vp, vp, vp, vp, ctypes.c_size_t,
+                                           vp]),
+        "gbdt_distill_loss": (ctypes.c_int, [P(Scores), P(Teacher), ctypes.c_float, vp, vp, vp,
+                                             ctypes.c_size_t, vp]),
+        "gbdt_distill_grad": (ctypes.c_int, [P(Scores), P(Teacher), ctypes.c_float, vp, vp, vp, i64, vp,
+                                             ctypes.c_size_t, vp]),
+        "gbdt_distill_step": (ctypes.c_int, [P(Scores), P(Teacher), ctypes.c_float, vp, vp, vp, i64, vp,
+                                             ctypes.c_size_t, vp]),
+        "gbdt_sample_classes": (ctypes.c_int, [P(Scores), vp, P(Sampling), vp, vp, vp, ctypes.c_size_t, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -456,6 +478,142 @@ def gbdt_predict_noalloc(X: Matrix, trees, n_nodes, n_trees, tree_stride, base_s
                                      int(tree_stride), float(base_score), float(learning_rate),
                                      _ptr(out), _ptr(status), _stream(stream))
     _check(rc, "gbdt_predict_noalloc")
+
+
+# ---------------------------------------------------- rows of class scores --
+
+MAX_CLASSES = 1 << 18
+MAX_LISTED = 256
+
+
+def gbdt_scores_workspace_bytes(n_rows: int, n_classes: int) -> int:
+    return int(load().gbdt_scores_workspace_bytes(int(n_rows), int(n_classes)))
+
+
+def _rows_2d(t, name, n=None, c=None):
+    """(rows, columns, row stride) of a device tensor of contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError("%s must be a two-dimensional device tensor" % name)
+    r, w = int(t.shape[0]), int(t.shape[1])
+    if (n is not None and r != n) or (c is not None and w != c):
+        raise ValueError("%s has shape %s, not (%s, %s)" % (name, tuple(t.shape), n, c))
+    if w > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if r > 1 and t.stride(0) < w:
+        raise ValueError("%s has overlapping rows" % name)
+    return r, w, int(t.stride(0))
+
+
+def _scores(x, name="scores") -> Scores:
+    import torch
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if x.dtype not in codes:
+        raise ValueError("%s must be float32, bfloat16 or float16" % name)
+    n, c, stride = _rows_2d(x, name)
+    return Scores(_ptr(x), n, stride, c, codes[x.dtype])
+
+
+def _vector(t, name, dtype, shape, x, optional=False):
+    """Pointer of a contiguous tensor of the given type and shape on x's device."""
+    if t is None and optional:
+        return None
+    if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != x.device or \
+            not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the scores' device"
+                         % (name, dtype, tuple(shape)))
+    return _ptr(t)
+
+
+def _teacher(x, values, classes, rest) -> Teacher:
+    import torch
+    k = int(values.shape[1]) if values.dim() == 2 else 0
+    n = int(x.shape[0])
+    return Teacher(_vector(values, "values", torch.float32, (n, k), x),
+                   _vector(classes, "classes", torch.int32, (n, k), x),
+                   _vector(rest, "rest", torch.float32, (n,), x, optional=True), k, 0)
+
+
+def _grad_rows(x, grad):
+    if grad.dtype != x.dtype or grad.device != x.device:
+        raise ValueError("grad must have the scores' type and device")
+    return _rows_2d(grad, "grad", int(x.shape[0]), int(x.shape[1]))[2]
+
+
+def gbdt_top_scores(scores, k, temperature, values, classes, rest, ws, stream=None):
+    """Teacher records of the rows of `scores` ([n, C] float32, bfloat16 or
+    float16, any row stride): values float32 [n, k] and classes int32 [n, k] in
+    the order of the scores (padded with -inf, -1), rest float32 [n] (or None),
+    the mass outside the list at the temperature."""
+    import torch
+    s = _scores(scores)
+    n, k = int(scores.shape[0]), int(k)
+    rc = load().gbdt_top_scores(ctypes.byref(s), k, float(temperature),
+                                _vector(values, "values", torch.float32, (n, k), scores),
+                                _vector(classes, "classes", torch.int32, (n, k), scores),
+                                _vector(rest, "rest", torch.float32, (n,), scores, optional=True),
+                                _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "gbdt_top_scores")
+
+
+def gbdt_distill_loss(scores, values, classes, rest, temperature, loss, stats, ws, stream=None):
+    """Forward pass of the distillation of `scores` from teacher records (values
+    float32 [n, k], classes int32 [n, k], rest float32 [n] or None): loss
+    float32 [n], and stats float32 [n, 3] for gbdt_distill_grad."""
+    import torch
+    s, t = _scores(scores), _teacher(scores, values, classes, rest)
+    n = int(scores.shape[0])
+    rc = load().gbdt_distill_loss(ctypes.byref(s), ctypes.byref(t), float(temperature),
+                                  _vector(loss, "loss", torch.float32, (n,), scores),
+                                  _vector(stats, "stats", torch.float32, (n, 3), scores),
+                                  _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "gbdt_distill_loss")
+
+
+def gbdt_distill_grad(scores, values, classes, rest, temperature, stats, weight, grad, ws, stream=None):
+    """Backward pass: grad (the scores' type and shape) = weight (float32 [n] or
+    None) times each row's dloss/dscores, from gbdt_distill_loss's stats."""
+    import torch
+    s, t = _scores(scores), _teacher(scores, values, classes, rest)
+    n = int(scores.shape[0])
+    rc = load().gbdt_distill_grad(ctypes.byref(s), ctypes.byref(t), float(temperature),
+                                  _vector(stats, "stats", torch.float32, (n, 3), scores),
+                                  _vector(weight, "weight", torch.float32, (n,), scores, optional=True),
+                                  _ptr(grad), _grad_rows(scores, grad), _ptr(ws), ws.numel(),
+                                  _stream(stream))
+    _check(rc, "gbdt_distill_grad")
+
+
+def gbdt_distill_step(scores, values, classes, rest, temperature, weight, loss, grad, ws, stream=None):
+    """Loss and gradient in one call: what gbdt_distill_loss and
+    gbdt_distill_grad give, from one read of the scores."""
+    import torch
+    s, t = _scores(scores), _teacher(scores, values, classes, rest)
+    n = int(scores.shape[0])
+    rc = load().gbdt_distill_step(ctypes.byref(s), ctypes.byref(t), float(temperature),
+                                  _vector(weight, "weight", torch.float32, (n,), scores, optional=True),
+                                  _vector(loss, "loss", torch.float32, (n,), scores), _ptr(grad),
+                                  _grad_rows(scores, grad), _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "gbdt_distill_step")
+
+
+def gbdt_sample_classes(scores, u, temperature, top_k, top_p, min_p, out, logp, ws, stream=None):
+    """One class per row of `scores`, drawn with the random numbers u (float32
+    [n] in [0, 1)) after per-row temperature (float32 [n]), top_k (int32 [n]),
+    top_p and min_p (float32 [n]), each of them a tensor or None (1, off, off,
+    off): out int32 [n], logp float32 [n] (or None)."""
+    import torch
+    s = _scores(scores)
+    n = int(scores.shape[0])
+    f32 = torch.float32
+    p = Sampling(_vector(temperature, "temperature", f32, (n,), scores, optional=True),
+                 _vector(top_k, "top_k", torch.int32, (n,), scores, optional=True),
+                 _vector(top_p, "top_p", f32, (n,), scores, optional=True),
+                 _vector(min_p, "min_p", f32, (n,), scores, optional=True))
+    rc = load().gbdt_sample_classes(ctypes.byref(s), _vector(u, "u", f32, (n,), scores), ctypes.byref(p),
+                                    _vector(out, "out", torch.int32, (n,), scores),
+                                    _vector(logp, "logp", f32, (n,), scores, optional=True),
+                                    _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "gbdt_sample_classes")
 
 
 # ------------------------------------------------------------ training run --

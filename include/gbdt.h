@@ -662,6 +662,128 @@ int gbdt_grow_tree(const gbdt_matrix* X /* host */, const gbdt_features* ft /* h
                    gbdt_node* nodes_out, int32_t* n_nodes_dev, const gbdt_grow_buffers* b /* host */,
                    void* stream);
 
+/* ------------------------------------------------- rows of class scores -- */
+
+/*
+ * Rows of class scores (logits): row i's score of class c is element
+ * data[i * row_stride + c], 0 <= c < n_classes.  Rows may start at any element
+ * (no alignment beyond the type's own) and may overlap nothing.  An inactive
+ * class has the score -inf.  Host struct holding a device pointer.
+ *
+ * The ORDER of a row's classes, wherever one is meant below, is by score,
+ * descending, equal scores (-0 equals +0) by class, ascending.  A NaN score
+ * counts as -inf in the order.
+ */
+#define GBDT_DTYPE_F32 0
+#define GBDT_DTYPE_BF16 1
+#define GBDT_DTYPE_F16 2
+#define GBDT_MAX_CLASSES (1 << 18)
+#define GBDT_MAX_LISTED 256 /* classes of one teacher record */
+
+typedef struct gbdt_scores {
+  const void* data;
+  int64_t n_rows;
+  int64_t row_stride; /* elements; at least n_classes (n_rows > 1) */
+  int32_t n_classes;
+  int32_t dtype; /* GBDT_DTYPE_* */
+} gbdt_scores;
+
+/*
+ * A teacher's records, one per row: k listed classes with the teacher's
+ * scores, and the probability mass of the classes that are not listed.
+ * values, classes: [n_rows][k] (device).  A class below 0 is padding (its
+ * value is not read); a class of n_classes or more is recorded as
+ * GBDT_E_RANGE and taken as padding; a class listed twice in one row is
+ * recorded as GBDT_E_ARG, and that row's outputs are unspecified.  rest
+ * (device, [n_rows], or NULL: no mass outside the list): in [0, 1], anything
+ * else is recorded as GBDT_E_RANGE and clamped (NaN to 0).  Host struct holding
+ * device pointers.
+ */
+typedef struct gbdt_teacher {
+  const float* values;
+  const int32_t* classes;
+  const float* rest;
+  int32_t k; /* 1 <= k <= GBDT_MAX_LISTED */
+  int32_t pad;
+} gbdt_teacher;
+
+/* Workspace bytes of every call of this section for n_rows x n_classes scores
+ * (0 if a size is out of range). */
+size_t gbdt_scores_workspace_bytes(int64_t n_rows, int32_t n_classes);
+
+/*
+ * Teacher records from a teacher's scores: the first k classes of each row's
+ * order with a score above -inf, in that order, padded with class -1 and value
+ * -inf, and (rest, may be NULL) the softmax mass of the others at the
+ * temperature,
+ *   rest = sum_{c not listed} e_c / sum_c e_c,   e_c = exp((x_c - max x) / T),
+ * 0 for a row without a score above -inf.  A score of +inf takes all the mass.
+ * values, classes: [n_rows][k]; k <= min(n_classes, GBDT_MAX_LISTED);
+ * temperature finite and > 0.
+ */
+int gbdt_top_scores(const gbdt_scores* x /* host */, int32_t k, float temperature, float* values,
+                    int32_t* classes, float* rest, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Distillation of a student's rows x from a teacher's records, with
+ * temperature T (finite, > 0): S the listed classes, r the rest,
+ *   p_j = (1 - r) softmax_j(values / T) over the record,  q = softmax(x / T),
+ *   q_r = sum of q outside S,
+ *   loss = T^2 (sum_j p_j log(p_j / q_j) + r log(r / q_r)),  0 log 0 = 0:
+ * the divergence of the teacher's distribution over S and the rest from the
+ * student's.  Its gradient, times the row's weight,
+ *   in S:       weight T (q_c - p_c)
+ *   outside S:  weight T q_c (1 - r / q_r).
+ * A row whose record lists no class with a value above -inf, and a row without
+ * a score above -inf, has loss 0 and gradient 0; a row of weight 0 has gradient
+ * 0 whatever its scores.  Other rows with a NaN (or +inf) score or value have
+ * NaN results.  A class with p_j > 0 and q_j = 0 makes the loss +inf and leaves
+ * the gradient finite.
+ *
+ * gbdt_distill_loss also writes stats[n_rows][3] = (max x, sum of
+ * exp((x_c - max x) / T) in S, the same outside S), which gbdt_distill_grad
+ * reads: the forward and the backward pass.  gbdt_distill_step does both and
+ * reads the scores once.  weight: [n_rows] or NULL (ones).  grad: the scores'
+ * type, rows grad_stride elements apart; it must not overlap the scores.
+ */
+int gbdt_distill_loss(const gbdt_scores* x /* host */, const gbdt_teacher* t /* host */,
+                      float temperature, float* loss, float* stats, void* ws, size_t ws_bytes,
+                      void* stream);
+int gbdt_distill_grad(const gbdt_scores* x /* host */, const gbdt_teacher* t /* host */,
+                      float temperature, const float* stats, const float* weight, void* grad,
+                      int64_t grad_stride, void* ws, size_t ws_bytes, void* stream);
+int gbdt_distill_step(const gbdt_scores* x /* host */, const gbdt_teacher* t /* host */,
+                      float temperature, const float* weight, float* loss, void* grad,
+                      int64_t grad_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One class drawn per row from given random numbers u[n_rows] in [0, 1).  With
+ * e_c = exp((x_c - max x) / T), the kept classes are: the first top_k of the
+ * row's order (top_k <= 0: all); of these the shortest prefix whose e sum is at
+ * least top_p times theirs (top_p = 1: all; the first is always kept); of these
+ * the ones with e_c >= min_p.  The drawn class is the first of the kept ones,
+ * in the order, whose running e sum exceeds u times the sum over all kept ones.
+ * T = 0 draws the first class of the order.  Sums and comparisons are carried
+ * in 64 bits (fixed point, so they do not depend on the order of addition).
+ * out[n_rows]: the class, or -1 for a row without a score above -inf;
+ * logp[n_rows] (or NULL): log(e_c / sum over the kept ones), -inf with -1.  A score of +inf
+ * has e = 1 and leaves all finite ones e = 0.
+ * Per-row parameters (device, [n_rows]); NULL: T = 1, top_k = 0, top_p = 1,
+ * min_p = 0.  T finite and >= 0; top_p, min_p in [0, 1]; u in [0, 1): a
+ * row that breaks this is recorded as GBDT_E_RANGE and gets -1.  Host struct
+ * holding device pointers.
+ */
+typedef struct gbdt_sampling {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} gbdt_sampling;
+
+int gbdt_sample_classes(const gbdt_scores* x /* host */, const float* u,
+                        const gbdt_sampling* p /* host */, int32_t* out, float* logp, void* ws,
+                        size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
