@@ -29,8 +29,15 @@ namespace gbdt {
 
 namespace {
 
-// What a launch does: write the statistics, write the loss, write the gradient.
-constexpr int kStats = 1, kLoss = 2, kGrad = 4;
+// What a launch does: write the statistics, write the loss, write the gradient;
+// of rows shared by several workgroups, write the part's sums or read them.
+constexpr int kStats = 1, kLoss = 2, kGrad = 4, kPart = 8, kJoin = 16;
+
+struct PartSum {
+  double s_out;
+  float m;
+  uint32_t pad;
+};
 
 struct DistillArgs {
   const void* x;
@@ -40,7 +47,7 @@ struct DistillArgs {
   const int32_t* tc;
   const float* tr;
   float T;
-  double c;  // log2(e) / T
+  double c, inv_T;  // log2(e) / T, 1 / T
   const float* weight;
   float* stats_out;
   const float* stats_in;
@@ -48,6 +55,9 @@ struct DistillArgs {
   void* grad;
   int64_t ldg;
   int32_t* err;
+  PartSum* parts;  // [n][n_joined]
+  int32_t n_parts, part_len, n_joined;
+  int64_t row0;  // of this launch
 };
 
 // The rest's mass of row i, clamped to [0, 1].
@@ -59,236 +69,409 @@ __device__ __forceinline__ double row_rest(const DistillArgs& a, int64_t i, bool
   return r > 1.0f ? 1.0 : 0.0;
 }
 
-// The loss from the row's sums; k_sum = sum_j p_j ((t_j - t_max) - (x_j - m)).
-__device__ __forceinline__ double row_loss(double T, double r, double z, double k_sum, double s_in,
+// The loss from the row's sums; kd = sum_j e_j ((t_j - t_max) - (x_j - m)).
+__device__ __forceinline__ double row_loss(double T, double inv_T, double r, double z, double kd, double s_in,
                                            double s_out) {
   const double s = s_in + s_out;
-  double l = k_sum / T;
-  if (r < 1.0) l += (1.0 - r) * log((1.0 - r) * s / z);
-  if (r > 0.0) l += r * log(r * s / s_out);
+  double l = 0.0;
+  if (r < 1.0) {
+    const double iz = rcp_64(z);
+    l += (1.0 - r) * (kd * iz * inv_T + log_64((1.0 - r) * s * iz));
+  }
+  if (r > 0.0) l += s_out == 0.0 ? __builtin_inf() : r * log_64(r * s * rcp_64(s_out));
   return T * T * l;
 }
 
-// One thread per row of at most CMAX classes; every exponential in FP64 (a
-// row's few terms do not average rounding errors away, and a small loss is
-// what is left when terms of order 1 cancel).
-template <int DT, int CMAX, int MODE>
-__global__ void __launch_bounds__(256) k_distill_rows(const DistillArgs a) {
+// One thread per row of at most CMAX classes, R rows a workgroup; k <= C.  Rows,
+// records and gradients pass through LDS, so that global memory sees whole
+// lines (a thread's own row is a stride of 4 C bytes from its neighbours'), in
+// rows of C | 1 words, which spreads the threads over the banks.  All loads are
+// in flight at once: the rows are few microseconds in all, one memory latency
+// each way.  The exponentials that the loss needs are in FP64 (a row's few
+// terms do not average rounding errors away, and a small loss is what is left
+// when terms of order 1 cancel).
+template <int DT, int R, int CMAX, int MODE>
+__global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const DistillArgs a) {
   using Elem = typename Score<DT>::Elem;
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= a.n) return;
-  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-  float x[CMAX], t[CMAX];
-#pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    x[c] = c < a.C ? Score<DT>::to_f32(xr[c]) : -kInf;
-    t[c] = -kInf;
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x;
+  const int64_t i0 = int64_t(blockIdx.x) * R, i = i0 + tid;
+  const int32_t rows = (int32_t)(a.n - i0 < R ? a.n - i0 : R);
+  const int32_t C = a.C, k = a.k, P = C | 1, PK = k | 1;
+  const RowDiv by_c(C), by_k(k);
+  float* __restrict__ all_t = lds + R * P;
+  int32_t* __restrict__ all_c = reinterpret_cast<int32_t*>(all_t + R * PK);
+  const Elem* __restrict__ xg = static_cast<const Elem*>(a.x) + i0 * a.ld;
+  {
+    Staged<R, CMAX, float> xs, ts;
+    Staged<R, CMAX, int32_t> cs;
+    xs.load(
+        rows, C, a.ld == C, by_c, [&](int32_t e) { return Score<DT>::to_f32(xg[(uint32_t)e]); },
+        [&](int32_t row, int32_t c) { return Score<DT>::to_f32(xg[row * a.ld + c]); });
+    const float* __restrict__ tg = a.tv + i0 * k;
+    const int32_t* __restrict__ cg = a.tc + i0 * k;
+    ts.load(rows, k, true, by_k, [&](int32_t e) { return tg[(uint32_t)e]; }, [](int32_t, int32_t) { return 0.0f; });
+    cs.load(rows, k, true, by_k, [&](int32_t e) { return cg[(uint32_t)e]; }, [](int32_t, int32_t) { return 0; });
+    ts.put(rows, k, by_k, all_t);
+    cs.put(rows, k, by_k, all_c);
+    xs.put(rows, C, by_c, lds);
   }
-  uint32_t in_s = 0u;
-  for (int32_t j = 0; j < a.k; ++j) {
-    const int32_t cls = a.tc[i * a.k + j];
-    if (cls < 0) continue;
-    if (cls >= a.C) {
-      dev_error(a.err, GBDT_E_RANGE);
-      continue;
+  const bool mine = tid < rows;
+  const double r = mine ? row_rest(a, i, true) : 0.0;
+  float wt = 1.0f, m = -kInf, tm = -kInf;
+  double s_in = 0.0, s_out = 0.0;
+  if (mine && (MODE & kGrad) && a.weight != nullptr) wt = a.weight[i];
+  if (mine && !(MODE & kStats)) {
+    m = a.stats_in[3 * i];
+    s_in = a.stats_in[3 * i + 1];
+    s_out = a.stats_in[3 * i + 2];
+  }
+  __syncthreads();
+  float* __restrict__ x = lds + tid * P;
+  float* __restrict__ tv = all_t + tid * PK;
+  const int32_t* __restrict__ tc = all_c + tid * PK;
+  if (mine) {
+    if (MODE & kStats) {
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c) m = c < C ? __builtin_fmaxf(m, x[c]) : m;
     }
-    if (in_s >> cls & 1u) dev_error(a.err, GBDT_E_ARG);
-    in_s |= 1u << cls;
-    const float tv = a.tv[i * a.k + j];
+    uint32_t in_s = 0u;
+    bool has = false;
+    for (int32_t j = 0; j < k; ++j) {
+      const int32_t cls = tc[j];
+      if (cls < 0) continue;
+      if (cls >= C) {
+        dev_error(a.err, GBDT_E_RANGE);
+        continue;
+      }
+      if (in_s >> cls & 1u) dev_error(a.err, GBDT_E_ARG);
+      in_s |= 1u << cls;
+      const float t = tv[j];
+      tm = __builtin_fmaxf(tm, t);
+      has = has || !(t == -kInf);
+    }
+    const double ms = m == -kInf ? 0.0 : (double)m;
+    const double ts = tm == -kInf ? 0.0 : (double)tm;
+    double z = 0.0, kd = 0.0;
+    for (int32_t j = 0; j < k; ++j) {
+      const int32_t cls = tc[j];
+      if (cls < 0 || cls >= C) continue;
+      const double d = (double)tv[j] - ts;
+      const double e = exp2_64(d * a.c);
+      z += e;
+      if ((MODE & kLoss) && !(e == 0.0)) kd += e * (d - ((double)x[cls] - ms));
+      if (MODE & kGrad) tv[j] = (float)e;
+    }
+    if (MODE & kStats) {
 #pragma unroll
-    for (int c = 0; c < CMAX; ++c) t[c] = c == cls ? tv : t[c];
+      for (int c = 0; c < CMAX; ++c) {
+        if (c < C) {
+          const double w = exp2_64(((double)x[c] - ms) * a.c);
+          if (in_s >> c & 1u) s_in += w; else s_out += w;
+          if (MODE & kGrad) x[c] = (float)w;
+        }
+      }
+    }
+    const double s = s_in + s_out;
+    const bool live = has && !(s == 0.0);
+    if ((MODE & kStats) && a.stats_out != nullptr) {
+      a.stats_out[3 * i] = m;
+      a.stats_out[3 * i + 1] = (float)s_in;
+      a.stats_out[3 * i + 2] = (float)s_out;
+    }
+    if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s_in, s_out) : 0.0f;
+    if (MODE & kGrad) {
+      const bool counts = live && !(wt == 0.0f);
+      const double g = (double)wt * (double)a.T;
+      const double share = s_out > 0.0 ? 1.0 - r * s * rcp_64(s_out) : (s_out == 0.0 ? 0.0 : s_out);
+      const double inv = rcp_64(s);
+      const float in = (float)inv, out = (float)(g * share * inv);
+      const float cf = exponent_scale(a.c), mf = (float)ms;
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c) {
+        if (c < C) {
+          const float w = MODE & kStats ? x[c] : exp2_32((x[c] - mf) * cf);
+          x[c] = counts ? w * (in_s >> c & 1u ? in : out) : 0.0f;
+        }
+      }
+      if (counts) {
+        const double pz = (1.0 - r) * rcp_64(z);
+        for (int32_t j = 0; j < k; ++j) {
+          const int32_t cls = tc[j];
+          if (cls < 0 || cls >= C) continue;
+          x[cls] = (float)(g * ((double)x[cls] - (double)tv[j] * pz));
+        }
+      }
+    }
   }
-  const double r = row_rest(a, i, true);
-  float m = -kInf, tm = -kInf;
+  if (MODE & kGrad) {
+    __syncthreads();
+    Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i0 * a.ldg;
+    unstage<R, CMAX>(
+        rows, C, a.ldg == C, by_c, lds, [&](int32_t e, float v) { gr[(uint32_t)e] = Score<DT>::from_f32(v); },
+        [&](int32_t row, int32_t c, float v) { gr[row * a.ldg + c] = Score<DT>::from_f32(v); });
+  }
+}
+
+// One workgroup per row, or per part of one: `part_len` classes (a multiple of
+// NT * kBlk) of a row that n_parts workgroups share; a first launch (kPart)
+// leaves each part's sums, a second (kJoin) adds them up.
+//
+// One pass takes the sum against a reference that is the first maximum the
+// thread meets and moves only when a score is above it by 2^20 in the
+// exponential, so a vector costs no rescaling; the second writes the gradient.
+// LDS: a bit per class (set: listed), laid out so that a thread's part of a
+// block is one word (or half of one).  Thread j of the first k owns entry j
+// (and j + NT, ...) of the record; its class's gradient replaces, behind a
+// barrier, what the vector stores left there.
+template <int DT, int NT, int MODE>
+__global__ void __launch_bounds__(NT, NT == 64 ? 6 : 8) k_distill_block(const DistillArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec, BLK = kBlk<DT>, W = NT / 64;
+  constexpr int KPT = (GBDT_MAX_LISTED + NT - 1) / NT;
+  constexpr bool kSums = (MODE & kStats) && !(MODE & kJoin);
+  extern __shared__ uint32_t bits[];
+  __shared__ float sh_m[W], sh_t[W];
+  __shared__ double sh_d[4][W];
+  const int tid = threadIdx.x, wid = tid >> 6;
+  const float cf = exponent_scale(a.c);
+  const uint32_t in_launch = a.n_parts > 1 ? blockIdx.x / (uint32_t)a.n_parts : blockIdx.x;
+  const int32_t part = (int32_t)(blockIdx.x - in_launch * (uint32_t)a.n_parts);
+  const int64_t i = a.row0 + in_launch;
+  const int32_t lo = part * a.part_len;
+  const int32_t hi = a.C - lo < a.part_len ? a.C : lo + a.part_len;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  RawBlock<DT> raw;
+  if (kSums) raw = load_block<DT, NT>(xr, lo, hi);
+  for (int32_t w = tid; w < ((hi - lo + NT * BLK - 1) / (NT * BLK) * BLK + 31) / 32 * NT; w += NT) bits[w] = 0u;
+  int32_t cls[KPT];
+  float t[KPT], xj[KPT];
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) {
+    const int32_t j = tid + u * NT;
+    cls[u] = -1;
+    t[u] = -kInf;
+    xj[u] = -kInf;
+    if (j < a.k) {
+      cls[u] = a.tc[i * a.k + j];
+      if (cls[u] >= a.C) {
+        dev_error(a.err, GBDT_E_RANGE);
+        cls[u] = -1;
+      }
+      if (cls[u] >= 0) {
+        t[u] = a.tv[i * a.k + j];
+        xj[u] = Score<DT>::to_f32(xr[cls[u]]);
+      }
+    }
+  }
+  __syncthreads();
+  float tm = -kInf;
   bool has = false;
 #pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    m = __builtin_fmaxf(m, x[c]);
-    tm = __builtin_fmaxf(tm, t[c]);
-    has = has || !(t[c] == -kInf);
+  for (int u = 0; u < KPT; ++u) {
+    if (cls[u] >= lo && cls[u] < hi) {
+      // (block, vector, thread, element) of the class
+      const int32_t e = cls[u] - lo, in = e % (NT * BLK), blk = e / (NT * BLK);
+      const int32_t bit = blk * BLK % 32 + in / (NT * VE) * VE + in % VE;
+      const int32_t word = blk * BLK / 32 * NT + in / VE % NT;
+      if (atomicOr(&bits[word], 1u << bit) >> bit & 1u) dev_error(a.err, GBDT_E_ARG);
+    }
+    tm = __builtin_fmaxf(tm, t[u]);
+    has = has || !(t[u] == -kInf);
   }
-  if (!(MODE & kStats)) m = a.stats_in[3 * i];
+  __syncthreads();
+  float m = -kInf, ref = -kInf;
+  double so = 0.0;
+  if (kSums) {
+    for (int32_t base = lo, b = 0;; b += BLK) {
+      const uint32_t in_s = bits[(b / 32) * NT + tid] >> (b % 32);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        float f[VE];
+        unpack<DT>(raw.v[j], f);
+        const float vm = max_of(f);
+        m = __builtin_fmaxf(m, vm);
+        if ((vm - ref) * cf > 20.0f) {  // (the first finite score among them)
+          so *= exp2_64(((double)ref - (double)vm) * a.c);
+          ref = vm;
+        }
+        const uint32_t in_v = in_s >> (j * VE) & ((1u << VE) - 1u);
+        if (in_v) {
+#pragma unroll
+          for (int q = 0; q < VE; ++q) f[q] = in_v >> q & 1u ? -kInf : f[q];
+        }
+        const float rf = ref == -kInf ? 0.0f : ref;
+#pragma unroll
+        for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - rf) * cf);
+        so += (double)sum_of(f);
+        __builtin_amdgcn_sched_barrier(0);  // (vector by vector: fewer registers)
+      }
+      base += NT * BLK;
+      if (base >= hi) break;
+      raw = load_block<DT, NT>(xr, base, hi);
+    }
+  } else if (MODE & kJoin) {
+    if (tid < a.n_joined) {
+      const PartSum p = a.parts[i * a.n_joined + tid];
+      m = ref = p.m;
+      so = p.s_out;
+    }
+  } else {
+    m = a.stats_in[3 * i];
+  }
+  // the row's maxima; NaN in the record counts as an entry
+  m = wave_max(m);
+  tm = wave_max(tm);
+  if ((tid & 63) == 0) {
+    sh_m[wid] = m;
+    sh_t[wid] = tm;
+  }
+  has = __syncthreads_or(has);
+  m = across_waves<W>(sh_m, [](float u, float v) { return __builtin_fmaxf(u, v); });
+  tm = across_waves<W>(sh_t, [](float u, float v) { return __builtin_fmaxf(u, v); });
   const double ms = m == -kInf ? 0.0 : (double)m;
   const double ts = tm == -kInf ? 0.0 : (double)tm;
-  double w[CMAX], p[CMAX], z = 0.0, s_in = 0.0, s_out = 0.0;
-#pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    w[c] = exp2_64(((double)x[c] - ms) * a.c);
-    p[c] = exp2_64(((double)t[c] - ts) * a.c);
-    z += p[c];
-    if (in_s >> c & 1u) s_in += w[c]; else s_out += w[c];
+  if ((MODE & kStats) && ref != m) so *= exp2_64(((double)ref - ms) * a.c);
+  if (MODE & kPart) {
+    so = block_sum<NT>(so, sh_d[0]);
+    if (tid == 0) a.parts[i * a.n_parts + part] = PartSum{so, m, 0u};
+    return;
   }
+  double e[KPT], wj[KPT], z = 0.0, kd = 0.0, si = 0.0;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) {
+    const double d = (double)t[u] - ts, dx = (double)xj[u] - ms;
+    e[u] = exp2_64(d * a.c);
+    wj[u] = exp2_64(dx * a.c);
+    z += e[u];
+    if (!(e[u] == 0.0)) kd += e[u] * (d - dx);
+    si += wj[u];
+  }
+  double sum[4] = {z, kd, si, so};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    sum[v] = wave_sum(sum[v]);
+    if ((tid & 63) == 0) sh_d[v][wid] = sum[v];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < 4; ++v) sum[v] = across_waves<W>(sh_d[v], [](double p, double q) { return p + q; });
+  z = sum[0];
+  kd = sum[1];
+  double s_in = sum[2], s_out = sum[3];
   if (!(MODE & kStats)) {
     s_in = a.stats_in[3 * i + 1];
     s_out = a.stats_in[3 * i + 2];
   }
+  const double r = row_rest(a, i, tid == 0);
   const double s = s_in + s_out;
   const bool live = has && !(s == 0.0);
-  const double pz = live ? (1.0 - r) / z : 0.0;
-  if ((MODE & kStats) && a.stats_out != nullptr) {
-    a.stats_out[3 * i] = m;
-    a.stats_out[3 * i + 1] = (float)s_in;
-    a.stats_out[3 * i + 2] = (float)s_out;
-  }
-  if (MODE & kLoss) {
-    double k_sum = 0.0;
-#pragma unroll
-    for (int c = 0; c < CMAX; ++c) {
-      const double pc = p[c] * pz;
-      if (!(pc == 0.0)) k_sum += pc * (((double)t[c] - ts) - ((double)x[c] - ms));
+  if (tid == 0 && part == 0) {
+    if ((MODE & kStats) && a.stats_out != nullptr) {
+      a.stats_out[3 * i] = m;
+      a.stats_out[3 * i + 1] = (float)s_in;
+      a.stats_out[3 * i + 2] = (float)s_out;
     }
-    a.loss[i] = live ? (float)row_loss(a.T, r, z, k_sum, s_in, s_out) : 0.0f;
+    if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s_in, s_out) : 0.0f;
   }
   if (MODE & kGrad) {
     const float wt = a.weight != nullptr ? a.weight[i] : 1.0f;
     const bool counts = live && !(wt == 0.0f);
     const double g = (double)wt * (double)a.T;
-    const double inv = 1.0 / s;
-    const double share = s_out > 0.0 ? 1.0 - r * s / s_out : (s_out == 0.0 ? 0.0 : s_out);
+    const double share = s_out > 0.0 ? 1.0 - r * s * rcp_64(s_out) : (s_out == 0.0 ? 0.0 : s_out);
+    const double inv = rcp_64(s);
+    const float scale = (float)(g * share * inv);
+    const float mf = (float)ms;
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
+    for (int32_t base = lo; base < hi; base += NT * BLK) {
+      RawBlock<DT> o;
+      if (counts) {
+        raw = load_block<DT, NT>(xr, base, hi);
 #pragma unroll
-    for (int c = 0; c < CMAX; ++c) {
-      const double q = w[c] * inv;
-      const double d = (in_s >> c & 1u) ? q - p[c] * pz : q * share;
-      if (c < a.C) gr[c] = Score<DT>::from_f32(counts ? (float)(g * d) : 0.0f);
+        for (int j = 0; j < kVecs; ++j) {
+          float f[VE];
+          unpack<DT>(raw.v[j], f);
+#pragma unroll
+          for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - mf) * cf) * scale;
+          o.v[j] = pack<DT>(f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        o = RawBlock<DT>{};
+      }
+      store_block<DT, NT>(gr, base, hi, o);
     }
-  }
-}
-
-// One workgroup per row.  LDS: a bit per class (set: listed).  Thread j < k
-// owns entry j of the record: its class's gradient is its to write, and the
-// vector stores leave the listed classes out, so no element is written twice.
-template <int DT, int NT, int MODE>
-__global__ void __launch_bounds__(NT) k_distill_block(const DistillArgs a) {
-  using Elem = typename Score<DT>::Elem;
-  constexpr int VE = Score<DT>::kVec;
-  extern __shared__ uint32_t bits[];
-  __shared__ float shf[NT / 64];
-  __shared__ double shd[NT / 64];
-  const int tid = threadIdx.x;
-  const int32_t C = a.C;
-  const float cf = (float)a.c;
-  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-    const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-    for (int32_t wd = tid; wd < (C + 31) / 32; wd += NT) bits[wd] = 0u;
     __syncthreads();
-    int32_t cls = -1;
-    float t = -kInf, xj = -kInf;
-    if (tid < a.k) {
-      cls = a.tc[i * a.k + tid];
-      if (cls >= C) {
-        dev_error(a.err, GBDT_E_RANGE);
-        cls = -1;
-      }
-      if (cls >= 0) {
-        const uint32_t b = 1u << (cls & 31);
-        if (atomicOr(&bits[cls >> 5], b) & b) dev_error(a.err, GBDT_E_ARG);
-        t = a.tv[i * a.k + tid];
-        xj = Score<DT>::to_f32(xr[cls]);
-      }
-    }
-    const double r = row_rest(a, i, tid == 0);
-    const bool has = __syncthreads_or(!(t == -kInf));
-    const float tm = block_max<NT>(t, shf);
-    const double ts = tm == -kInf ? 0.0 : (double)tm;
-    const double e = exp2_64(((double)t - ts) * a.c);
-    const double z = block_sum<NT>(e, shd);
-    float m = -kInf;
-    double s_in, s_out;
-    if (MODE & kStats) {
-      for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
-        float f[VE];
-        load_chunk<DT>(xr, c0, C, f);
+    if (counts) {
 #pragma unroll
-        for (int q = 0; q < VE; ++q) m = __builtin_fmaxf(m, f[q]);
-      }
-      m = block_max<NT>(m, shf);
-    } else {
-      m = a.stats_in[3 * i];
+      for (int u = 0; u < KPT; ++u)
+        if (cls[u] >= lo && cls[u] < hi)
+          gr[cls[u]] = Score<DT>::from_f32((float)(g * (wj[u] * inv - e[u] * ((1.0 - r) * rcp_64(z)))));
     }
-    const float mf = m == -kInf ? 0.0f : m;
-    const double ms = (double)mf;
-    const double wj = cls >= 0 ? exp2_64(((double)xj - ms) * a.c) : 0.0;
-    if (MODE & kStats) {
-      s_in = block_sum<NT>(wj, shd);
-      double so = 0.0;
-      for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
-        float f[VE];
-        load_chunk<DT>(xr, c0, C, f);
-        const uint32_t in_s = bits[c0 >> 5] >> (c0 & 31);
-#pragma unroll
-        for (int q = 0; q < VE; ++q) {
-          const float wq = exp2_32((f[q] - mf) * cf);
-          so += (in_s >> q & 1u) ? 0.0 : (double)wq;
-        }
-      }
-      s_out = block_sum<NT>(so, shd);
-    } else {
-      s_in = a.stats_in[3 * i + 1];
-      s_out = a.stats_in[3 * i + 2];
-    }
-    const double s = s_in + s_out;
-    const bool live = has && !(s == 0.0);
-    const double pj = live ? e * (1.0 - r) / z : 0.0;
-    if ((MODE & kStats) && a.stats_out != nullptr && tid == 0) {
-      a.stats_out[3 * i] = m;
-      a.stats_out[3 * i + 1] = (float)s_in;
-      a.stats_out[3 * i + 2] = (float)s_out;
-    }
-    if (MODE & kLoss) {
-      const double d = (((double)t - ts) - ((double)xj - ms));
-      const double k_sum = block_sum<NT>(pj == 0.0 ? 0.0 : pj * d, shd);
-      if (tid == 0) a.loss[i] = live ? (float)row_loss(a.T, r, z, k_sum, s_in, s_out) : 0.0f;
-    }
-    if (MODE & kGrad) {
-      const float wt = a.weight != nullptr ? a.weight[i] : 1.0f;
-      const bool counts = live && !(wt == 0.0f);
-      const double g = (double)wt * (double)a.T;
-      const double share = s_out > 0.0 ? 1.0 - r * s / s_out : (s_out == 0.0 ? 0.0 : s_out);
-      const float scale = counts ? (float)(g * share / s) : 0.0f;
-      Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
-      for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
-        float f[VE];
-        load_chunk<DT>(xr, c0, C, f);
-        const uint32_t in_s = (bits[c0 >> 5] >> (c0 & 31)) & ((1u << VE) - 1u);
-        Vec16<DT> o;
-#pragma unroll
-        for (int q = 0; q < VE; ++q)
-          o.e[q] = Score<DT>::from_f32(counts ? exp2_32((f[q] - mf) * cf) * scale : 0.0f);
-        if (in_s == 0u && c0 + VE <= C) {
-          __builtin_memcpy(gr + c0, &o, 16);
-        } else {
-#pragma unroll
-          for (int q = 0; q < VE; ++q)
-            if (c0 + q < C && !(in_s >> q & 1u)) gr[c0 + q] = o.e[q];
-        }
-      }
-      if (cls >= 0) gr[cls] = Score<DT>::from_f32(counts ? (float)(g * (wj / s - pj)) : 0.0f);
-    }
-    __syncthreads();  // (the bits are free)
   }
 }
 
-constexpr int64_t kMaxRowGrid = 1 << 20;  // workgroups of a row launch, at most
+template <int DT, int R, int CMAX, int MODE>
+void launch_rows(const DistillArgs& a, hipStream_t s) {
+  const size_t lds = size_t(R) * 4 * ((a.C | 1) + 2 * (a.k | 1));
+  const dim3 grid((unsigned)((a.n + R - 1) / R));
+  hipLaunchKernelGGL((k_distill_rows<DT, R, CMAX, MODE>), grid, dim3(R), lds, s, a);
+}
 
+template <int DT, int NT, int MODE>
+void launch_block(DistillArgs a, hipStream_t s) {
+  constexpr int32_t kStep = NT * kBlk<DT>;
+  if (a.n_parts == 1) a.part_len = (a.C + kStep - 1) / kStep * kStep;
+  const size_t lds = size_t((a.part_len / kStep * kBlk<DT> + 31) / 32) * NT * 4;
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
+    const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    hipLaunchKernelGGL((k_distill_block<DT, NT, MODE>), dim3((unsigned)(n * a.n_parts)), dim3(NT), lds, s, a);
+  }
+}
+
+// Threads for a row: a wave up to 2,048 classes (no barrier waits for others),
+// 1,024 threads where a row is long enough to be read twice from memory: then
+// fewer rows are between their two reads at a time, and more of them are still
+// in the last-level cache (step, 4,096 x 131,072 bf16: 444 us with 1,024
+// threads, 496 with 512, 588 with 256; grad, 2,048 x 50,001 f32: 152, 161, 164).
+// In between 256: more rows side by side hide the rows' own latencies (loss,
+// 1,000 x 32,003 f16: 20 us with 256 threads, 22 with 512, 34 with 1,024).
+// Few rows are split: 1 x 131,072 f32 takes 12 us with 32 workgroups and 26 with
+// one, 64 rows bf16 18 and 25; at 128 rows both take 27.
 template <int DT, int MODE>
-int launch_distill(const DistillArgs& a, hipStream_t s) {
+int launch_distill(const DistillArgs& args, hipStream_t s) {
+  DistillArgs a = args;
+  a.n_parts = a.n_joined = 1;
+  a.part_len = 0;
+  constexpr int32_t kPartStep = 256 * kBlk<DT>;
+  const int32_t steps = (a.C + kPartStep - 1) / kPartStep;
   diag_begin(kDiagDistill, s);
-  if (a.C <= kRowsMaxClasses) {
-    const dim3 grid((unsigned)((a.n + 255) / 256));
-    if (a.C <= 8)
-      hipLaunchKernelGGL((k_distill_rows<DT, 8, MODE>), grid, dim3(256), 0, s, a);
-    else if (a.C <= 16)
-      hipLaunchKernelGGL((k_distill_rows<DT, 16, MODE>), grid, dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((k_distill_rows<DT, 32, MODE>), grid, dim3(256), 0, s, a);
+  const bool short_rows = a.C <= kRowsMaxClasses && a.k <= a.C;
+  if (short_rows && a.C <= 8) {
+    launch_rows<DT, 64, 8, MODE>(a, s);
+  } else if (short_rows && a.C <= 16) {
+    launch_rows<DT, 128, 16, MODE>(a, s);
+  } else if (short_rows) {
+    launch_rows<DT, 64, 32, MODE>(a, s);
+  } else if (a.n <= kSplitRows && steps >= 4) {
+    const int32_t want = (int32_t)(kSplitGrid / a.n);
+    const int32_t per = (steps + want - 1) / want;
+    const int32_t parts = (steps + per - 1) / per;
+    a.part_len = per * kPartStep;
+    a.n_parts = a.n_joined = parts;
+    if (MODE & kStats) {
+      launch_block<DT, 256, kStats | kPart>(a, s);
+      if (!(MODE & kGrad)) a.n_parts = 1;
+      launch_block<DT, 256, MODE | kJoin>(a, s);
+    } else {
+      launch_block<DT, 256, MODE>(a, s);
+    }
+  } else if (a.C <= 2048) {
+    launch_block<DT, 64, MODE>(a, s);
+  } else if (a.C <= 40000) {
+    launch_block<DT, 256, MODE>(a, s);
   } else {
-    const dim3 grid((unsigned)(a.n < kMaxRowGrid ? a.n : kMaxRowGrid));
-    const size_t lds = size_t((a.C + 31) / 32) * 4;
-    if (a.C <= 8192)
-      hipLaunchKernelGGL((k_distill_block<DT, 256, MODE>), grid, dim3(256), lds, s, a);
-    else
-      hipLaunchKernelGGL((k_distill_block<DT, 1024, MODE>), grid, dim3(1024), lds, s, a);
+    launch_block<DT, 1024, MODE>(a, s);
   }
   diag_end(s);
   const hipError_t e = hipGetLastError();
@@ -330,12 +513,14 @@ int distill(const gbdt_scores* x, const gbdt_teacher* t, float temperature, cons
   a.tr = t->rest;
   a.T = temperature;
   a.c = kLog2e / (double)temperature;
+  a.inv_T = 1.0 / (double)temperature;
   a.weight = weight;
   a.stats_out = stats_out;
   a.stats_in = stats_in;
   a.loss = loss;
   a.grad = grad;
   a.ldg = grad_stride;
+  a.parts = reinterpret_cast<PartSum*>(static_cast<char*>(ws) + sizeof(WsCtrl));
   a.err = &static_cast<WsCtrl*>(ws)->err;
   switch (x->dtype) {
     case GBDT_DTYPE_F32: return launch_distill<GBDT_DTYPE_F32, MODE>(a, s);
@@ -378,7 +563,7 @@ extern "C" {
 
 size_t gbdt_scores_workspace_bytes(int64_t n_rows, int32_t n_classes) {
   if (n_rows < 0 || n_rows > (int64_t(1) << 31) || n_classes < 1 || n_classes > GBDT_MAX_CLASSES) return 0;
-  return sizeof(WsCtrl);
+  return sizeof(WsCtrl) + kScoresPartBytes;
 }
 
 int gbdt_distill_loss(const gbdt_scores* x, const gbdt_teacher* t, float temperature, float* loss,

@@ -694,8 +694,6 @@ __global__ void __launch_bounds__(256) k_sample_rows(const SampleArgs a) {
   if (a.logp != nullptr) a.logp[i] = (float)log(ew / W);
 }
 
-constexpr int64_t kMaxRowGrid = 1 << 20;  // workgroups of a row launch, at most
-
 template <int DT>
 int launch_top(const TopArgs& a, hipStream_t s) {
   diag_begin(kDiagTopScores, s);
