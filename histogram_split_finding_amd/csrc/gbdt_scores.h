@@ -91,23 +91,38 @@ __device__ __forceinline__ Vec16<DT> pack(const float (&f)[Score<DT>::kVec]) {
 }
 
 // Elements [c, c + kVec) of a row of C, c < C or not: -inf past the row's end.
-// (The elements are shifted in from the last one down, in a loop: one thread
-// of a row comes here, and unrolled it would cost every kernel registers.)
+// The vector that the end cuts is the row's last one, shifted down: one load
+// (a load for each element would be a chain of latencies in every short row).
 template <int DT>
 __device__ __forceinline__ Vec16<DT> load_tail(const typename Score<DT>::Elem* __restrict__ row, int32_t c, int32_t C) {
-  if (c + Score<DT>::kVec <= C) return load_vec<DT>(row + c);
+  constexpr int VE = Score<DT>::kVec;
+  if (c + VE <= C) return load_vec<DT>(row + c);
   constexpr uint32_t inf = DT == GBDT_DTYPE_F32 ? 0xff800000u : DT == GBDT_DTYPE_BF16 ? 0xff80ff80u : 0xfc00fc00u;
   Vec16<DT> v = {{inf, inf, inf, inf}};
+  if (c >= C) return v;
+  if (C < VE) {
 #pragma unroll 1
-  for (int32_t e = C - 1; e >= c; --e) {
-    if constexpr (DT == GBDT_DTYPE_F32) {
-      v = {{__float_as_uint(row[e]), v.w[0], v.w[1], v.w[2]}};
-    } else {
-      const uint32_t x = __builtin_bit_cast(uint16_t, row[e]);
-      v = {{v.w[0] << 16 | x, v.w[1] << 16 | v.w[0] >> 16, v.w[2] << 16 | v.w[1] >> 16,
-            v.w[3] << 16 | v.w[2] >> 16}};
+    for (int32_t e = C - 1; e >= c; --e) {
+      if constexpr (DT == GBDT_DTYPE_F32) {
+        v = {{__float_as_uint(row[e]), v.w[0], v.w[1], v.w[2]}};
+      } else {
+        const uint32_t x = __builtin_bit_cast(uint16_t, row[e]);
+        v = {{v.w[0] << 16 | x, v.w[1] << 16 | v.w[0] >> 16, v.w[2] << 16 | v.w[1] >> 16,
+              v.w[3] << 16 | v.w[2] >> 16}};
+      }
     }
+    return v;
   }
+  v = load_vec<DT>(row + (C - VE));
+  int32_t down = c + VE - C;  // elements, 1 .. VE - 1
+  if constexpr (DT != GBDT_DTYPE_F32) {
+    if (down & 1)
+      v = {{v.w[0] >> 16 | v.w[1] << 16, v.w[1] >> 16 | v.w[2] << 16, v.w[2] >> 16 | v.w[3] << 16,
+            v.w[3] >> 16 | (inf & 0xffff0000u)}};
+    down >>= 1;
+  }
+  if (down & 1) v = {{v.w[1], v.w[2], v.w[3], inf}};
+  if (down & 2) v = {{v.w[2], v.w[3], inf, inf}};
   return v;
 }
 
@@ -144,12 +159,12 @@ __device__ __forceinline__ double scalar_const(double c) {
   return c;
 }
 
-// 2^y for y <= 1 in FP64: y = n + r with |r| <= 1/2 (n by adding 1.5 2^52,
-// whose last bit is 1), 2^r = 1 + r Q(r) with Q the degree-9 polynomial
-// through (2^r - 1) / r at the Chebyshev nodes of [-1/2, 1/2] (relative error
-// 5.7e-16, 1 at r = 0), n added to the exponent.  0 below 2^-1020; NaN stays.
-// 17 instructions, FP64 ones at the FP32 rate.
-__device__ __forceinline__ double exp2_64(double y) {
+// 2^y for -1020 <= y <= 1 in FP64: y = n + r with |r| <= 1/2 (n by adding
+// 1.5 2^52, whose last bit is 1), 2^r = 1 + r Q(r) with Q the degree-9
+// polynomial through (2^r - 1) / r at the Chebyshev nodes of [-1/2, 1/2]
+// (relative error 5.7e-16, 1 at r = 0), n added to the exponent.
+// 14 instructions, FP64 ones at the FP32 rate.
+__device__ __forceinline__ double exp2_64_near(double y) {
   const double t = y + 0x1.8p52;
   const double r = y - (t - 0x1.8p52);
   double p = __builtin_fma(r, scalar_const(0x1.e5e9f550503fcp-28), scalar_const(0x1.b6571deaf97c8p-24));
@@ -163,7 +178,11 @@ __device__ __forceinline__ double exp2_64(double y) {
   p = __builtin_fma(p, r, scalar_const(0x1.62e42fefa39f7p-1));
   p = __builtin_fma(p, r, 1.0);
   const int32_t n = __double2loint(t);
-  const double e = __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
+  return __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
+}
+// The same, 0 for y below -1020; NaN stays.
+__device__ __forceinline__ double exp2_64(double y) {
+  const double e = exp2_64_near(y);
   return y < -1020.0 ? 0.0 : e;
 }
 
@@ -259,6 +278,22 @@ __device__ __forceinline__ RawBlock<DT> load_block(const typename Score<DT>::Ele
     for (int j = 0; j < kVecs; ++j) r.v[j] = load_tail<DT>(row, c0 + j * NT * VE, C);
   }
   return r;
+}
+
+// All blocks of a row, the next one on its way while one is worked on.
+template <int DT, int NT, typename Work>
+__device__ __forceinline__ void each_block(const typename Score<DT>::Elem* __restrict__ row, int32_t C, Work work) {
+  RawBlock<DT> raw = load_block<DT, NT>(row, 0, C);
+  for (int32_t base = 0;;) {
+    RawBlock<DT> next;
+    const bool more = base + NT * kBlk<DT> < C;
+    if (more) next = load_block<DT, NT>(row, base + NT * kBlk<DT>, C);
+    __builtin_amdgcn_sched_barrier(0);
+    work(raw, base);
+    if (!more) break;
+    base += NT * kBlk<DT>;
+    raw = next;
+  }
 }
 
 // The stores are marked as not read again soon: they leave the caches to the

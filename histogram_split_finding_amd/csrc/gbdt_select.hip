@@ -5,15 +5,19 @@
 // Both come down to places in a row's order (score descending, class
 // ascending).  The kept classes of a draw are a prefix of the order whichever
 // filters are on, and the draw itself is the place where a running sum passes
-// a target.  Two ways to a place:
-//  - collect_top (k small): the k-th largest of the threads' own maxima is a
-//    lower bound of the k-th largest score; the few scores that reach it are
-//    listed in LDS and ranked by counting.
-//  - locate (any place, by count or by mass): the scores between two bounds
+// a target.
+//  - One pass over the row lists in LDS the few classes that reach a threshold
+//    and adds up what lies below it (a record's rest, a draw's other masses).
+//    The threshold comes from the row's first block: the r-th largest of its
+//    threads' (or of four times as many groups') maxima, r so that the whole
+//    row should list about twice what is needed.  The list is ranked by
+//    counting.  Records, draws with top-k, and draws whose cut and target fall
+//    on listed classes are complete then, from one read of the row.
+//  - A row that lists too few or too many, and other draws: counts or masses
 //    are summed into value bins in LDS (64-bit integers, so the order of the
-//    atomics changes nothing), the bin with the target is found, its members
-//    are listed and ranked, or, when they are too many, take the place of the
-//    bounds; equal scores are counted off in class order.
+//    atomics changes nothing), the bin with the target is found, and its members
+//    are listed and ranked; members that are too many take the place of the row,
+//    and equal scores are counted off in class order.
 //
 // Masses are integers: rint(e_c 2^s), s = min(50, 62 - ceil(log2 C)), so C of
 // them fit 62 bits and a sum is exact.
@@ -34,13 +38,12 @@ namespace gbdt {
 
 namespace {
 
-constexpr int kBins = 2048;   // value bins of a locate level
-constexpr int kList = 1024;   // members that are ranked in LDS
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
 // Order-preserving key of a score: larger for a larger score, the same for -0
 // and +0, that of -inf for NaN.
 __device__ __forceinline__ float canon(float x) { return x == x ? x + 0.0f : -kInf; }
+__device__ __forceinline__ float canon_max(float x) { return __builtin_fmaxf(x, -kInf); }  // (-0 stays)
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
   return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
@@ -57,15 +60,20 @@ __device__ __forceinline__ int32_t class_of(uint64_t p) { return int32_t(~uint32
 
 // A row's e_c = 2^((x - m) c) as FP64 and as an integer of s fraction bits.
 struct Mass {
-  double m, c, magic;
-  bool inf;  // m = +inf: e is 1 for +inf, 0 otherwise
+  double m, c, magic, low;  // low: 2^low rounds to mass 0
+  bool inf;                 // m = +inf: e is 1 for +inf, 0 otherwise
   __device__ __forceinline__ double e(float x) const {
     if (inf) return x == kInf ? 1.0 : 0.0;
     return exp2_64(((double)x - m) * c);
   }
   // rint(e 2^s): added to 2^(52 - s), e's last bit is the sum's last bit
-  __device__ __forceinline__ uint64_t q(float x) const {
-    return uint64_t(__double_as_longlong(e(x) + magic)) - uint64_t(__double_as_longlong(magic));
+  __device__ __forceinline__ uint64_t raw(double e) const { return uint64_t(__double_as_longlong(e + magic)); }
+  __device__ __forceinline__ uint64_t raw_zero() const { return uint64_t(__double_as_longlong(magic)); }
+  __device__ __forceinline__ uint64_t q(float x) const { return raw(e(x)) - raw_zero(); }
+  // the same plus raw_zero() for any score (NaN: 0) of a row whose m is finite;
+  // d = x - m
+  __device__ __forceinline__ uint64_t raw_at(double d) const {
+    return raw(exp2_64_near(__builtin_fmax(d * c, low)));
   }
 };
 __device__ __forceinline__ int mass_bits(int32_t C) {
@@ -78,21 +86,24 @@ __device__ __forceinline__ Mass make_mass(float m, double c, int bits) {
   r.m = (double)m;
   r.c = c;
   r.magic = __builtin_ldexp(1.0, 52 - bits);
+  r.low = -(double)(bits + 2);
   return r;
 }
 
+template <int NT>
 struct SelLds {
+  static constexpr int kBins = NT == 64 ? 256 : NT == 256 ? 1024 : 2048;  // value bins of a locate level
+  static constexpr int kList = NT == 64 ? 512 : 1024;  // members that are ranked in LDS
   uint64_t hist[kBins];
-  uint64_t list[kList];
+  alignas(16) uint64_t list[kList];
   uint64_t sorted[kList];
-  double shd[16];
   uint64_t shu[16];
+  double shd[16];
   uint64_t found[4];
-  float shf[16];
-  uint32_t cnt[2][16];
+  float shf[2][16];
+  uint64_t cnt[2][16];
   int32_t sh32[32];
   uint32_t n_list, kmin, kmax;
-  int32_t ibest;
 };
 
 // Exclusive scan of one uint64 per thread; *total = the sum.
@@ -117,35 +128,208 @@ __device__ inline uint64_t block_scan_u64(uint64_t v, uint64_t* total, uint64_t*
   return before + x - v;
 }
 
-// The k-th largest of the threads' keys (0 when fewer than k are above 0).
+// A key that at least k of the groups' maxima gm (all scores above -inf, if
+// those are fewer) reach, and not many more than k; m, lowest: the largest and
+// the smallest of the maxima.
 template <int NT>
-__device__ inline uint32_t kth_key(uint32_t key, int32_t k, uint32_t (*cnt)[16]) {
-  uint32_t thr = 0u;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t trial = thr | (1u << bit);
-    const uint64_t b = __ballot(key >= trial);
-    uint32_t* sh = cnt[bit & 1];  // (two buffers: one barrier a step)
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = uint32_t(__popcll(b));
-    __syncthreads();
-    uint32_t n = 0;
+__device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float lowest, int32_t k, SelLds<NT>& L) {
+  // (with 1,024 threads their own maxima are enough groups)
+  constexpr int G = NT >= 1024 ? 1 : kVecs;
+  uint32_t key[G];
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) n += sh[w];
-    if (n >= (uint32_t)k) thr = trial;
+  for (int j = 0; j < G; ++j) key[j] = key_of(gm[j]);
+  if (G == 1) key[0] = key_of(max_of(gm));
+  if (k > G * NT) return kKeyNegInf + 1u;
+  uint32_t lo = key_of(lowest), hi = key_of(m) + 1u;  // reached by >= k, by none
+  lo = lo > kKeyNegInf ? lo : kKeyNegInf + 1u;
+  for (int step = 0; hi - lo > 1u; ++step) {
+    // three points of the interval at a time: half the barriers
+    const uint32_t q = (hi - lo) / 4u, p2 = lo + (hi - lo) / 2u;
+    const uint32_t p1 = q > 0u ? lo + q : p2, p3 = q > 0u ? p2 + q : p2;
+    uint64_t n = 0;  // three counts of 21 bits
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      n += uint64_t(__popcll(__ballot(key[j] >= p1)));
+      n += uint64_t(__popcll(__ballot(key[j] >= p2))) << 21;
+      n += uint64_t(__popcll(__ballot(key[j] >= p3))) << 42;
+    }
+    if (NT > 64) {
+      uint64_t* sh = L.cnt[step & 1];  // (two buffers: one barrier a step)
+      if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = n;
+      __syncthreads();
+      n = across_waves<NT / 64>(sh, [](uint64_t a, uint64_t b) { return a + b; });
+    }
+    const int32_t n1 = int32_t(n & 0x1fffffu), n2 = int32_t(n >> 21 & 0x1fffffu), n3 = int32_t(n >> 42);
+    int32_t at_lo;
+    if (n3 >= k) {
+      lo = p3;
+      at_lo = n3;
+    } else if (n2 >= k) {
+      lo = p2;
+      hi = p3;
+      at_lo = n2;
+    } else if (n1 >= k) {
+      lo = p1;
+      hi = p2;
+      at_lo = n1;
+    } else {
+      hi = p1;
+      continue;
+    }
+    if (at_lo <= k + k / 4 + 8) break;
   }
-  __syncthreads();
-  return thr;
+  if (NT > 64) __syncthreads();
+  return lo;
 }
 
-// list[0..n) into sorted[], first of the order first (all entries differ).
+// list[0..n) into sorted[], first of the order first (all entries differ): each
+// entry's place is the number of entries before it.  Eight entries are read at
+// a time, for all of the thread's own ones.
 template <int NT>
-__device__ inline void rank_list(SelLds& L, int32_t n) {
-  for (int32_t i = threadIdx.x; i < n; i += NT) {
-    const uint64_t p = L.list[i];
-    int32_t r = 0;
-    for (int32_t j = 0; j < n; ++j) r += L.list[j] > p ? 1 : 0;
-    L.sorted[r] = p;
+__device__ inline void rank_list(SelLds<NT>& L, int32_t n) {
+  constexpr int PT = SelLds<NT>::kList / NT >= 8 ? 4 : 2;
+  const int tid = threadIdx.x;
+  const int32_t n8 = (n + 7) & ~7;
+  if (tid < n8 - n) L.list[n + tid] = 0ull;
+  __syncthreads();
+  for (int32_t i0 = 0; i0 < n; i0 += PT * NT) {
+    uint64_t p[PT];
+    int32_t r[PT];
+#pragma unroll
+    for (int u = 0; u < PT; ++u) {
+      const int32_t i = i0 + tid + u * NT;
+      p[u] = i < n ? L.list[i] : ~uint64_t(0);
+      r[u] = 0;
+    }
+    if (i0 + (tid & ~63) < n) {  // (whole waves)
+      for (int32_t j = 0; j < n8; j += 8) {
+        uint64_t e[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) e[v] = L.list[j + v];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+#pragma unroll
+          for (int u = 0; u < PT; ++u)
+            if (u == 0 || u * NT < n - i0) r[u] += e[v] > p[u] ? 1 : 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < PT; ++u)
+      if (i0 + tid + u * NT < n) L.sorted[r[u]] = p[u];
   }
   __syncthreads();
+}
+
+// The value of the first lane, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+__device__ __forceinline__ double uniform(double x) {
+  return __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(x)),
+                          __builtin_amdgcn_readfirstlane(__double2loint(x)));
+}
+
+// What the pass over a row gives: the maximum, how many classes reached the
+// threshold (the first kList of them are in L.list), and the sum of the others'
+// exp2((x - ref) c), in FP64; with kSum32 the exponentials are the hardware's.
+enum { kNoSum, kSum32, kSum64 };
+struct Scan {
+  float m, ref;
+  int32_t n;
+  double sum;
+};
+
+template <int DT, int NT, int SUM>
+__device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, int32_t k,
+                                         double c, SelLds<NT>& L) {
+  constexpr int VE = Score<DT>::kVec, NL = SelLds<NT>::kList, STEP = NT * kBlk<DT>;
+  const int tid = threadIdx.x;
+  RawBlock<DT> raw = load_block<DT, NT>(xr, 0, C);
+  float gm[kVecs], hi = -kInf, lo = kInf;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    float f[VE];
+    unpack<DT>(raw.v[j], f);
+    gm[j] = __builtin_fmaxf(max_of(f), -kInf) + 0.0f;
+    hi = __builtin_fmaxf(hi, gm[j]);
+    lo = __builtin_fminf(lo, gm[j]);
+  }
+  hi = wave_max(hi);
+  lo = wave_min(lo);
+  if ((tid & 63) == 0) {
+    L.shf[0][tid >> 6] = hi;
+    L.shf[1][tid >> 6] = lo;
+  }
+  if (tid == 0) L.n_list = 0u;
+  __syncthreads();
+  hi = across_waves<NT / 64>(L.shf[0], [](float a, float b) { return __builtin_fmaxf(a, b); });
+  lo = across_waves<NT / 64>(L.shf[1], [](float a, float b) { return __builtin_fminf(a, b); });
+  // of a row of one block at least k; of a longer one its share of 2 k + 64
+  // (k = 64 of 8 blocks: 24 of the first, so 192 +- 39 of the row)
+  const int32_t r = C <= STEP ? k : (int32_t)((int64_t)(2 * k + 64) * STEP / C) + 1;
+  const float thr = uniform(of_key(group_threshold<NT>(gm, hi, lo, r, L)));
+  Scan s;
+  s.ref = hi > -kInf ? uniform(hi) : 0.0f;  // (a masked block: the rest is listed or binned)
+  const float cf = uniform(exponent_scale(c));
+  const double ref = (double)s.ref, cd = uniform(c);
+  float m = -kInf;
+  double sum = 0.0;
+  for (int32_t base = 0;;) {
+    // the next block is on its way while this one is worked on
+    RawBlock<DT> next;
+    const bool more = base + STEP < C;
+    if (more) next = load_block<DT, NT>(xr, base + STEP, C);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float f[VE];
+      unpack<DT>(raw.v[j], f);
+      const float vm = max_of(f);
+      m = __builtin_fmaxf(m, vm);
+      if (vm >= thr) {
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+          if (f[q] >= thr) {
+            const uint32_t at = atomicAdd(&L.n_list, 1u);
+            if (at < (uint32_t)NL) L.list[at] = place_of(f[q] + 0.0f, base + (j * NT + tid) * VE + q);
+            f[q] = -kInf;
+          }
+        }
+      }
+      if (SUM == kSum32) {
+#pragma unroll
+        for (int q = 0; q < VE; ++q) f[q] = exp2_32((canon_max(f[q]) - s.ref) * cf);
+        sum += (double)sum_of(f);
+      }
+      if (SUM == kSum64) {
+        // four at a time: enough to cover an addition's latency, in few registers
+#pragma unroll
+        for (int h = 0; h < VE; h += 4) {
+#pragma unroll
+          for (int q = h; q < h + 4; ++q)
+            sum += exp2_64_near(__builtin_fmax(((double)f[q] - ref) * cd, -1000.0));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!more) break;
+    base += STEP;
+    raw = next;
+  }
+  m = wave_max(m);
+  if ((tid & 63) == 0) L.shf[0][tid >> 6] = m;
+  if (SUM != kNoSum) {
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) L.shd[tid >> 6] = sum;
+  }
+  __syncthreads();
+  s.m = uniform(across_waves<NT / 64>(L.shf[0], [](float a, float b) { return __builtin_fmaxf(a, b); }) + 0.0f);
+  s.sum = SUM == kNoSum ? 0.0 : across_waves<NT / 64>(L.shd, [](double a, double b) { return a + b; });
+  s.n = (int32_t)L.n_list;
+  __syncthreads();
+  return s;
 }
 
 // What a place search finds: the place, the sum up to and with it, the sum of
@@ -160,45 +344,69 @@ struct Found {
 // `count` classes.
 enum { kTargetCount, kTargetFrac, kTargetOver };
 
+// Value bins between vlo and vhi, bin 0 first in the order.
+struct Bins {
+  double hi, scale;
+  float vlo, vhi;
+  bool flat, open;  // one value; +inf in a bin of its own
+  template <int NB>
+  __device__ __forceinline__ void set(float lo, float h) {
+    vlo = lo;
+    vhi = h;
+    flat = lo == h;
+    open = h == kInf && !flat;
+    hi = (double)h;
+    scale = (double)NB / ((double)h - (double)lo);
+  }
+  template <int NB>
+  __device__ __forceinline__ int32_t at(double below) const {  // below: hi - v
+    const int32_t b = (int32_t)(below * scale);
+    return b < NB - 1 ? b : NB - 1;
+  }
+  template <int NB>
+  __device__ __forceinline__ int32_t of(float v) const {
+    if (flat) return 0;
+    if (open) return v == kInf ? 0 : 1;
+    return at<NB>(hi - (double)v);
+  }
+};
+
+// The bins of a row's masses: scores below them have mass 0.
+template <int NB>
+__device__ __forceinline__ void mass_bins(const Mass& mass, float m, Bins* b) {
+  const float floor_v = (float)(mass.m + mass.low / mass.c);
+  b->set<NB>(mass.inf ? kInf : __builtin_fminf(floor_v > -kInf ? floor_v : -3.4e38f, m), m);
+}
+
+// have: L.hist holds the masses in the bins of mass_bins() (cleared when it no
+// longer does), and `total` is the kept ones' sum; otherwise the first level
+// finds both.
 template <int DT, int NT, int TARGET>
 __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, uint64_t keep,
-                        uint64_t count, double frac, float m, float lowest, int bits, const Mass& mass,
-                        SelLds& L) {
-  constexpr int VE = Score<DT>::kVec;
+                        uint64_t count, double frac, float m, const Mass& mass, SelLds<NT>& L, bool& have,
+                        uint64_t total) {
+  constexpr int VE = Score<DT>::kVec, NB = SelLds<NT>::kBins, NL = SelLds<NT>::kList;
   constexpr bool kCount = TARGET == kTargetCount;
   const int tid = threadIdx.x;
-  float vhi = m, vlo = __builtin_fmaxf(lowest, score_of(keep));
-  if (!kCount) {
-    if (mass.inf) {
-      vlo = kInf;
-    } else {
-      // scores whose integer mass is 0 (e < 2^-(s+1)) need no bins
-      const float floor_v = (float)((double)m - (double)(bits + 2) / mass.c);
-      vlo = __builtin_fmaxf(vlo, __builtin_fminf(floor_v, m));
-    }
-  }
-  uint64_t above = 0, total = 0, target = count;
+  Bins bins;
+  if (kCount)
+    bins.set<NB>(score_of(keep), m);
+  else
+    mass_bins<NB>(mass, m, &bins);
+  uint64_t above = 0, target = count;
   bool first = true;
   Found out;
   for (;;) {
-    const bool flat = vlo == vhi;
-    const bool open = vhi == kInf && !flat;  // +inf in a bin of its own
-    const double scale = (double)kBins / ((double)vhi - (double)vlo);
-    const double hi = (double)vhi;
-    auto bin_of = [&](float v) -> int32_t {
-      if (flat) return 0;
-      if (open) return v == kInf ? 0 : 1;
-      const int32_t b = (int32_t)((hi - (double)v) * scale);
-      return b < kBins - 1 ? b : kBins - 1;
-    };
-    for (int b = tid; b < kBins; b += NT) L.hist[b] = 0ull;
+    if (!have)
+      for (int b = tid; b < NB; b += NT) L.hist[b] = 0ull;
     if (tid == 0) {
       L.n_list = 0u;
       L.kmin = 0xffffffffu;
       L.kmax = 0u;
     }
     __syncthreads();
-    if (flat) {
+    if (bins.flat) {
+      const float vhi = bins.vhi;
       uint64_t n = 0;
       for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
         float f[VE];
@@ -215,9 +423,9 @@ __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t
         total = n_eq * w;
         if (TARGET == kTargetFrac) target = (uint64_t)__builtin_ceil(frac * (double)total);
         if (TARGET == kTargetOver) target = (uint64_t)(frac * (double)total) + 1ull;
+        if (target < 1) target = 1;
+        if (target > total) target = total;
       }
-      if (target < 1) target = 1;
-      if (target > total) target = total;
       // the r-th of the equal scores, in class order
       uint64_t r = target > above ? (target - above + w - 1) / (w > 0 ? w : 1) : 1;
       if (r > n_eq) r = n_eq;
@@ -251,27 +459,29 @@ __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t
       __syncthreads();
       return out;
     }
-    for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
-      float f[VE];
-      load_chunk<DT>(xr, c0, C, f);
+    if (!have) {
+      for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
+        float f[VE];
+        load_chunk<DT>(xr, c0, C, f);
 #pragma unroll
-      for (int q = 0; q < VE; ++q) {
-        const float v = canon(f[q]);
-        if (c0 + q < C && v >= vlo && v <= vhi && v > -kInf && place_of(v, c0 + q) >= keep)
-          atomicAdd(reinterpret_cast<unsigned long long*>(&L.hist[bin_of(v)]),
-                    kCount ? 1ull : (unsigned long long)mass.q(v));
+        for (int q = 0; q < VE; ++q) {
+          const float v = canon(f[q]);
+          if (c0 + q < C && v >= bins.vlo && v <= bins.vhi && v > -kInf && place_of(v, c0 + q) >= keep)
+            atomicAdd(reinterpret_cast<unsigned long long*>(&L.hist[bins.of<NB>(v)]),
+                      kCount ? 1ull : (unsigned long long)mass.q(v));
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
     // the bin in which the running sum reaches the target
-    constexpr int PB = kBins / NT;
+    constexpr int PB = NB / NT;
     uint64_t mine = 0;
 #pragma unroll
     for (int b = 0; b < PB; ++b) mine += L.hist[tid * PB + b];
     uint64_t sum;
     uint64_t run = block_scan_u64<NT>(mine, &sum, L.shu);
     if (first) {
-      total = sum;
+      if (!have) total = sum;
       if (TARGET == kTargetFrac) target = (uint64_t)__builtin_ceil(frac * (double)total);
       if (TARGET == kTargetOver) target = (uint64_t)(frac * (double)total) + 1ull;
       if (target < 1) target = 1;
@@ -291,24 +501,40 @@ __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t
     __syncthreads();
     const int32_t bin = (int32_t)L.found[0];
     above = L.found[1];
-    for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
-      float f[VE];
-      load_chunk<DT>(xr, c0, C, f);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) {
-        const float v = canon(f[q]);
-        if (c0 + q < C && v >= vlo && v <= vhi && v > -kInf && place_of(v, c0 + q) >= keep &&
-            bin_of(v) == bin) {
-          const uint32_t at = atomicAdd(&L.n_list, 1u);
-          if (at < (uint32_t)kList) L.list[at] = place_of(v, c0 + q);
-          atomicMin(&L.kmin, key_of(v));
-          atomicMax(&L.kmax, key_of(v));
-        }
-      }
+    // an interval that holds the bin's scores (half a bin more on both sides),
+    // so that the exact test is made for few
+    float from = bins.vlo, to = bins.vhi;
+    if (!bins.open) {
+      to = __builtin_fminf(to, (float)(bins.hi - ((double)bin - 0.5) / bins.scale));
+      if (bin < NB - 1) from = __builtin_fmaxf(from, (float)(bins.hi - ((double)bin + 1.5) / bins.scale));
     }
+    from = uniform(__builtin_fmaxf(from, score_of(keep)));
+    to = uniform(to);
+    each_block<DT, NT>(xr, C, [&](const RawBlock<DT>& raw, int32_t base) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        float f[VE];
+        unpack<DT>(raw.v[j], f);
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+          // (NaN fails; past the row's end is -inf, as a masked class)
+          if (f[q] >= from && f[q] <= to) {
+            const float v = f[q] + 0.0f;
+            const uint64_t p = place_of(v, base + (j * NT + tid) * VE + q);
+            if (bins.of<NB>(v) == bin && p >= keep) {
+              const uint32_t at = atomicAdd(&L.n_list, 1u);
+              if (at < (uint32_t)NL) L.list[at] = p;
+              atomicMin(&L.kmin, key_of(v));
+              atomicMax(&L.kmax, key_of(v));
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    });
     __syncthreads();
     const int32_t n = (int32_t)L.n_list;
-    if (n <= kList) {
+    if (n <= NL) {
       rank_list<NT>(L, n);
       // running sums in the order, by one wave
       if (tid < 64) {
@@ -338,67 +564,35 @@ __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t
     }
     const uint32_t kmin = L.kmin, kmax = L.kmax;
     __syncthreads();
-    vlo = of_key(kmin);
-    vhi = of_key(kmax);
+    bins.set<NB>(of_key(kmin), of_key(kmax));
+    have = false;
   }
 }
 
-// The first min(k, scores above -inf) places of the order into L.sorted, in
-// order; returns how many.  tmax: this thread's largest score.
+// The list of all places >= keep into L.sorted, in order; returns how many
+// there are (ranked only when they fit).
 template <int DT, int NT>
-__device__ int32_t collect_top(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, int32_t k,
-                               float tmax, float m, float lowest, const Mass& mass, SelLds& L) {
-  constexpr int VE = Score<DT>::kVec;
-  uint32_t thr = kth_key<NT>(key_of(tmax), k, L.cnt);
-  uint64_t keep = uint64_t(thr > kKeyNegInf ? thr : kKeyNegInf + 1u) << 32;
-  for (;;) {
-    if (threadIdx.x == 0) L.n_list = 0u;
-    __syncthreads();
-    for (int32_t c0 = threadIdx.x * VE; c0 < C; c0 += NT * VE) {
-      float f[VE];
-      load_chunk<DT>(xr, c0, C, f);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) {
-        const uint64_t p = place_of(canon(f[q]), c0 + q);
-        if (c0 + q < C && p >= keep) {
-          const uint32_t at = atomicAdd(&L.n_list, 1u);
-          if (at < (uint32_t)kList) L.list[at] = p;
-        }
-      }
-    }
-    __syncthreads();
-    const int32_t n = (int32_t)L.n_list;
-    if (n <= kList) {
-      rank_list<NT>(L, n);
-      return n < k ? n : k;
-    }
-    // too many reach the bound: the exact k-th place (then exactly k are listed)
-    __syncthreads();
-    keep = locate<DT, NT, kTargetCount>(xr, C, uint64_t(kKeyNegInf + 1u) << 32, (uint64_t)k, 0.0, m, lowest, 0,
-                                        mass, L)
-               .place;
-  }
-}
-
-// Largest score of the row, this thread's own, and the lowest above -inf.
-template <int DT, int NT>
-__device__ void row_range(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, float* m, float* tmax,
-                          float* lowest, SelLds& L) {
-  constexpr int VE = Score<DT>::kVec;
-  float hi = -kInf, lo = kInf;
+__device__ int32_t list_from(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, uint64_t keep,
+                             SelLds<NT>& L) {
+  constexpr int VE = Score<DT>::kVec, NL = SelLds<NT>::kList;
+  if (threadIdx.x == 0) L.n_list = 0u;
+  __syncthreads();
   for (int32_t c0 = threadIdx.x * VE; c0 < C; c0 += NT * VE) {
     float f[VE];
     load_chunk<DT>(xr, c0, C, f);
 #pragma unroll
     for (int q = 0; q < VE; ++q) {
-      const float v = canon(f[q]);
-      hi = __builtin_fmaxf(hi, v);
-      lo = v > -kInf ? __builtin_fminf(lo, v) : lo;
+      const uint64_t p = place_of(canon(f[q]), c0 + q);
+      if (c0 + q < C && p >= keep) {
+        const uint32_t at = atomicAdd(&L.n_list, 1u);
+        if (at < (uint32_t)NL) L.list[at] = p;
+      }
     }
   }
-  *tmax = hi;
-  *m = block_max<NT>(hi, L.shf);
-  *lowest = block_min<NT>(lo, L.shf);
+  __syncthreads();
+  const int32_t n = (int32_t)L.n_list;
+  if (n <= NL) rank_list<NT>(L, n);
+  return n;
 }
 
 // -------------------------------------------------------------- top scores --
@@ -411,105 +605,164 @@ struct TopArgs {
   float* values;
   int32_t* classes;
   float* rest;
+  int64_t row0;  // of this launch
 };
 
+// One workgroup per row.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT) k_top_block(const TopArgs a) {
+__global__ void __launch_bounds__(NT, NT == 64 ? 4 : 6) k_top_block(const TopArgs a) {
   using Elem = typename Score<DT>::Elem;
-  constexpr int VE = Score<DT>::kVec;
-  __shared__ SelLds L;
+  constexpr int VE = Score<DT>::kVec, NL = SelLds<NT>::kList;
+  __shared__ SelLds<NT> L;
   const int tid = threadIdx.x;
-  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-    const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-    float m, tmax, lowest;
-    row_range<DT, NT>(xr, a.C, &m, &tmax, &lowest, L);
-    int32_t got = 0;
-    if (m > -kInf) {
-      const Mass mass = make_mass(m, a.c, mass_bits(a.C));
-      got = collect_top<DT, NT>(xr, a.C, a.k, tmax, m, lowest, mass, L);
+  const int32_t C = a.C, k = a.k;
+  const int64_t i = a.row0 + blockIdx.x;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  const Scan sc = scan_row<DT, NT, kSum32>(xr, C, k, a.c, L);
+  const float m = sc.m;
+  int32_t got = 0;
+  float rest = 0.0f;
+  if (m > -kInf) {
+    const bool inf = m == kInf;
+    const float cf = exponent_scale(a.c);
+    auto weight = [&](float v) { return inf ? (v == kInf ? 1.0f : 0.0f) : exp2_32((v - m) * cf); };
+    int32_t n = sc.n;
+    double out = 0.0;  // (one thread's part)
+    if (n <= NL && (n >= k || C <= NT * kBlk<DT>)) {
+      rank_list<NT>(L, n);
+      if (tid == 0 && !inf && sc.sum > 0.0) out = sc.sum * exp2_64(((double)sc.ref - (double)m) * a.c);
+    } else {
+      // from the exact k-th place on, exactly k (or all above -inf) are listed
+      uint64_t last = uint64_t(kKeyNegInf + 1u) << 32;
+      bool have = false;
+      last = locate<DT, NT, kTargetCount>(xr, C, last, (uint64_t)k, 0.0, m, Mass(), L, have, 0).place;
+      n = list_from<DT, NT>(xr, C, last, L);
       if (a.rest != nullptr) {
-        const uint64_t last = L.sorted[got - 1];
-        const float cf = (float)a.c;
-        double in = 0.0, out = 0.0;
-        for (int32_t j = tid; j < got; j += NT) in += mass.e(score_of(L.sorted[j]));
-        for (int32_t c0 = tid * VE; c0 < a.C; c0 += NT * VE) {
+        for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
           float f[VE];
-          load_chunk<DT>(xr, c0, a.C, f);
+          load_chunk<DT>(xr, c0, C, f);
 #pragma unroll
           for (int q = 0; q < VE; ++q) {
             const float v = canon(f[q]);
-            const float w = mass.inf ? (v == kInf ? 1.0f : 0.0f) : exp2_32((v - m) * cf);
-            out += c0 + q < a.C && place_of(v, c0 + q) < last ? (double)w : 0.0;
+            out += c0 + q < C && place_of(v, c0 + q) < last ? (double)weight(v) : 0.0;
           }
         }
-        in = block_sum<NT>(in, L.shd);
-        out = block_sum<NT>(out, L.shd);
-        if (tid == 0) a.rest[i] = (float)(out / (in + out));
       }
-    } else if (a.rest != nullptr && tid == 0) {
-      a.rest[i] = 0.0f;
     }
-    for (int32_t j = tid; j < a.k; j += NT) {
-      a.values[i * a.k + j] = j < got ? score_of(L.sorted[j]) : -kInf;
-      a.classes[i * a.k + j] = j < got ? class_of(L.sorted[j]) : -1;
+    got = n < k ? n : k;
+    if (a.rest != nullptr) {
+      double in = 0.0;
+      for (int32_t j = tid; j < n; j += NT) {
+        const double w = (double)weight(score_of(L.sorted[j]));
+        if (j < got) in += w; else out += w;
+      }
+      in = block_sum<NT>(in, L.shd);
+      out = block_sum<NT>(out, L.shd);
+      rest = (float)(out / (in + out));
     }
-    __syncthreads();
+  }
+  if (a.rest != nullptr && tid == 0) a.rest[i] = rest;
+  for (int32_t j = tid; j < k; j += NT) {
+    a.values[i * k + j] = j < got ? score_of(L.sorted[j]) : -kInf;
+    a.classes[i * k + j] = j < got ? class_of(L.sorted[j]) : -1;
   }
 }
 
 // A row of at most CMAX classes in one thread: its places sorted in registers
-// (bitonic network, largest first; 0 past the row's end).
-template <int DT, int CMAX>
-__device__ __forceinline__ void sort_row(const typename Score<DT>::Elem* __restrict__ xr, int32_t C,
-                                         uint64_t (&p)[CMAX]) {
+// (Batcher's odd-even merge network, largest first).  A place is a positive
+// FP64 number here, key and class in its last 56 bits: its order is the
+// place's, and a comparator is two instructions, max and min.
+template <int CMAX>
+__device__ __forceinline__ double short_place(float x, int32_t c) {
+  return __longlong_as_double(int64_t(uint64_t(1) << 62 | uint64_t(key_of(x)) << 24 | uint64_t(CMAX - 1 - c)));
+}
+__device__ __forceinline__ float short_score(double p) {
+  return of_key(uint32_t(uint64_t(__double_as_longlong(p)) >> 24));
+}
+template <int CMAX>
+__device__ __forceinline__ int32_t short_class(double p) {
+  return CMAX - 1 - (__double2loint(p) & (CMAX - 1));
+}
+template <int CMAX>
+__device__ __forceinline__ void sort_row(const float* __restrict__ x, int32_t C, double (&p)[CMAX]) {
 #pragma unroll
-  for (int c = 0; c < CMAX; ++c) p[c] = c < C ? place_of(canon(Score<DT>::to_f32(xr[c])), c) : 0ull;
+  for (int c = 0; c < CMAX; ++c) p[c] = short_place<CMAX>(c < C ? canon(x[c]) : -kInf, c);
 #pragma unroll
-  for (int len = 2; len <= CMAX; len <<= 1) {
+  for (int s = 1; s < CMAX; s <<= 1) {
 #pragma unroll
-    for (int d = len >> 1; d > 0; d >>= 1) {
+    for (int d = s; d >= 1; d >>= 1) {
 #pragma unroll
-      for (int a = 0; a < CMAX; ++a) {
-        const int b = a ^ d;
-        if (b > a) {
-          const bool down = (a & len) == 0;
-          const bool swap = down ? p[a] < p[b] : p[a] > p[b];
-          const uint64_t u = swap ? p[b] : p[a], v = swap ? p[a] : p[b];
-          p[a] = u;
-          p[b] = v;
+      for (int i = 0; i + d < CMAX; ++i) {
+        // (i from d mod s on, in runs of d, both ends in one half of 2 s)
+        if (i >= d % s && (i - d % s) / d % 2 == 0 && i / (2 * s) == (i + d) / (2 * s)) {
+          const double u = __builtin_fmax(p[i], p[i + d]), v = __builtin_fmin(p[i], p[i + d]);
+          p[i] = u;
+          p[i + d] = v;
         }
       }
     }
   }
 }
 
-template <int DT, int CMAX>
-__global__ void __launch_bounds__(256) k_top_rows(const TopArgs a) {
-  using Elem = typename Score<DT>::Elem;
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= a.n) return;
-  uint64_t p[CMAX];
-  sort_row<DT, CMAX>(static_cast<const Elem*>(a.x) + i * a.ld, a.C, p);
-  const float m = score_of(p[0]);
-  double in = 0.0, out = 0.0;
-  if (a.rest != nullptr && m > -kInf) {
-    const Mass mass = make_mass(m, a.c, 50);
+// The rows of a workgroup into LDS, in rows of C | 1 words.
+template <int DT, int R, int CMAX>
+__device__ __forceinline__ void stage_scores(const void* x, int64_t i0, int32_t rows, int32_t C, int64_t ld,
+                                             const RowDiv& by_c, float* lds) {
+  const auto* __restrict__ xg = static_cast<const typename Score<DT>::Elem*>(x) + i0 * ld;
+  Staged<R, CMAX, float> xs;
+  xs.load(
+      rows, C, ld == C, by_c, [&](int32_t e) { return Score<DT>::to_f32(xg[(uint32_t)e]); },
+      [&](int32_t row, int32_t c) { return Score<DT>::to_f32(xg[row * ld + c]); });
+  xs.put(rows, C, by_c, lds);
+}
+
+template <int DT, int R, int CMAX>
+__global__ void __launch_bounds__(R) k_top_rows(const TopArgs a) {
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x;
+  const int64_t i0 = int64_t(blockIdx.x) * R, i = i0 + tid;
+  const int32_t rows = (int32_t)(a.n - i0 < R ? a.n - i0 : R);
+  const int32_t C = a.C, k = a.k, P = C | 1, PK = k | 1;
+  const RowDiv by_c(C), by_k(k);
+  float* __restrict__ values = lds + R * P;
+  int32_t* __restrict__ classes = reinterpret_cast<int32_t*>(values + R * PK);
+  stage_scores<DT, R, CMAX>(a.x, i0, rows, C, a.ld, by_c, lds);
+  __syncthreads();
+  if (tid < rows) {
+    double p[CMAX];
+    sort_row<CMAX>(lds + tid * P, C, p);
+    const float m = short_score(p[0]);
+    if (a.rest != nullptr) {
+      const bool inf = m == kInf;
+      const float cf = exponent_scale(a.c);
+      double in = 0.0, out = 0.0;
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c) {
+        if (c < C) {
+          const float v = short_score(p[c]);
+          const double e = (double)(inf ? (v == kInf ? 1.0f : 0.0f) : exp2_32((v - m) * cf));
+          if (c < k) in += e; else out += e;
+        }
+      }
+      a.rest[i] = m > -kInf ? (float)(out * rcp_64(in + out)) : 0.0f;
+    }
 #pragma unroll
     for (int c = 0; c < CMAX; ++c) {
-      const float v = score_of(p[c]);
-      const double e = c < a.C && v > -kInf ? mass.e(v) : 0.0;
-      if (c < a.k) in += e; else out += e;
+      if (c < k) {
+        const float v = short_score(p[c]);
+        values[tid * PK + c] = v;
+        classes[tid * PK + c] = v > -kInf ? short_class<CMAX>(p[c]) : -1;
+      }
     }
   }
-  if (a.rest != nullptr) a.rest[i] = in > 0.0 ? (float)(out / (in + out)) : 0.0f;
-#pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    const float v = score_of(p[c]);
-    if (c < a.k) {
-      a.values[i * a.k + c] = v > -kInf ? v : -kInf;
-      a.classes[i * a.k + c] = v > -kInf ? class_of(p[c]) : -1;
-    }
-  }
+  __syncthreads();
+  float* __restrict__ vg = a.values + i0 * k;
+  int32_t* __restrict__ cg = a.classes + i0 * k;
+  unstage<R, CMAX>(
+      rows, k, true, by_k, values, [&](int32_t e, float v) { vg[(uint32_t)e] = v; }, [](int32_t, int32_t, float) {});
+  unstage<R, CMAX>(
+      rows, k, true, by_k, classes, [&](int32_t e, int32_t c) { cg[(uint32_t)e] = c; },
+      [](int32_t, int32_t, int32_t) {});
 }
 
 // ---------------------------------------------------------------- sampling --
@@ -523,6 +776,7 @@ struct SampleArgs {
   int32_t* out;
   float* logp;
   int32_t* err;
+  int64_t row0;  // of this launch
 };
 
 struct RowParams {
@@ -548,187 +802,339 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t i) 
   return r;
 }
 
+// The mass of all places >= keep (m finite).
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT) k_sample_block(const SampleArgs a) {
-  using Elem = typename Score<DT>::Elem;
-  __shared__ SelLds L;
-  const int tid = threadIdx.x;
-  const int bits = mass_bits(a.C);
-  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-    const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-    const RowParams r = row_params(a, i);
-    float m = -kInf, tmax = -kInf, lowest = -kInf;
-    if (r.ok) row_range<DT, NT>(xr, a.C, &m, &tmax, &lowest, L);
-    if (!(m > -kInf)) {
-      if (tid == 0) {
-        if (!r.ok) dev_error(a.err, GBDT_E_RANGE);
-        a.out[i] = -1;
-        if (a.logp != nullptr) a.logp[i] = -kInf;
-      }
-      continue;
+__device__ uint64_t kept_sum(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, uint64_t keep,
+                             const Mass& mass, SelLds<NT>& L) {
+  constexpr int VE = Score<DT>::kVec;
+  uint64_t sum = 0;
+  for (int32_t c0 = threadIdx.x * VE; c0 < C; c0 += NT * VE) {
+    float f[VE];
+    load_chunk<DT>(xr, c0, C, f);
+#pragma unroll
+    for (int q = 0; q < VE; ++q) {
+      const float v = canon(f[q]);
+      if (c0 + q < C && place_of(v, c0 + q) >= keep) sum += mass.q(v);
     }
-    const Mass mass = make_mass(m, r.T > 0.0 ? kLog2e / r.T : 0.0, bits);
-    uint64_t place = 0, total = 0;
-    if (r.top_k <= GBDT_MAX_LISTED) {
-      const int32_t got = collect_top<DT, NT>(xr, a.C, r.top_k, tmax, m, lowest, mass, L);
-      // running sums over the list, then its two cuts and the draw, by one wave
-      if (tid < 64) {
-        constexpr int PL = GBDT_MAX_LISTED / 64;
-        uint64_t w[PL], run[PL], carry = 0;
+  }
+  return block_sum<NT>(sum, L.shu);
+}
+
+// All masses of a row into the bins; returns their sum.
+template <int DT, int NT>
+__device__ uint64_t bin_masses(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, const Mass& mass,
+                               const Bins& bins, SelLds<NT>& L) {
+  constexpr int VE = Score<DT>::kVec, NB = SelLds<NT>::kBins;
+  const int tid = threadIdx.x;
+  uint64_t sum = 0;
+  for (int b = tid; b < NB; b += NT) L.hist[b] = 0ull;
+  __syncthreads();
+  const uint64_t zero = mass.raw_zero();
+  each_block<DT, NT>(xr, C, [&](const RawBlock<DT>& raw, int32_t) {
 #pragma unroll
-        for (int b = 0; b < PL; ++b) {
-          const int32_t at = b * 64 + tid;
-          w[b] = at < got ? mass.q(score_of(L.sorted[at])) : 0ull;
-          uint64_t x = w[b];
-          for (int off = 1; off < 64; off <<= 1) {
-            const uint64_t y = __shfl_up(x, off, 64);
-            if (tid >= off) x += y;
-          }
-          run[b] = x + carry;
-          carry = __shfl(run[b], 63, 64);
-        }
-        const uint64_t target =
-            r.top_p < 1.0 ? (uint64_t)__builtin_ceil(r.top_p * (double)carry) : ~uint64_t(0);
-        uint64_t W = 0;
+    for (int j = 0; j < kVecs; ++j) {
+      float f[VE];
+      unpack<DT>(raw.v[j], f);
 #pragma unroll
-        for (int b = 0; b < PL; ++b) {
-          const int32_t at = b * 64 + tid;
-          const bool kept = at < got && w[b] > 0 && (at == 0 || run[b] - w[b] < target) &&
-                            (at == 0 || mass.e(score_of(L.sorted[at])) >= r.min_p);
-          if (kept) W = run[b];  // (a prefix is kept: the last one's running sum is the largest)
-        }
-        for (int off = 32; off > 0; off >>= 1) {
-          const uint64_t y = __shfl_xor(W, off, 64);
-          W = y > W ? y : W;
-        }
-        uint64_t over = (uint64_t)(r.u * (double)W) + 1ull;
-        if (over > W) over = W;
+      for (int h = 0; h < VE; h += 4) {
 #pragma unroll
-        for (int b = 0; b < PL; ++b) {
-          if (b * 64 + tid < got && run[b] >= over && run[b] - w[b] < over) L.found[0] = L.sorted[b * 64 + tid];
+        for (int q = h; q < h + 4; ++q) {
+          const double d = (double)f[q] - mass.m;
+          const uint64_t w = mass.raw_at(d) - zero;
+          sum += w;
+          if (w != 0)
+            atomicAdd(reinterpret_cast<unsigned long long*>(&L.hist[bins.at<NB>(-d)]), (unsigned long long)w);
         }
-        if (tid == 0) L.found[1] = W;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  });
+  return block_sum<NT>(sum, L.shu);
+}
+
+// One workgroup per row.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int NL = SelLds<NT>::kList, PL = NL / NT, NB = SelLds<NT>::kBins;
+  __shared__ SelLds<NT> L;
+  const int tid = threadIdx.x;
+  const int32_t C = a.C;
+  const int64_t i = a.row0 + blockIdx.x;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  const RowParams r = row_params(a, i);
+  // With a top-k of at most GBDT_MAX_LISTED the list is all that counts; without
+  // one it holds the likely classes, and the others' masses are summed.
+  const bool few = r.top_k <= GBDT_MAX_LISTED, open = r.top_k >= C;
+  Scan sc{-kInf, 0.0f, 0, 0.0};
+  const double c = r.T > 0.0 ? kLog2e / r.T : 0.0;
+  if (r.ok) {
+    if (few || !open)
+      sc = scan_row<DT, NT, kNoSum>(xr, C, few ? r.top_k : 1, c, L);
+    else
+      sc = scan_row<DT, NT, kSum64>(xr, C, 32, c, L);
+  }
+  const float m = sc.m;
+  if (!(m > -kInf)) {
+    if (tid == 0) {
+      if (!r.ok) dev_error(a.err, GBDT_E_RANGE);
+      a.out[i] = -1;
+      if (a.logp != nullptr) a.logp[i] = -kInf;
+    }
+    return;
+  }
+  const int bits = mass_bits(C);
+  const Mass mass = make_mass(m, c, bits);
+  const uint64_t all_kept = uint64_t(kKeyNegInf + 1u) << 32;
+  uint64_t place = 0, total = 0;
+  bool done = false, have = false;
+  if (few || (open && !mass.inf)) {
+    int32_t n = sc.n;
+    bool listed = n <= NL && (!few || n >= r.top_k || C <= NT * kBlk<DT>);
+    if (listed) {
+      rank_list<NT>(L, n);
+    } else if (few) {
+      // from the exact k-th place on, exactly k (or all above -inf) are listed
+      const uint64_t last =
+          locate<DT, NT, kTargetCount>(xr, C, all_kept, (uint64_t)r.top_k, 0.0, m, mass, L, have, 0).place;
+      n = list_from<DT, NT>(xr, C, last, L);
+      listed = true;
+    }
+    if (listed) {
+      // running sums over the list, its two cuts, and the draw
+      const int32_t got = few && n > r.top_k ? r.top_k : n;
+      uint64_t w[PL], before = 0;
+      double e[PL];
+      uint64_t mine = 0;
+#pragma unroll
+      for (int b = 0; b < PL; ++b) {
+        const int32_t at = tid * PL + b;
+        e[b] = at < got ? mass.e(score_of(L.sorted[at])) : 0.0;
+        w[b] = mass.raw(e[b]) - mass.raw_zero();
+        mine += w[b];
+      }
+      uint64_t in_list;
+      before = block_scan_u64<NT>(mine, &in_list, L.shu);
+      // (the others' sum is in FP64, against another reference)
+      uint64_t sum = in_list;
+      if (!few && sc.sum > 0.0)
+        sum += (uint64_t)__builtin_rint(__builtin_ldexp(sc.sum * exp2_64(((double)sc.ref - (double)m) * c), bits));
+      total = sum;
+      const uint64_t most = r.top_p < 1.0 ? (uint64_t)__builtin_ceil(r.top_p * (double)total) : ~uint64_t(0);
+      uint64_t run = before, upto = 0;
+      int32_t kept = 0;
+#pragma unroll
+      for (int b = 0; b < PL; ++b) {
+        const int32_t at = tid * PL + b;
+        const bool keep = at < got && w[b] > 0 && (at == 0 || (run < most && e[b] >= r.min_p));
+        run += w[b];
+        // (a prefix is kept: the last one's running sum is the largest)
+        if (keep) {
+          upto = run;
+          ++kept;
+        }
+      }
+      kept = block_sum<NT>(kept, L.sh32);
+      for (int off = 32; off > 0; off >>= 1) {
+        const uint64_t y = __shfl_xor(upto, off, 64);
+        upto = y > upto ? y : upto;
+      }
+      if ((tid & 63) == 0) L.shu[tid >> 6] = upto;
+      __syncthreads();
+      uint64_t W = across_waves<NT / 64>(L.shu, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
+      // is what is kept known: all of the row, or cut inside the list?
+      const bool cut = few || kept < got || in_list >= most;
+      const bool whole = r.top_p >= 1.0 && r.min_p == 0.0;
+      if (!cut) W = sum;
+      uint64_t over = (uint64_t)(r.u * (double)W) + 1ull;
+      if (over > W) over = W;
+      done = cut || (whole && over <= in_list);
+      run = before;
+#pragma unroll
+      for (int b = 0; b < PL; ++b) {
+        if (run < over && run + w[b] >= over) L.found[0] = L.sorted[tid * PL + b];
+        run += w[b];
       }
       __syncthreads();
       place = L.found[0];
-      total = L.found[1];
-    } else {
-      uint64_t keep = uint64_t(kKeyNegInf + 1u) << 32;
-      if (r.top_k < a.C)
-        keep = locate<DT, NT, kTargetCount>(xr, a.C, keep, (uint64_t)r.top_k, 0.0, m, lowest, bits, mass, L).place;
-      if (r.top_p < 1.0)
-        keep = locate<DT, NT, kTargetFrac>(xr, a.C, keep, 0, r.top_p, m, lowest, bits, mass, L).place;
-      if (r.min_p > 0.0 && !mass.inf) {
-        // e >= min_p exactly where x >= m + log2(min_p) / c
-        const double v = mass.m + log2(r.min_p) / mass.c;
-        const float f = (float)v + 0.0f;
-        uint64_t cut = uint64_t(key_of(f) + ((double)f < v ? 1u : 0u)) << 32;
-        const uint64_t top = uint64_t(key_of(m)) << 32;
-        cut = cut < top ? cut : top;
-        keep = cut > keep ? cut : keep;
-      }
-      const Found f = locate<DT, NT, kTargetOver>(xr, a.C, keep, 0, r.u, m, lowest, bits, mass, L);
-      place = f.place;
-      total = f.total;
+      total = W;
+      __syncthreads();
     }
-    if (tid == 0) {
-      a.out[i] = class_of(place);
-      if (a.logp != nullptr) {
-        const double x = (double)score_of(place);
-        const double d = mass.inf || r.T == 0.0 ? 0.0 : (x - mass.m) / r.T;
-        a.logp[i] = (float)(d - log(__builtin_ldexp((double)total, -bits)));
+  }
+  if (!done) {
+    // by places: the top-k and top-p cuts, the min-p cut, the draw
+    uint64_t keep = all_kept;
+    if (!open) {
+      keep = locate<DT, NT, kTargetCount>(xr, C, keep, (uint64_t)r.top_k, 0.0, m, mass, L, have, 0).place;
+    } else if (!mass.inf) {
+      Bins bins;
+      mass_bins<NB>(mass, m, &bins);
+      if (!bins.flat) {
+        total = bin_masses<DT, NT>(xr, C, mass, bins, L);
+        have = true;
       }
     }
-    __syncthreads();
+    if (r.top_p < 1.0) {
+      const Found f = locate<DT, NT, kTargetFrac>(xr, C, keep, 0, r.top_p, m, mass, L, have, total);
+      keep = f.place;
+      total = f.upto;
+    }
+    bool known = true;  // total: the kept ones' sum
+    if (r.min_p > 0.0 && !mass.inf) {
+      // e >= min_p exactly where x >= m + log2(min_p) / c
+      const double v = mass.m + log2(r.min_p) / mass.c;
+      const float f = (float)v + 0.0f;
+      uint64_t cut = uint64_t(key_of(f) + ((double)f < v ? 1u : 0u)) << 32;
+      const uint64_t top = uint64_t(key_of(m)) << 32;
+      cut = cut < top ? cut : top;
+      if (cut > keep) {
+        keep = cut;
+        known = false;
+      }
+    }
+    if (have && !known) total = kept_sum<DT, NT>(xr, C, keep, mass, L);
+    const Found f = locate<DT, NT, kTargetOver>(xr, C, keep, 0, r.u, m, mass, L, have, total);
+    place = f.place;
+    total = f.total;
+  }
+  if (tid == 0) {
+    a.out[i] = class_of(place);
+    if (a.logp != nullptr) {
+      const double x = (double)score_of(place);
+      const double d = mass.inf || r.T == 0.0 ? 0.0 : (x - mass.m) / r.T;
+      a.logp[i] = (float)(d - log_64(__builtin_ldexp((double)total, -bits)));
+    }
   }
 }
 
-template <int DT, int CMAX>
-__global__ void __launch_bounds__(256) k_sample_rows(const SampleArgs a) {
-  using Elem = typename Score<DT>::Elem;
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= a.n) return;
-  const RowParams r = row_params(a, i);
-  uint64_t p[CMAX];
-  sort_row<DT, CMAX>(static_cast<const Elem*>(a.x) + i * a.ld, a.C, p);
-  const float m = score_of(p[0]);
+// One thread per row of at most CMAX classes, R rows a workgroup.
+template <int DT, int R, int CMAX>
+__global__ void __launch_bounds__(R, CMAX == 8 ? 6 : 3) k_sample_rows(const SampleArgs a) {
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x;
+  const int64_t i0 = int64_t(blockIdx.x) * R, i = i0 + tid;
+  const int32_t rows = (int32_t)(a.n - i0 < R ? a.n - i0 : R);
+  const int32_t C = a.C;
+  const RowDiv by_c(C);
+  stage_scores<DT, R, CMAX>(a.x, i0, rows, C, a.ld, by_c, lds);
+  RowParams r;
+  if (tid < rows) r = row_params(a, i);
+  __syncthreads();
+  if (tid >= rows) return;
+  double p[CMAX];
+  sort_row<CMAX>(lds + tid * (C | 1), C, p);
+  const float m = short_score(p[0]);
   if (!r.ok || !(m > -kInf)) {
     if (!r.ok) dev_error(a.err, GBDT_E_RANGE);
     a.out[i] = -1;
     if (a.logp != nullptr) a.logp[i] = -kInf;
     return;
   }
-  const Mass mass = make_mass(m, r.T > 0.0 ? kLog2e / r.T : 0.0, 50);
-  double e[CMAX], all = 0.0;
+  const bool inf = m == kInf;
+  const double ms = (double)m, c_T = r.T > 0.0 ? kLog2e / r.T : 0.0;
+  double e[CMAX], all = 1.0;  // (the first one's e is 1)
+  e[0] = 1.0;
 #pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    const float v = score_of(p[c]);
-    e[c] = c < r.top_k && c < a.C && v > -kInf ? mass.e(v) : 0.0;
-    all += e[c];
-  }
-  const double most = r.top_p < 1.0 ? r.top_p * all : kInf;
-  double run = 0.0, W = 0.0;
-#pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    const bool kept = c == 0 || (run < most && e[c] >= r.min_p && e[c] > 0.0);
-    run += e[c];
-    e[c] = kept ? e[c] : 0.0;
-    W += e[c];
-  }
-  const double over = r.u * W;
-  uint64_t place = p[0];
-  double ew = e[0];
-  run = 0.0;
-  bool done = false;
-#pragma unroll
-  for (int c = 0; c < CMAX; ++c) {
-    run += e[c];
-    // (the last kept one where rounding leaves none)
-    if (!done && e[c] > 0.0) {
-      place = p[c];
-      ew = e[c];
-      done = run > over;
+  for (int c = 1; c < CMAX; ++c) {
+    e[c] = 0.0;
+    if (c < C) {
+      const float v = short_score(p[c]);
+      const double x = inf ? (v == kInf ? 1.0 : 0.0) : exp2_64(((double)v - ms) * c_T);
+      e[c] = c < r.top_k && v > -kInf ? x : 0.0;
+      all += e[c];
     }
   }
-  a.out[i] = class_of(place);
-  if (a.logp != nullptr) a.logp[i] = (float)log(ew / W);
+  const double most = r.top_p < 1.0 ? r.top_p * all : kInf;
+  double run = 1.0, W = 1.0;
+#pragma unroll
+  for (int c = 1; c < CMAX; ++c) {
+    if (c < C) {
+      const bool kept = run < most && e[c] >= r.min_p && e[c] > 0.0;
+      run += e[c];
+      e[c] = kept ? e[c] : 0.0;
+      W += e[c];
+    }
+  }
+  const double over = r.u * W;
+  double place = p[0], ew = 1.0;
+  run = 1.0;
+  bool found = run > over;
+#pragma unroll
+  for (int c = 1; c < CMAX; ++c) {
+    if (c < C) {
+      run += e[c];
+      // (the last kept one where rounding leaves none)
+      const bool take = !found && e[c] > 0.0;
+      place = take ? p[c] : place;
+      ew = take ? e[c] : ew;
+      found = found || (take && run > over);
+    }
+  }
+  a.out[i] = short_class<CMAX>(place);
+  if (a.logp != nullptr) a.logp[i] = (float)log_64(ew * rcp_64(W));
+}
+
+template <int DT, int NT>
+void launch_top_block(TopArgs a, hipStream_t s) {
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
+    const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    hipLaunchKernelGGL((k_top_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
+  }
+}
+template <int DT, int R, int CMAX>
+void launch_top_rows(const TopArgs& a, hipStream_t s) {
+  const size_t lds = size_t(R) * 4 * ((a.C | 1) + 2 * (a.k | 1));
+  hipLaunchKernelGGL((k_top_rows<DT, R, CMAX>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
 }
 
 template <int DT>
 int launch_top(const TopArgs& a, hipStream_t s) {
   diag_begin(kDiagTopScores, s);
-  const dim3 lanes((unsigned)((a.n + 255) / 256));
-  const dim3 rows((unsigned)(a.n < kMaxRowGrid ? a.n : kMaxRowGrid));
   if (a.C <= 8)
-    hipLaunchKernelGGL((k_top_rows<DT, 8>), lanes, dim3(256), 0, s, a);
+    launch_top_rows<DT, 256, 8>(a, s);
   else if (a.C <= 16)
-    hipLaunchKernelGGL((k_top_rows<DT, 16>), lanes, dim3(256), 0, s, a);
+    launch_top_rows<DT, 128, 16>(a, s);
   else if (a.C <= kRowsMaxClasses)
-    hipLaunchKernelGGL((k_top_rows<DT, 32>), lanes, dim3(256), 0, s, a);
-  else if (a.C <= 8192)
-    hipLaunchKernelGGL((k_top_block<DT, 256>), rows, dim3(256), 0, s, a);
+    launch_top_rows<DT, 64, 32>(a, s);
+  else if (a.C <= 2048)
+    launch_top_block<DT, 64>(a, s);
+  else if (a.C <= 40000)
+    launch_top_block<DT, 256>(a, s);
   else
-    hipLaunchKernelGGL((k_top_block<DT, 1024>), rows, dim3(1024), 0, s, a);
+    launch_top_block<DT, 512>(a, s);
   diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_top");
 }
 
+template <int DT, int NT>
+void launch_sample_block(SampleArgs a, hipStream_t s) {
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
+    const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    hipLaunchKernelGGL((k_sample_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
+  }
+}
+template <int DT, int R, int CMAX>
+void launch_sample_rows(const SampleArgs& a, hipStream_t s) {
+  const size_t lds = size_t(R) * 4 * (a.C | 1);
+  hipLaunchKernelGGL((k_sample_rows<DT, R, CMAX>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
+}
+
 template <int DT>
 int launch_sample(const SampleArgs& a, hipStream_t s) {
   diag_begin(kDiagSample, s);
-  const dim3 lanes((unsigned)((a.n + 255) / 256));
-  const dim3 rows((unsigned)(a.n < kMaxRowGrid ? a.n : kMaxRowGrid));
   if (a.C <= 8)
-    hipLaunchKernelGGL((k_sample_rows<DT, 8>), lanes, dim3(256), 0, s, a);
+    launch_sample_rows<DT, 256, 8>(a, s);
   else if (a.C <= 16)
-    hipLaunchKernelGGL((k_sample_rows<DT, 16>), lanes, dim3(256), 0, s, a);
+    launch_sample_rows<DT, 128, 16>(a, s);
   else if (a.C <= kRowsMaxClasses)
-    hipLaunchKernelGGL((k_sample_rows<DT, 32>), lanes, dim3(256), 0, s, a);
-  else if (a.C <= 8192)
-    hipLaunchKernelGGL((k_sample_block<DT, 256>), rows, dim3(256), 0, s, a);
+    launch_sample_rows<DT, 64, 32>(a, s);
+  else if (a.C <= 2048)
+    launch_sample_block<DT, 64>(a, s);
+  else if (a.C <= 40000)
+    launch_sample_block<DT, 256>(a, s);
   else
-    hipLaunchKernelGGL((k_sample_block<DT, 1024>), rows, dim3(1024), 0, s, a);
+    launch_sample_block<DT, 512>(a, s);
   diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_sample");
