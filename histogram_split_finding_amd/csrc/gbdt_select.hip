@@ -51,12 +51,21 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ (uint32_t(int32_t(~k) >> 31) | 0x80000000u));
 }
-// (score, class) as one integer: larger earlier in the order.
-__device__ __forceinline__ uint64_t place_of(float x, int32_t c) {
-  return uint64_t(key_of(x)) << 32 | uint32_t(~c);
+// (score, class) as one integer: larger earlier in the order.  The bits are
+// those of an FP64 number in [2, 4), whose comparison is one full-rate
+// instruction (an integer one of 64 bits takes four times that).
+constexpr int kClassBits = 20;
+static_assert(GBDT_MAX_CLASSES <= 1 << kClassBits, "a place holds any class");
+__device__ __forceinline__ uint64_t first_place(uint32_t key) {  // below all places of the key
+  return uint64_t(1) << 62 | uint64_t(key) << kClassBits;
 }
-__device__ __forceinline__ float score_of(uint64_t p) { return of_key(uint32_t(p >> 32)); }
-__device__ __forceinline__ int32_t class_of(uint64_t p) { return int32_t(~uint32_t(p)); }
+__device__ __forceinline__ uint64_t place_of(float x, int32_t c) {
+  return first_place(key_of(x)) | uint32_t((1 << kClassBits) - 1 - c);
+}
+__device__ __forceinline__ float score_of(uint64_t p) { return of_key(uint32_t(p >> kClassBits)); }
+__device__ __forceinline__ int32_t class_of(uint64_t p) {
+  return (1 << kClassBits) - 1 - int32_t(p & ((1u << kClassBits) - 1u));
+}
 
 // A row's e_c = 2^((x - m) c) as FP64 and as an integer of s fraction bits.
 struct Mass {
@@ -90,20 +99,27 @@ __device__ __forceinline__ Mass make_mass(float m, double c, int bits) {
   return r;
 }
 
+// Waves per SIMD of the record kernel.
 template <int NT>
-struct SelLds {
-  static constexpr int kBins = NT == 64 ? 256 : NT == 256 ? 1024 : 2048;  // value bins of a locate level
+constexpr int kHotWaves = NT == 64 ? 4 : 6;
+
+template <int NT>
+struct ListLds {
   static constexpr int kList = NT == 64 ? 512 : 1024;  // members that are ranked in LDS
-  uint64_t hist[kBins];
   alignas(16) uint64_t list[kList];
   uint64_t sorted[kList];
   uint64_t shu[16];
   double shd[16];
+  uint64_t cnt[2][16];
   uint64_t found[4];
   float shf[2][16];
-  uint64_t cnt[2][16];
   int32_t sh32[32];
   uint32_t n_list, kmin, kmax;
+};
+template <int NT>
+struct SelLds : ListLds<NT> {
+  static constexpr int kBins = NT == 64 ? 256 : NT == 256 ? 1024 : 2048;  // value bins of a locate level
+  uint64_t hist[kBins];
 };
 
 // Exclusive scan of one uint64 per thread; *total = the sum.
@@ -132,7 +148,7 @@ __device__ inline uint64_t block_scan_u64(uint64_t v, uint64_t* total, uint64_t*
 // those are fewer) reach, and not many more than k; m, lowest: the largest and
 // the smallest of the maxima.
 template <int NT>
-__device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float lowest, int32_t k, SelLds<NT>& L) {
+__device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float lowest, int32_t k, ListLds<NT>& L) {
   // (with 1,024 threads their own maxima are enough groups)
   constexpr int G = NT >= 1024 ? 1 : kVecs;
   uint32_t key[G];
@@ -144,8 +160,19 @@ __device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float low
   lo = lo > kKeyNegInf ? lo : kKeyNegInf + 1u;
   for (int step = 0; hi - lo > 1u; ++step) {
     // three points of the interval at a time: half the barriers
-    const uint32_t q = (hi - lo) / 4u, p2 = lo + (hi - lo) / 2u;
-    const uint32_t p1 = q > 0u ? lo + q : p2, p3 = q > 0u ? p2 + q : p2;
+    // (quarters of the values first, of the keys if that is not enough)
+    const uint32_t q = (hi - lo) / 4u;
+    uint32_t p1 = lo + q, p2 = lo + (hi - lo) / 2u, p3 = p2 + q;
+    if (step < 6 && hi <= 0xff800000u) {
+      const float a = of_key(lo), d = of_key(hi) * 0.25f - a * 0.25f;
+      const uint32_t v1 = key_of(a + d), v2 = key_of(a + 2.0f * d), v3 = key_of(a + 3.0f * d);
+      if (lo < v1 && v1 < v2 && v2 < v3 && v3 < hi) {
+        p1 = v1;
+        p2 = v2;
+        p3 = v3;
+      }
+    }
+    p1 = p1 > lo ? p1 : p2;
     uint64_t n = 0;  // three counts of 21 bits
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -186,37 +213,40 @@ __device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float low
 // entry's place is the number of entries before it.  Eight entries are read at
 // a time, for all of the thread's own ones.
 template <int NT>
-__device__ inline void rank_list(SelLds<NT>& L, int32_t n) {
-  constexpr int PT = SelLds<NT>::kList / NT >= 8 ? 4 : 2;
+__device__ inline void rank_list(ListLds<NT>& L, int32_t n) {
+  constexpr int PT = NT == 64 ? 4 : 1;
   const int tid = threadIdx.x;
   const int32_t n8 = (n + 7) & ~7;
-  if (tid < n8 - n) L.list[n + tid] = 0ull;
+  double* list = reinterpret_cast<double*>(L.list);
+  double* sorted = reinterpret_cast<double*>(L.sorted);
+  if (tid < n8 - n) list[n + tid] = 0.0;
   __syncthreads();
   for (int32_t i0 = 0; i0 < n; i0 += PT * NT) {
-    uint64_t p[PT];
+    double p[PT];
     int32_t r[PT];
 #pragma unroll
     for (int u = 0; u < PT; ++u) {
       const int32_t i = i0 + tid + u * NT;
-      p[u] = i < n ? L.list[i] : ~uint64_t(0);
+      p[u] = i < n ? list[i] : 4.0;
       r[u] = 0;
     }
     if (i0 + (tid & ~63) < n) {  // (whole waves)
       for (int32_t j = 0; j < n8; j += 8) {
-        uint64_t e[8];
+        double e[8];
 #pragma unroll
-        for (int v = 0; v < 8; ++v) e[v] = L.list[j + v];
+        for (int v = 0; v < 8; ++v) e[v] = list[j + v];
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
+        for (int u = 0; u < PT; ++u) {
+          if (u == 0 || u * NT < n - i0) {
 #pragma unroll
-          for (int u = 0; u < PT; ++u)
-            if (u == 0 || u * NT < n - i0) r[u] += e[v] > p[u] ? 1 : 0;
+            for (int v = 0; v < 8; ++v) r[u] += e[v] > p[u] ? 1 : 0;
+          }
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < PT; ++u)
-      if (i0 + tid + u * NT < n) L.sorted[r[u]] = p[u];
+      if (i0 + tid + u * NT < n) sorted[r[u]] = p[u];
   }
   __syncthreads();
 }
@@ -230,20 +260,30 @@ __device__ __forceinline__ double uniform(double x) {
                           __builtin_amdgcn_readfirstlane(__double2loint(x)));
 }
 
+// Bins of the exponents y = (x - ref) c in [low, 0].
+template <int NB>
+__device__ __forceinline__ int32_t bin_of_exponent(double y, double scale) {
+  const int32_t b = (int32_t)(y * scale);
+  return b < NB - 1 ? b : NB - 1;
+}
+
 // What the pass over a row gives: the maximum, how many classes reached the
 // threshold (the first kList of them are in L.list), and the sum of the others'
-// exp2((x - ref) c), in FP64; with kSum32 the exponentials are the hardware's.
-enum { kNoSum, kSum32, kSum64 };
+// exp2((x - ref) c), in FP64; with kSum32 the exponentials are the hardware's;
+// with kBinned they are integers of `bits` fraction bits, also in L.hist by
+// their exponents.  depth > 0: classes with an exponent down to -depth are
+// listed too, if that should not take more than 700 places.
+enum { kNoSum, kSum32, kSum64, kBinned };
 struct Scan {
-  float m, ref;
+  float m, ref, thr;
   int32_t n;
   double sum;
 };
 
-template <int DT, int NT, int SUM>
+template <int DT, int NT, int SUM, typename Lds>
 __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, int32_t k,
-                                         double c, SelLds<NT>& L) {
-  constexpr int VE = Score<DT>::kVec, NL = SelLds<NT>::kList, STEP = NT * kBlk<DT>;
+                                         double c, Lds& L, double depth = 0.0, int bits = 0) {
+  constexpr int VE = Score<DT>::kVec, NL = ListLds<NT>::kList, STEP = NT * kBlk<DT>;
   const int tid = threadIdx.x;
   RawBlock<DT> raw = load_block<DT, NT>(xr, 0, C);
   float gm[kVecs], hi = -kInf, lo = kInf;
@@ -262,19 +302,40 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
     L.shf[1][tid >> 6] = lo;
   }
   if (tid == 0) L.n_list = 0u;
+  if constexpr (SUM == kBinned) {
+    for (int b = tid; b < Lds::kBins; b += NT) L.hist[b] = 0ull;
+  }
   __syncthreads();
   hi = across_waves<NT / 64>(L.shf[0], [](float a, float b) { return __builtin_fmaxf(a, b); });
   lo = across_waves<NT / 64>(L.shf[1], [](float a, float b) { return __builtin_fminf(a, b); });
   // of a row of one block at least k; of a longer one its share of 2 k + 64
   // (k = 64 of 8 blocks: 24 of the first, so 192 +- 39 of the row)
   const int32_t r = C <= STEP ? k : (int32_t)((int64_t)(2 * k + 64) * STEP / C) + 1;
-  const float thr = uniform(of_key(group_threshold<NT>(gm, hi, lo, r, L)));
+  float thr = uniform(of_key(group_threshold<NT>(gm, hi, lo, r, L)));
+  if (depth > 0.0) {
+    const float cut = (float)((double)hi - depth / c);
+    int32_t n = 0;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float f[VE];
+      unpack<DT>(raw.v[j], f);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) n += f[q] >= cut ? 1 : 0;
+    }
+    n = block_sum<NT>(n, L.sh32);
+    const int64_t all = C <= STEP ? n : (int64_t)n * C / STEP;
+    if (all <= (NL == 1024 ? 700 : 350)) thr = uniform(__builtin_fminf(thr, cut));
+  }
   Scan s;
+  s.thr = thr;
   s.ref = hi > -kInf ? uniform(hi) : 0.0f;  // (a masked block: the rest is listed or binned)
   const float cf = uniform(exponent_scale(c));
   const double ref = (double)s.ref, cd = uniform(c);
   float m = -kInf;
   double sum = 0.0;
+  uint64_t sum_q = 0;
+  const double magic = __builtin_ldexp(1.0, 52 - bits), low = -(double)(bits + 2);
+  const uint64_t zero = uint64_t(__double_as_longlong(magic));
   for (int32_t base = 0;;) {
     // the next block is on its way while this one is worked on
     RawBlock<DT> next;
@@ -312,6 +373,22 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      if constexpr (SUM == kBinned) {
+        const double scale = (double)Lds::kBins / low;
+#pragma unroll
+        for (int h = 0; h < VE; h += 4) {
+#pragma unroll
+          for (int q = h; q < h + 4; ++q) {
+            const double y = __builtin_fmax(((double)f[q] - ref) * cd, low);
+            const uint64_t w = uint64_t(__double_as_longlong(exp2_64_near(y) + magic)) - zero;
+            sum_q += w;
+            if (w != 0)
+              atomicAdd(reinterpret_cast<unsigned long long*>(&L.hist[bin_of_exponent<Lds::kBins>(y, scale)]),
+                        (unsigned long long)w);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     if (!more) break;
@@ -320,13 +397,19 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
   }
   m = wave_max(m);
   if ((tid & 63) == 0) L.shf[0][tid >> 6] = m;
-  if (SUM != kNoSum) {
+  if (SUM == kBinned) {
+    sum_q = wave_sum(sum_q);
+    if ((tid & 63) == 0) L.shu[tid >> 6] = sum_q;
+  } else if (SUM != kNoSum) {
     sum = wave_sum(sum);
     if ((tid & 63) == 0) L.shd[tid >> 6] = sum;
   }
   __syncthreads();
   s.m = uniform(across_waves<NT / 64>(L.shf[0], [](float a, float b) { return __builtin_fmaxf(a, b); }) + 0.0f);
-  s.sum = SUM == kNoSum ? 0.0 : across_waves<NT / 64>(L.shd, [](double a, double b) { return a + b; });
+  if (SUM == kBinned)
+    s.sum = (double)across_waves<NT / 64>(L.shu, [](uint64_t a, uint64_t b) { return a + b; });
+  else
+    s.sum = SUM == kNoSum ? 0.0 : across_waves<NT / 64>(L.shd, [](double a, double b) { return a + b; });
   s.n = (int32_t)L.n_list;
   __syncthreads();
   return s;
@@ -385,7 +468,7 @@ template <int DT, int NT, int TARGET>
 __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, uint64_t keep,
                         uint64_t count, double frac, float m, const Mass& mass, SelLds<NT>& L, bool& have,
                         uint64_t total) {
-  constexpr int VE = Score<DT>::kVec, NB = SelLds<NT>::kBins, NL = SelLds<NT>::kList;
+  constexpr int VE = Score<DT>::kVec, NB = SelLds<NT>::kBins, NL = ListLds<NT>::kList;
   constexpr bool kCount = TARGET == kTargetCount;
   const int tid = threadIdx.x;
   Bins bins;
@@ -573,8 +656,8 @@ __device__ Found locate(const typename Score<DT>::Elem* __restrict__ xr, int32_t
 // there are (ranked only when they fit).
 template <int DT, int NT>
 __device__ int32_t list_from(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, uint64_t keep,
-                             SelLds<NT>& L) {
-  constexpr int VE = Score<DT>::kVec, NL = SelLds<NT>::kList;
+                             ListLds<NT>& L) {
+  constexpr int VE = Score<DT>::kVec, NL = ListLds<NT>::kList;
   if (threadIdx.x == 0) L.n_list = 0u;
   __syncthreads();
   for (int32_t c0 = threadIdx.x * VE; c0 < C; c0 += NT * VE) {
@@ -595,6 +678,48 @@ __device__ int32_t list_from(const typename Score<DT>::Elem* __restrict__ xr, in
   return n;
 }
 
+// Rows that the one-read kernel could not finish carry kUnfinished where their
+// first class belongs; a second kernel finds and finishes them.  (Its code in
+// the first one would cost that registers, and every row is done faster by a
+// kernel that has them.)  Each workgroup looks after the rows blockIdx.x +
+// j gridDim.x, a thread a row at a time, and lists the unfinished in LDS.
+constexpr int32_t kUnfinished = -2;
+constexpr int64_t kRestGrid = 256;
+
+template <int NT, typename Work>
+__device__ __forceinline__ void each_unfinished(const int32_t* first, int64_t stride, int64_t n, Work work) {
+  __shared__ int32_t todo[NT];
+  __shared__ uint32_t n_todo;
+  for (int64_t j0 = 0; blockIdx.x + j0 * gridDim.x < n; j0 += NT) {
+    if (threadIdx.x == 0) n_todo = 0u;
+    __syncthreads();
+    const int64_t i = blockIdx.x + (j0 + threadIdx.x) * gridDim.x;
+    if (i < n && first[i * stride] == kUnfinished) todo[atomicAdd(&n_todo, 1u)] = (int32_t)threadIdx.x;
+    __syncthreads();
+    const int32_t left = (int32_t)n_todo;
+    for (int32_t t = 0; t < left; ++t) {
+      work(blockIdx.x + (j0 + todo[t]) * gridDim.x);
+      __syncthreads();
+    }
+    __syncthreads();
+  }
+}
+
+// The largest score of the row.
+template <int DT, int NT>
+__device__ float row_max(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, ListLds<NT>& L) {
+  float m = -kInf;
+  each_block<DT, NT>(xr, C, [&](const RawBlock<DT>& raw, int32_t) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float f[Score<DT>::kVec];
+      unpack<DT>(raw.v[j], f);
+      m = __builtin_fmaxf(m, max_of(f));
+    }
+  });
+  return block_max<NT>(m, L.shf[0]) + 0.0f;
+}
+
 // -------------------------------------------------------------- top scores --
 
 struct TopArgs {
@@ -610,62 +735,82 @@ struct TopArgs {
 
 // One workgroup per row.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, NT == 64 ? 4 : 6) k_top_block(const TopArgs a) {
+__global__ void __launch_bounds__(NT, kHotWaves<NT>) k_top_block(const TopArgs a) {
   using Elem = typename Score<DT>::Elem;
-  constexpr int VE = Score<DT>::kVec, NL = SelLds<NT>::kList;
-  __shared__ SelLds<NT> L;
+  constexpr int NL = ListLds<NT>::kList;
+  __shared__ ListLds<NT> L;
   const int tid = threadIdx.x;
   const int32_t C = a.C, k = a.k;
   const int64_t i = a.row0 + blockIdx.x;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
   const Scan sc = scan_row<DT, NT, kSum32>(xr, C, k, a.c, L);
   const float m = sc.m;
-  int32_t got = 0;
-  float rest = 0.0f;
-  if (m > -kInf) {
+  const int32_t n = sc.n, got = n < k ? n : k;
+  if (m > -kInf && !(n <= NL && (n >= k || C <= NT * kBlk<DT>))) {
+    if (tid == 0) a.classes[i * k] = kUnfinished;
+    return;
+  }
+  if (n > 0) rank_list<NT>(L, n);
+  if (a.rest != nullptr) {
     const bool inf = m == kInf;
     const float cf = exponent_scale(a.c);
-    auto weight = [&](float v) { return inf ? (v == kInf ? 1.0f : 0.0f) : exp2_32((v - m) * cf); };
-    int32_t n = sc.n;
-    double out = 0.0;  // (one thread's part)
-    if (n <= NL && (n >= k || C <= NT * kBlk<DT>)) {
-      rank_list<NT>(L, n);
-      if (tid == 0 && !inf && sc.sum > 0.0) out = sc.sum * exp2_64(((double)sc.ref - (double)m) * a.c);
-    } else {
-      // from the exact k-th place on, exactly k (or all above -inf) are listed
-      uint64_t last = uint64_t(kKeyNegInf + 1u) << 32;
-      bool have = false;
-      last = locate<DT, NT, kTargetCount>(xr, C, last, (uint64_t)k, 0.0, m, Mass(), L, have, 0).place;
-      n = list_from<DT, NT>(xr, C, last, L);
-      if (a.rest != nullptr) {
-        for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
-          float f[VE];
-          load_chunk<DT>(xr, c0, C, f);
-#pragma unroll
-          for (int q = 0; q < VE; ++q) {
-            const float v = canon(f[q]);
-            out += c0 + q < C && place_of(v, c0 + q) < last ? (double)weight(v) : 0.0;
-          }
-        }
-      }
+    double in = 0.0, out = 0.0;
+    for (int32_t j = tid; j < n; j += NT) {
+      const float v = score_of(L.sorted[j]);
+      const double w = (double)(inf ? (v == kInf ? 1.0f : 0.0f) : exp2_32((v - m) * cf));
+      if (j < got) in += w; else out += w;
     }
-    got = n < k ? n : k;
-    if (a.rest != nullptr) {
-      double in = 0.0;
-      for (int32_t j = tid; j < n; j += NT) {
-        const double w = (double)weight(score_of(L.sorted[j]));
-        if (j < got) in += w; else out += w;
-      }
-      in = block_sum<NT>(in, L.shd);
-      out = block_sum<NT>(out, L.shd);
-      rest = (float)(out / (in + out));
-    }
+    if (tid == 0 && !inf && sc.sum > 0.0) out += sc.sum * exp2_64(((double)sc.ref - (double)m) * a.c);
+    in = block_sum<NT>(in, L.shd);
+    out = block_sum<NT>(out, L.shd);
+    if (tid == 0) a.rest[i] = n > 0 ? (float)(out / (in + out)) : 0.0f;
   }
-  if (a.rest != nullptr && tid == 0) a.rest[i] = rest;
   for (int32_t j = tid; j < k; j += NT) {
     a.values[i * k + j] = j < got ? score_of(L.sorted[j]) : -kInf;
     a.classes[i * k + j] = j < got ? class_of(L.sorted[j]) : -1;
   }
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 4) k_top_rest(const TopArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec;
+  __shared__ SelLds<NT> L;
+  const int tid = threadIdx.x;
+  const int32_t C = a.C, k = a.k;
+  each_unfinished<NT>(a.classes, k, a.n, [&](int64_t i) {
+    const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+    const float m = row_max<DT, NT>(xr, C, L);
+    // from the exact k-th place on, exactly k (or all above -inf) are listed
+    uint64_t last = first_place(kKeyNegInf + 1u);
+    bool have = false;
+    last = locate<DT, NT, kTargetCount>(xr, C, last, (uint64_t)k, 0.0, m, Mass(), L, have, 0).place;
+    const int32_t got = list_from<DT, NT>(xr, C, last, L);
+    if (a.rest != nullptr) {
+      const bool inf = m == kInf;
+      const float cf = exponent_scale(a.c);
+      double in = 0.0, out = 0.0;
+      for (int32_t c0 = tid * VE; c0 < C; c0 += NT * VE) {
+        float f[VE];
+        load_chunk<DT>(xr, c0, C, f);
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+          const float v = canon(f[q]);
+          const double w = (double)(inf ? (v == kInf ? 1.0f : 0.0f) : exp2_32((v - m) * cf));
+          if (c0 + q < C) {
+            if (place_of(v, c0 + q) >= last) in += w; else out += w;
+          }
+        }
+      }
+      in = block_sum<NT>(in, L.shd);
+      out = block_sum<NT>(out, L.shd);
+      if (tid == 0) a.rest[i] = (float)(out / (in + out));
+    }
+    for (int32_t j = tid; j < k; j += NT) {
+      a.values[i * k + j] = j < got ? score_of(L.sorted[j]) : -kInf;
+      a.classes[i * k + j] = j < got ? class_of(L.sorted[j]) : -1;
+    }
+  });
 }
 
 // A row of at most CMAX classes in one thread: its places sorted in registers
@@ -805,7 +950,7 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t i) 
 // The mass of all places >= keep (m finite).
 template <int DT, int NT>
 __device__ uint64_t kept_sum(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, uint64_t keep,
-                             const Mass& mass, SelLds<NT>& L) {
+                             const Mass& mass, ListLds<NT>& L) {
   constexpr int VE = Score<DT>::kVec;
   uint64_t sum = 0;
   for (int32_t c0 = threadIdx.x * VE; c0 < C; c0 += NT * VE) {
@@ -852,119 +997,292 @@ __device__ uint64_t bin_masses(const typename Score<DT>::Elem* __restrict__ xr, 
   return block_sum<NT>(sum, L.shu);
 }
 
-// One workgroup per row.
+__device__ __forceinline__ void write_draw(const SampleArgs& a, int64_t i, const RowParams& r, float m, uint64_t place,
+                                           uint64_t total, int bits) {
+  a.out[i] = class_of(place);
+  if (a.logp != nullptr) {
+    const double d = m == kInf || r.T == 0.0 ? 0.0 : ((double)score_of(place) - (double)m) / r.T;
+    a.logp[i] = (float)(d - log_64(__builtin_ldexp((double)total, -bits)));
+  }
+}
+
+// The bin in which the running sum reaches the target (1 <= target <= their
+// sum), or the given bin, and the sum before it: into L.found[0..1]; the target
+// (at most the sum) into L.found[2].
+template <int NT>
+__device__ __forceinline__ void find_bin(uint64_t target, int32_t given, SelLds<NT>& L) {
+  constexpr int PB = SelLds<NT>::kBins / NT;
+  uint64_t mine = 0, all;
+#pragma unroll
+  for (int b = 0; b < PB; ++b) mine += L.hist[threadIdx.x * PB + b];
+  uint64_t run = block_scan_u64<NT>(mine, &all, L.shu);
+  target = target < all ? target : all;
+#pragma unroll
+  for (int b = 0; b < PB; ++b) {
+    const int32_t at = (int32_t)threadIdx.x * PB + b;
+    const uint64_t h = L.hist[at];
+    if (given >= 0 ? at == given : run < target && run + h >= target) {
+      L.found[0] = uint64_t(at);
+      L.found[1] = run;
+      L.found[2] = target;
+    }
+    run += h;
+  }
+  __syncthreads();
+}
+
+// Of the classes below the list, in the order: the place where their running
+// sum reaches the target (into L.found[0]) and the sum up to it (L.found[1]); or
+// with by_value the sum of those with a score >= least.  False if the bin has
+// more members than the list holds.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
+__device__ __forceinline__ bool search_bins(const typename Score<DT>::Elem* __restrict__ xr, int32_t C,
+                                            uint64_t target, bool by_value, float least, const Scan& sc, double c,
+                                            int bits, SelLds<NT>& L) {
+  constexpr int VE = Score<DT>::kVec, NL = ListLds<NT>::kList, NB = SelLds<NT>::kBins;
+  const int tid = threadIdx.x;
+  const double low = -(double)(bits + 2), scale = (double)NB / low, ref = (double)sc.ref;
+  const double magic = __builtin_ldexp(1.0, 52 - bits);
+  const uint64_t zero = uint64_t(__double_as_longlong(magic));
+  int32_t given = -1;
+  if (by_value) given = bin_of_exponent<NB>(__builtin_fmax(((double)least - ref) * c, low), scale);
+  find_bin<NT>(target, given, L);
+  const int32_t bin = (int32_t)L.found[0];
+  const uint64_t above = L.found[1];
+  target = L.found[2];
+  if (tid == 0) L.n_list = 0u;
+  __syncthreads();
+  // The bin's scores lie within 1.5 bins' width of its middle, if a vector has
+  // one this near: the exact test.
+  const float mid = uniform((float)(ref + ((double)bin + 0.5) / scale / c));
+  const float wide = uniform((float)(-1.5 / scale / c) + 1e-6f * __builtin_fabsf(mid));
+  each_block<DT, NT>(xr, C, [&](const RawBlock<DT>& raw, int32_t base) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float f[VE], d[VE];
+      unpack<DT>(raw.v[j], f);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) d[q] = -__builtin_fabsf(f[q] - mid);
+      if (max_of(d) >= -wide) {
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+          const double y = ((double)f[q] - ref) * c;
+          if (f[q] < sc.thr && y >= low && bin_of_exponent<NB>(y, scale) == bin) {
+            const uint32_t at = atomicAdd(&L.n_list, 1u);
+            if (at < (uint32_t)NL) L.list[at] = place_of(f[q] + 0.0f, base + (j * NT + tid) * VE + q);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  });
+  __syncthreads();
+  const int32_t n = (int32_t)L.n_list;
+  if (n > NL) return false;
+  rank_list<NT>(L, n);
+  // running sums in the order, by one wave
+  if (tid < 64) {
+    uint64_t carry = above;
+    if (tid == 0 && by_value) L.found[1] = above;
+    for (int32_t b = 0; b < n; b += 64) {
+      const int32_t at = b + tid;
+      const float v = at < n ? score_of(L.sorted[at]) : -kInf;
+      const double y = at < n ? ((double)v - ref) * c : low;
+      const uint64_t w = uint64_t(__double_as_longlong(exp2_64_near(y) + magic)) - zero;
+      uint64_t x = w;
+      for (int off = 1; off < 64; off <<= 1) {
+        const uint64_t up = __shfl_up(x, off, 64);
+        if (tid >= off) x += up;
+      }
+      x += carry;
+      if (by_value) {
+        const uint64_t in = __ballot(v >= least);
+        if (in != 0 && tid == 63 - __builtin_clzll(in)) L.found[1] = x;
+      } else if (at < n && x >= target && x - w < target) {
+        L.found[0] = L.sorted[at];
+        L.found[1] = x;
+      }
+      carry = __shfl(x, 63, 64);
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// How a row is drawn: from its first top-k classes; or from the likely classes
+// and the others' sum; or with the others' masses in bins (whose atomics make
+// the pass half as long again: rows with a min-p, whose cut is seldom below the
+// likely classes, are tried without first).
+enum { kDrawFew, kDrawLikely, kDrawBinned };
+
+// The first place of the scores with e >= min_p (x >= m + log2(min_p) / c).
+__device__ __forceinline__ uint64_t min_p_place(double min_p, const Mass& mass) {
+  const double v = mass.m + log2(min_p) / mass.c;
+  const float f = (float)v + 0.0f;
+  const uint64_t cut = first_place(key_of(f) + ((double)f < v ? 1u : 0u));
+  const uint64_t top = first_place(key_of((float)mass.m));
+  return cut < top ? cut : top;
+}
+
+template <int DT, int NT, int HOW>
+__device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const RowParams& r, SelLds<NT>& L) {
   using Elem = typename Score<DT>::Elem;
-  constexpr int NL = SelLds<NT>::kList, PL = NL / NT, NB = SelLds<NT>::kBins;
-  __shared__ SelLds<NT> L;
+  constexpr int NL = ListLds<NT>::kList, PL = NL / NT;
+  constexpr bool FEW = HOW == kDrawFew;
   const int tid = threadIdx.x;
   const int32_t C = a.C;
-  const int64_t i = a.row0 + blockIdx.x;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-  const RowParams r = row_params(a, i);
-  // With a top-k of at most GBDT_MAX_LISTED the list is all that counts; without
-  // one it holds the likely classes, and the others' masses are summed.
-  const bool few = r.top_k <= GBDT_MAX_LISTED, open = r.top_k >= C;
-  Scan sc{-kInf, 0.0f, 0, 0.0};
   const double c = r.T > 0.0 ? kLog2e / r.T : 0.0;
-  if (r.ok) {
-    if (few || !open)
-      sc = scan_row<DT, NT, kNoSum>(xr, C, few ? r.top_k : 1, c, L);
-    else
-      sc = scan_row<DT, NT, kSum64>(xr, C, 32, c, L);
-  }
+  const int bits = mass_bits(C);
+  Scan sc;
+  if (HOW == kDrawFew) sc = scan_row<DT, NT, kNoSum>(xr, C, r.top_k, c, L);
+  if (HOW == kDrawLikely) sc = scan_row<DT, NT, kSum64>(xr, C, 32, c, L, -log_64(r.min_p) * kLog2e, bits);
+  if (HOW == kDrawBinned) sc = scan_row<DT, NT, kBinned>(xr, C, 32, c, L, 0.0, bits);
   const float m = sc.m;
+  const int32_t n = sc.n, got = FEW && n > r.top_k ? r.top_k : n;
   if (!(m > -kInf)) {
     if (tid == 0) {
-      if (!r.ok) dev_error(a.err, GBDT_E_RANGE);
       a.out[i] = -1;
       if (a.logp != nullptr) a.logp[i] = -kInf;
     }
-    return;
+    return true;
   }
-  const int bits = mass_bits(C);
+  if (n > NL || n == 0 || (FEW ? n < r.top_k && C > NT * kBlk<DT> : m == kInf)) return false;
+  rank_list<NT>(L, n);
   const Mass mass = make_mass(m, c, bits);
-  const uint64_t all_kept = uint64_t(kKeyNegInf + 1u) << 32;
-  uint64_t place = 0, total = 0;
-  bool done = false, have = false;
-  if (few || (open && !mass.inf)) {
-    int32_t n = sc.n;
-    bool listed = n <= NL && (!few || n >= r.top_k || C <= NT * kBlk<DT>);
-    if (listed) {
-      rank_list<NT>(L, n);
-    } else if (few) {
-      // from the exact k-th place on, exactly k (or all above -inf) are listed
-      const uint64_t last =
-          locate<DT, NT, kTargetCount>(xr, C, all_kept, (uint64_t)r.top_k, 0.0, m, mass, L, have, 0).place;
-      n = list_from<DT, NT>(xr, C, last, L);
-      listed = true;
-    }
-    if (listed) {
-      // running sums over the list, its two cuts, and the draw
-      const int32_t got = few && n > r.top_k ? r.top_k : n;
-      uint64_t w[PL], before = 0;
-      double e[PL];
-      uint64_t mine = 0;
+  // running sums over the list (thread by thread PL entries), its two cuts, and
+  // the draw
+  uint64_t p[PL], w[PL], mine = 0;
 #pragma unroll
-      for (int b = 0; b < PL; ++b) {
-        const int32_t at = tid * PL + b;
-        e[b] = at < got ? mass.e(score_of(L.sorted[at])) : 0.0;
-        w[b] = mass.raw(e[b]) - mass.raw_zero();
-        mine += w[b];
-      }
-      uint64_t in_list;
-      before = block_scan_u64<NT>(mine, &in_list, L.shu);
-      // (the others' sum is in FP64, against another reference)
-      uint64_t sum = in_list;
-      if (!few && sc.sum > 0.0)
-        sum += (uint64_t)__builtin_rint(__builtin_ldexp(sc.sum * exp2_64(((double)sc.ref - (double)m) * c), bits));
-      total = sum;
-      const uint64_t most = r.top_p < 1.0 ? (uint64_t)__builtin_ceil(r.top_p * (double)total) : ~uint64_t(0);
-      uint64_t run = before, upto = 0;
-      int32_t kept = 0;
+  for (int b = 0; b < PL; ++b) {
+    const int32_t at = tid * PL + b;
+    p[b] = at < got ? L.sorted[at] : 0;
+    w[b] = at < got ? mass.q(score_of(p[b])) : 0;
+    mine += w[b];
+  }
+  uint64_t in_list;
+  const uint64_t before = block_scan_u64<NT>(mine, &in_list, L.shu);
+  // the others' sum is against another reference
+  const double below = FEW ? 0.0 : HOW == kDrawBinned ? sc.sum : __builtin_ldexp(sc.sum, bits);
+  const double to_m = below > 0.0 ? exp2_64(((double)sc.ref - (double)m) * c) : 0.0;
+  const uint64_t sum = in_list + (uint64_t)__builtin_rint(below * to_m);
+  const uint64_t most = r.top_p < 1.0 ? (uint64_t)__builtin_ceil(r.top_p * (double)sum) : ~uint64_t(0);
+  uint64_t run = before, upto = 0;
+  int32_t kept = 0;
 #pragma unroll
-      for (int b = 0; b < PL; ++b) {
-        const int32_t at = tid * PL + b;
-        const bool keep = at < got && w[b] > 0 && (at == 0 || (run < most && e[b] >= r.min_p));
-        run += w[b];
-        // (a prefix is kept: the last one's running sum is the largest)
-        if (keep) {
-          upto = run;
-          ++kept;
-        }
-      }
-      kept = block_sum<NT>(kept, L.sh32);
-      for (int off = 32; off > 0; off >>= 1) {
-        const uint64_t y = __shfl_xor(upto, off, 64);
-        upto = y > upto ? y : upto;
-      }
-      if ((tid & 63) == 0) L.shu[tid >> 6] = upto;
-      __syncthreads();
-      uint64_t W = across_waves<NT / 64>(L.shu, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
-      // is what is kept known: all of the row, or cut inside the list?
-      const bool cut = few || kept < got || in_list >= most;
-      const bool whole = r.top_p >= 1.0 && r.min_p == 0.0;
-      if (!cut) W = sum;
-      uint64_t over = (uint64_t)(r.u * (double)W) + 1ull;
-      if (over > W) over = W;
-      done = cut || (whole && over <= in_list);
-      run = before;
-#pragma unroll
-      for (int b = 0; b < PL; ++b) {
-        if (run < over && run + w[b] >= over) L.found[0] = L.sorted[tid * PL + b];
-        run += w[b];
-      }
-      __syncthreads();
-      place = L.found[0];
-      total = W;
-      __syncthreads();
+  for (int b = 0; b < PL; ++b) {
+    const int32_t at = tid * PL + b;
+    const bool keep =
+        at < got && w[b] > 0 && (at == 0 || (run < most && (r.min_p == 0.0 || mass.e(score_of(p[b])) >= r.min_p)));
+    run += w[b];
+    // (a prefix is kept: the last one's running sum is the largest)
+    if (keep) {
+      upto = run;
+      ++kept;
     }
   }
-  if (!done) {
-    // by places: the top-k and top-p cuts, the min-p cut, the draw
-    uint64_t keep = all_kept;
-    if (!open) {
+  kept = block_sum<NT>(kept, L.sh32);
+  for (int off = 32; off > 0; off >>= 1) {
+    const uint64_t y = __shfl_xor(upto, off, 64);
+    upto = y > upto ? y : upto;
+  }
+  if ((tid & 63) == 0) L.shu[tid >> 6] = upto;
+  __syncthreads();
+  uint64_t W = across_waves<NT / 64>(L.shu, [](uint64_t u, uint64_t v) { return u > v ? u : v; });
+  // is what is kept known: cut inside the list, or all of the row?
+  bool known = FEW || kept < got || in_list >= most || sum == in_list;
+  if (!known && r.top_p >= 1.0 && r.min_p == 0.0) {
+    W = sum;
+    known = true;
+  }
+  uint64_t last = 0;  // (below the list: the last place that is kept)
+  if (HOW == kDrawBinned && !known) {
+    W = sum;
+    if (most < sum) {
+      const uint64_t target = (uint64_t)__builtin_ceil((double)(most - in_list) / to_m);
+      if (!search_bins<DT, NT>(xr, C, target, false, 0.0f, sc, c, bits, L)) return false;
+      last = L.found[0];
+      W = in_list + (uint64_t)__builtin_rint((double)L.found[1] * to_m);
+      __syncthreads();
+    }
+    if (r.min_p > 0.0) {
+      const uint64_t cut = min_p_place(r.min_p, mass);
+      if (cut > last) {
+        if (!search_bins<DT, NT>(xr, C, 0, true, score_of(cut), sc, c, bits, L)) return false;
+        last = cut;
+        W = in_list + (uint64_t)__builtin_rint((double)L.found[1] * to_m);
+        __syncthreads();
+      }
+    }
+    known = true;
+  }
+  if (!known) return false;
+  uint64_t over = (uint64_t)(r.u * (double)W) + 1ull;
+  if (over > W) over = W;
+  if (over <= in_list) {
+    run = before;
+#pragma unroll
+    for (int b = 0; b < PL; ++b) {
+      if (run < over && run + w[b] >= over) write_draw(a, i, r, m, p[b], W, bits);
+      run += w[b];
+    }
+    return true;
+  }
+  if (HOW != kDrawBinned) return false;
+  const uint64_t target = (uint64_t)__builtin_ceil((double)(over - in_list) / to_m);
+  if (!search_bins<DT, NT>(xr, C, target, false, 0.0f, sc, c, bits, L)) return false;
+  if (tid == 0) write_draw(a, i, r, m, L.found[0], W, bits);
+  return true;
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
+  __shared__ SelLds<NT> L;
+  const int64_t i = a.row0 + blockIdx.x;
+  const RowParams r = row_params(a, i);
+  if (!r.ok) {
+    if (threadIdx.x == 0) {
+      dev_error(a.err, GBDT_E_RANGE);
+      a.out[i] = -1;
+      if (a.logp != nullptr) a.logp[i] = -kInf;
+    }
+  } else if (r.top_k <= GBDT_MAX_LISTED) {
+    if (sample_row<DT, NT, kDrawFew>(a, i, r, L)) return;
+    if (threadIdx.x == 0) a.out[i] = kUnfinished;
+  } else if (r.top_k >= a.C) {
+    if (r.min_p > 0.0 && sample_row<DT, NT, kDrawLikely>(a, i, r, L)) return;
+    __syncthreads();
+    if (sample_row<DT, NT, kDrawBinned>(a, i, r, L)) return;
+    if (threadIdx.x == 0) a.out[i] = kUnfinished;
+  } else if (threadIdx.x == 0) {
+    a.out[i] = kUnfinished;
+  }
+}
+
+// The rows that are left, by places: the top-k and top-p cuts, the min-p cut,
+// the draw.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 4) k_sample_rest(const SampleArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int NB = SelLds<NT>::kBins;
+  __shared__ SelLds<NT> L;
+  const int32_t C = a.C;
+  const int bits = mass_bits(C);
+  each_unfinished<NT>(a.out, 1, a.n, [&](int64_t i) {
+    const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+    const RowParams r = row_params(a, i);
+    const float m = row_max<DT, NT>(xr, C, L);
+    if (!(m > -kInf)) {
+      if (threadIdx.x == 0) {
+        a.out[i] = -1;
+        if (a.logp != nullptr) a.logp[i] = -kInf;
+      }
+      return;
+    }
+    const Mass mass = make_mass(m, r.T > 0.0 ? kLog2e / r.T : 0.0, bits);
+    uint64_t keep = first_place(kKeyNegInf + 1u), total = 0;
+    bool have = false;
+    if (r.top_k < C) {
       keep = locate<DT, NT, kTargetCount>(xr, C, keep, (uint64_t)r.top_k, 0.0, m, mass, L, have, 0).place;
     } else if (!mass.inf) {
       Bins bins;
@@ -974,37 +1292,30 @@ __global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
         have = true;
       }
     }
-    if (r.top_p < 1.0) {
+    if (r.T > 0.0 && r.top_p < 1.0) {
       const Found f = locate<DT, NT, kTargetFrac>(xr, C, keep, 0, r.top_p, m, mass, L, have, total);
       keep = f.place;
       total = f.upto;
     }
     bool known = true;  // total: the kept ones' sum
-    if (r.min_p > 0.0 && !mass.inf) {
-      // e >= min_p exactly where x >= m + log2(min_p) / c
-      const double v = mass.m + log2(r.min_p) / mass.c;
-      const float f = (float)v + 0.0f;
-      uint64_t cut = uint64_t(key_of(f) + ((double)f < v ? 1u : 0u)) << 32;
-      const uint64_t top = uint64_t(key_of(m)) << 32;
-      cut = cut < top ? cut : top;
+    if (r.T > 0.0 && r.min_p > 0.0 && !mass.inf) {
+      const uint64_t cut = min_p_place(r.min_p, mass);
       if (cut > keep) {
         keep = cut;
         known = false;
       }
     }
     if (have && !known) total = kept_sum<DT, NT>(xr, C, keep, mass, L);
-    const Found f = locate<DT, NT, kTargetOver>(xr, C, keep, 0, r.u, m, mass, L, have, total);
-    place = f.place;
-    total = f.total;
-  }
-  if (tid == 0) {
-    a.out[i] = class_of(place);
-    if (a.logp != nullptr) {
-      const double x = (double)score_of(place);
-      const double d = mass.inf || r.T == 0.0 ? 0.0 : (x - mass.m) / r.T;
-      a.logp[i] = (float)(d - log_64(__builtin_ldexp((double)total, -bits)));
+    uint64_t place = keep;
+    if (r.T > 0.0) {
+      const Found f = locate<DT, NT, kTargetOver>(xr, C, keep, 0, r.u, m, mass, L, have, total);
+      place = f.place;
+      total = f.total;
+    } else {
+      total = uint64_t(1) << bits;  // (top_k is 1: the first place has all the mass)
     }
-  }
+    if (threadIdx.x == 0) write_draw(a, i, r, m, place, total, bits);
+  });
 }
 
 // One thread per row of at most CMAX classes, R rows a workgroup.
@@ -1080,6 +1391,11 @@ void launch_top_block(TopArgs a, hipStream_t s) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
     hipLaunchKernelGGL((k_top_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
   }
+  // (a row of one block that fits the list is always finished)
+  if (a.C <= ListLds<NT>::kList && a.C <= NT * kBlk<DT>) return;
+  const dim3 rest((unsigned)(a.n < kRestGrid ? a.n : kRestGrid));
+  constexpr int RT = NT < 512 ? NT : 512;
+  hipLaunchKernelGGL((k_top_rest<DT, RT>), rest, dim3(RT), 0, s, a);
 }
 template <int DT, int R, int CMAX>
 void launch_top_rows(const TopArgs& a, hipStream_t s) {
@@ -1113,6 +1429,9 @@ void launch_sample_block(SampleArgs a, hipStream_t s) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
     hipLaunchKernelGGL((k_sample_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
   }
+  const dim3 rest((unsigned)(a.n < kRestGrid ? a.n : kRestGrid));
+  constexpr int RT = NT < 512 ? NT : 512;
+  hipLaunchKernelGGL((k_sample_rest<DT, RT>), rest, dim3(RT), 0, s, a);
 }
 template <int DT, int R, int CMAX>
 void launch_sample_rows(const SampleArgs& a, hipStream_t s) {
