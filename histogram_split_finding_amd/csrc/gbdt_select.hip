@@ -118,7 +118,7 @@ struct ListLds {
 };
 template <int NT>
 struct SelLds : ListLds<NT> {
-  static constexpr int kBins = NT == 64 ? 256 : NT == 256 ? 1024 : 2048;  // value bins of a locate level
+  static constexpr int kBins = NT == 64 ? 256 : 2048;  // value bins of a locate level
   uint64_t hist[kBins];
 };
 
@@ -271,27 +271,34 @@ __device__ __forceinline__ int32_t bin_of_exponent(double y, double scale) {
 // threshold (the first kList of them are in L.list), and the sum of the others'
 // exp2((x - ref) c), in FP64; with kSum32 the exponentials are the hardware's;
 // with kBinned they are integers of `bits` fraction bits, also in L.hist by
-// their exponents.  depth > 0: classes with an exponent down to -depth are
-// listed too, if that should not take more than 700 places.
+// their exponents.  scan_begin() finds the threshold; with depth > 0 classes
+// with an exponent down to -depth are to be listed too: if that should take
+// too many places, `deep` says so.
 enum { kNoSum, kSum32, kSum64, kBinned };
 struct Scan {
   float m, ref, thr;
   int32_t n;
   double sum;
+  double bins_low;  // exponent of the lowest bin's end
+  bool deep;
 };
 
-template <int DT, int NT, int SUM, typename Lds>
-__device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, int32_t k,
-                                         double c, Lds& L, double depth = 0.0, int bits = 0) {
+template <int DT, int NT, bool BINS>
+__device__ __forceinline__ Scan scan_begin(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, int32_t k,
+                                           double c, double depth, RawBlock<DT>& raw, ListLds<NT>& L) {
   constexpr int VE = Score<DT>::kVec, NL = ListLds<NT>::kList, STEP = NT * kBlk<DT>;
   const int tid = threadIdx.x;
-  RawBlock<DT> raw = load_block<DT, NT>(xr, 0, C);
-  float gm[kVecs], hi = -kInf, lo = kInf;
+  raw = load_block<DT, NT>(xr, 0, C);
+  float gm[kVecs], hi = -kInf, lo = kInf, least = kInf;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     float f[VE];
     unpack<DT>(raw.v[j], f);
     gm[j] = __builtin_fmaxf(max_of(f), -kInf) + 0.0f;
+    if (BINS) {
+#pragma unroll
+      for (int q = 0; q < VE; ++q) least = __builtin_fminf(least, f[q] == -kInf ? kInf : f[q]);
+    }
     hi = __builtin_fmaxf(hi, gm[j]);
     lo = __builtin_fminf(lo, gm[j]);
   }
@@ -302,8 +309,9 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
     L.shf[1][tid >> 6] = lo;
   }
   if (tid == 0) L.n_list = 0u;
-  if constexpr (SUM == kBinned) {
-    for (int b = tid; b < Lds::kBins; b += NT) L.hist[b] = 0ull;
+  if (BINS) {
+    least = wave_min(least);
+    if ((tid & 63) == 0) L.shd[tid >> 6] = (double)least;
   }
   __syncthreads();
   hi = across_waves<NT / 64>(L.shf[0], [](float a, float b) { return __builtin_fmaxf(a, b); });
@@ -311,9 +319,12 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
   // of a row of one block at least k; of a longer one its share of 2 k + 64
   // (k = 64 of 8 blocks: 24 of the first, so 192 +- 39 of the row)
   const int32_t r = C <= STEP ? k : (int32_t)((int64_t)(2 * k + 64) * STEP / C) + 1;
+  Scan s;
+  s.deep = false;
   float thr = uniform(of_key(group_threshold<NT>(gm, hi, lo, r, L)));
   if (depth > 0.0) {
-    const float cut = (float)((double)hi - depth / c);
+    // (a little lower: roundings take no class off that belongs)
+    const float cut = (float)((double)hi - depth / c * (1.0 + 1e-6)) - 1e-6f * __builtin_fabsf(hi);
     int32_t n = 0;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -324,11 +335,33 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
     }
     n = block_sum<NT>(n, L.sh32);
     const int64_t all = C <= STEP ? n : (int64_t)n * C / STEP;
-    if (all <= (NL == 1024 ? 700 : 350)) thr = uniform(__builtin_fminf(thr, cut));
+    s.deep = all > NL / 3 * 2;
+    if (!s.deep) thr = uniform(__builtin_fminf(thr, cut));
   }
-  Scan s;
   s.thr = thr;
   s.ref = hi > -kInf ? uniform(hi) : 0.0f;  // (a masked block: the rest is listed or binned)
+  // the bins end a little below the block's lowest class (what is lower shares
+  // the last one), or where masses end
+  s.bins_low = -1100.0;
+  if (BINS) {
+    const double l = across_waves<NT / 64>(L.shd, [](double a, double b) { return a < b ? a : b; });
+    s.bins_low = uniform((l - (double)hi) * c * 1.125 - 0.01);
+    __syncthreads();
+  }
+  return s;
+}
+
+// The pass itself; raw: the first block.
+template <int DT, int NT, int SUM, typename Lds>
+__device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, double c,
+                                            int bits, RawBlock<DT> raw, Lds& L, Scan& s) {
+  constexpr int VE = Score<DT>::kVec, NL = ListLds<NT>::kList, STEP = NT * kBlk<DT>;
+  const int tid = threadIdx.x;
+  if constexpr (SUM == kBinned) {
+    for (int b = tid; b < Lds::kBins; b += NT) L.hist[b] = 0ull;
+    __syncthreads();
+  }
+  const float thr = s.thr;
   const float cf = uniform(exponent_scale(c));
   const double ref = (double)s.ref, cd = uniform(c);
   float m = -kInf;
@@ -374,7 +407,7 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
         }
       }
       if constexpr (SUM == kBinned) {
-        const double scale = (double)Lds::kBins / low;
+        const double scale = (double)Lds::kBins / (s.bins_low > low ? s.bins_low : low);
 #pragma unroll
         for (int h = 0; h < VE; h += 4) {
 #pragma unroll
@@ -412,7 +445,6 @@ __device__ __forceinline__ Scan scan_row(const typename Score<DT>::Elem* __restr
     s.sum = SUM == kNoSum ? 0.0 : across_waves<NT / 64>(L.shd, [](double a, double b) { return a + b; });
   s.n = (int32_t)L.n_list;
   __syncthreads();
-  return s;
 }
 
 // What a place search finds: the place, the sum up to and with it, the sum of
@@ -743,7 +775,9 @@ __global__ void __launch_bounds__(NT, kHotWaves<NT>) k_top_block(const TopArgs a
   const int32_t C = a.C, k = a.k;
   const int64_t i = a.row0 + blockIdx.x;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-  const Scan sc = scan_row<DT, NT, kSum32>(xr, C, k, a.c, L);
+  RawBlock<DT> raw;
+  Scan sc = scan_begin<DT, NT, false>(xr, C, k, a.c, 0.0, raw, L);
+  scan_blocks<DT, NT, kSum32>(xr, C, a.c, 0, raw, L, sc);
   const float m = sc.m;
   const int32_t n = sc.n, got = n < k ? n : k;
   if (m > -kInf && !(n <= NL && (n >= k || C <= NT * kBlk<DT>))) {
@@ -1041,7 +1075,8 @@ __device__ __forceinline__ bool search_bins(const typename Score<DT>::Elem* __re
                                             int bits, SelLds<NT>& L) {
   constexpr int VE = Score<DT>::kVec, NL = ListLds<NT>::kList, NB = SelLds<NT>::kBins;
   const int tid = threadIdx.x;
-  const double low = -(double)(bits + 2), scale = (double)NB / low, ref = (double)sc.ref;
+  const double low = -(double)(bits + 2), ref = (double)sc.ref;
+  const double scale = (double)NB / (sc.bins_low > low ? sc.bins_low : low);
   const double magic = __builtin_ldexp(1.0, 52 - bits);
   const uint64_t zero = uint64_t(__double_as_longlong(magic));
   int32_t given = -1;
@@ -1052,10 +1087,10 @@ __device__ __forceinline__ bool search_bins(const typename Score<DT>::Elem* __re
   target = L.found[2];
   if (tid == 0) L.n_list = 0u;
   __syncthreads();
-  // The bin's scores lie within 1.5 bins' width of its middle, if a vector has
-  // one this near: the exact test.
+  // The bin's scores lie within a bin's width of its middle (the last one's
+  // anywhere below); where a vector has one, the exact test.
   const float mid = uniform((float)(ref + ((double)bin + 0.5) / scale / c));
-  const float wide = uniform((float)(-1.5 / scale / c) + 1e-6f * __builtin_fabsf(mid));
+  const float wide = bin == NB - 1 ? kInf : uniform((float)(-1.0 / scale / c) + 1e-6f * __builtin_fabsf(mid));
   each_block<DT, NT>(xr, C, [&](const RawBlock<DT>& raw, int32_t base) {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -1109,12 +1144,6 @@ __device__ __forceinline__ bool search_bins(const typename Score<DT>::Elem* __re
   return true;
 }
 
-// How a row is drawn: from its first top-k classes; or from the likely classes
-// and the others' sum; or with the others' masses in bins (whose atomics make
-// the pass half as long again: rows with a min-p, whose cut is seldom below the
-// likely classes, are tried without first).
-enum { kDrawFew, kDrawLikely, kDrawBinned };
-
 // The first place of the scores with e >= min_p (x >= m + log2(min_p) / c).
 __device__ __forceinline__ uint64_t min_p_place(double min_p, const Mass& mass) {
   const double v = mass.m + log2(min_p) / mass.c;
@@ -1124,20 +1153,28 @@ __device__ __forceinline__ uint64_t min_p_place(double min_p, const Mass& mass) 
   return cut < top ? cut : top;
 }
 
-template <int DT, int NT, int HOW>
+// A row is drawn from its first top-k classes (FEW); or from its likely classes
+// and the others' sum, where a min-p cuts not far below the maximum; or with
+// the others' masses in bins, whose atomics make the pass half as long again.
+template <int DT, int NT, bool FEW>
 __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const RowParams& r, SelLds<NT>& L) {
   using Elem = typename Score<DT>::Elem;
   constexpr int NL = ListLds<NT>::kList, PL = NL / NT;
-  constexpr bool FEW = HOW == kDrawFew;
   const int tid = threadIdx.x;
   const int32_t C = a.C;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
   const double c = r.T > 0.0 ? kLog2e / r.T : 0.0;
   const int bits = mass_bits(C);
-  Scan sc;
-  if (HOW == kDrawFew) sc = scan_row<DT, NT, kNoSum>(xr, C, r.top_k, c, L);
-  if (HOW == kDrawLikely) sc = scan_row<DT, NT, kSum64>(xr, C, 32, c, L, -log_64(r.min_p) * kLog2e, bits);
-  if (HOW == kDrawBinned) sc = scan_row<DT, NT, kBinned>(xr, C, 32, c, L, 0.0, bits);
+  RawBlock<DT> raw;
+  const double depth = !FEW && r.min_p > 0.0 ? -log_64(r.min_p) * kLog2e : 0.0;
+  Scan sc = scan_begin<DT, NT, !FEW>(xr, C, FEW ? r.top_k : 32, c, depth, raw, L);
+  const bool binned = !FEW && (r.min_p == 0.0 || sc.deep);
+  if (FEW)
+    scan_blocks<DT, NT, kNoSum>(xr, C, c, bits, raw, L, sc);
+  else if (binned)
+    scan_blocks<DT, NT, kBinned>(xr, C, c, bits, raw, L, sc);
+  else
+    scan_blocks<DT, NT, kSum64>(xr, C, c, bits, raw, L, sc);
   const float m = sc.m;
   const int32_t n = sc.n, got = FEW && n > r.top_k ? r.top_k : n;
   if (!(m > -kInf)) {
@@ -1163,7 +1200,7 @@ __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const
   uint64_t in_list;
   const uint64_t before = block_scan_u64<NT>(mine, &in_list, L.shu);
   // the others' sum is against another reference
-  const double below = FEW ? 0.0 : HOW == kDrawBinned ? sc.sum : __builtin_ldexp(sc.sum, bits);
+  const double below = FEW ? 0.0 : binned ? sc.sum : __builtin_ldexp(sc.sum, bits);
   const double to_m = below > 0.0 ? exp2_64(((double)sc.ref - (double)m) * c) : 0.0;
   const uint64_t sum = in_list + (uint64_t)__builtin_rint(below * to_m);
   const uint64_t most = r.top_p < 1.0 ? (uint64_t)__builtin_ceil(r.top_p * (double)sum) : ~uint64_t(0);
@@ -1190,13 +1227,14 @@ __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const
   __syncthreads();
   uint64_t W = across_waves<NT / 64>(L.shu, [](uint64_t u, uint64_t v) { return u > v ? u : v; });
   // is what is kept known: cut inside the list, or all of the row?
-  bool known = FEW || kept < got || in_list >= most || sum == in_list;
+  // (a min-p cut that is not deep is above the threshold)
+  bool known = FEW || kept < got || in_list >= most || sum == in_list || (r.min_p > 0.0 && !sc.deep);
   if (!known && r.top_p >= 1.0 && r.min_p == 0.0) {
     W = sum;
     known = true;
   }
   uint64_t last = 0;  // (below the list: the last place that is kept)
-  if (HOW == kDrawBinned && !known) {
+  if (binned && !known) {
     W = sum;
     if (most < sum) {
       const uint64_t target = (uint64_t)__builtin_ceil((double)(most - in_list) / to_m);
@@ -1228,7 +1266,7 @@ __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const
     }
     return true;
   }
-  if (HOW != kDrawBinned) return false;
+  if (!binned) return false;
   const uint64_t target = (uint64_t)__builtin_ceil((double)(over - in_list) / to_m);
   if (!search_bins<DT, NT>(xr, C, target, false, 0.0f, sc, c, bits, L)) return false;
   if (tid == 0) write_draw(a, i, r, m, L.found[0], W, bits);
@@ -1247,12 +1285,10 @@ __global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
       if (a.logp != nullptr) a.logp[i] = -kInf;
     }
   } else if (r.top_k <= GBDT_MAX_LISTED) {
-    if (sample_row<DT, NT, kDrawFew>(a, i, r, L)) return;
+    if (sample_row<DT, NT, true>(a, i, r, L)) return;
     if (threadIdx.x == 0) a.out[i] = kUnfinished;
   } else if (r.top_k >= a.C) {
-    if (r.min_p > 0.0 && sample_row<DT, NT, kDrawLikely>(a, i, r, L)) return;
-    __syncthreads();
-    if (sample_row<DT, NT, kDrawBinned>(a, i, r, L)) return;
+    if (sample_row<DT, NT, false>(a, i, r, L)) return;
     if (threadIdx.x == 0) a.out[i] = kUnfinished;
   } else if (threadIdx.x == 0) {
     a.out[i] = kUnfinished;
