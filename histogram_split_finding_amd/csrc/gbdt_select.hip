@@ -174,6 +174,19 @@ __device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float low
     }
     p1 = p1 > lo ? p1 : p2;
     uint64_t n = 0;  // three counts of 21 bits
+    if (NT == 64) {
+      // (one wave has no barriers to save: the middle alone)
+      int32_t n2 = 0;
+#pragma unroll
+      for (int j = 0; j < G; ++j) n2 += __popcll(__ballot(key[j] >= p2));
+      if (n2 >= k) {
+        lo = p2;
+        if (n2 <= k + k / 4 + 8) break;
+      } else {
+        hi = p2;
+      }
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       n += uint64_t(__popcll(__ballot(key[j] >= p1)));
@@ -214,7 +227,7 @@ __device__ uint32_t group_threshold(const float (&gm)[kVecs], float m, float low
 // a time, for all of the thread's own ones.
 template <int NT>
 __device__ inline void rank_list(ListLds<NT>& L, int32_t n) {
-  constexpr int PT = NT == 64 ? 4 : 1;
+  constexpr int PT = NT == 64 ? 4 : NT == 256 ? 2 : 1;
   const int tid = threadIdx.x;
   const int32_t n8 = (n + 7) & ~7;
   double* list = reinterpret_cast<double*>(L.list);
@@ -806,7 +819,7 @@ __global__ void __launch_bounds__(NT, kHotWaves<NT>) k_top_block(const TopArgs a
 }
 
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 4) k_top_rest(const TopArgs a) {
+__global__ void __launch_bounds__(NT, 2) k_top_rest(const TopArgs a) {
   using Elem = typename Score<DT>::Elem;
   constexpr int VE = Score<DT>::kVec;
   __shared__ SelLds<NT> L;
@@ -1298,7 +1311,7 @@ __global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
 // The rows that are left, by places: the top-k and top-p cuts, the min-p cut,
 // the draw.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 4) k_sample_rest(const SampleArgs a) {
+__global__ void __launch_bounds__(NT, 2) k_sample_rest(const SampleArgs a) {
   using Elem = typename Score<DT>::Elem;
   constexpr int NB = SelLds<NT>::kBins;
   __shared__ SelLds<NT> L;
@@ -1430,7 +1443,7 @@ void launch_top_block(TopArgs a, hipStream_t s) {
   // (a row of one block that fits the list is always finished)
   if (a.C <= ListLds<NT>::kList && a.C <= NT * kBlk<DT>) return;
   const dim3 rest((unsigned)(a.n < kRestGrid ? a.n : kRestGrid));
-  constexpr int RT = NT < 512 ? NT : 512;
+  constexpr int RT = NT < 256 ? NT : 256;
   hipLaunchKernelGGL((k_top_rest<DT, RT>), rest, dim3(RT), 0, s, a);
 }
 template <int DT, int R, int CMAX>
@@ -1438,6 +1451,12 @@ void launch_top_rows(const TopArgs& a, hipStream_t s) {
   const size_t lds = size_t(R) * 4 * ((a.C | 1) + 2 * (a.k | 1));
   hipLaunchKernelGGL((k_top_rows<DT, R, CMAX>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
 }
+
+// Threads for a row: a wave up to 2,048 classes, 256 up to 40,000 (draws of
+// 2,000 x 20,000 f32: 95 us with 256, 106 with 512), then 512 (records of
+// 2,048 x 131,072 bf16: 145 us with 512, 161 with 256, 229 with 1,024); at most
+// a row a CU: 1,024 (records of 32 such rows: 33 us, 38 with 512).
+constexpr int64_t kFewRows = 256;
 
 template <int DT>
 int launch_top(const TopArgs& a, hipStream_t s) {
@@ -1452,8 +1471,10 @@ int launch_top(const TopArgs& a, hipStream_t s) {
     launch_top_block<DT, 64>(a, s);
   else if (a.C <= 40000)
     launch_top_block<DT, 256>(a, s);
-  else
+  else if (a.n > kFewRows)
     launch_top_block<DT, 512>(a, s);
+  else
+    launch_top_block<DT, 1024>(a, s);
   diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_top");
@@ -1466,7 +1487,7 @@ void launch_sample_block(SampleArgs a, hipStream_t s) {
     hipLaunchKernelGGL((k_sample_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
   }
   const dim3 rest((unsigned)(a.n < kRestGrid ? a.n : kRestGrid));
-  constexpr int RT = NT < 512 ? NT : 512;
+  constexpr int RT = NT < 256 ? NT : 256;
   hipLaunchKernelGGL((k_sample_rest<DT, RT>), rest, dim3(RT), 0, s, a);
 }
 template <int DT, int R, int CMAX>
@@ -1488,8 +1509,10 @@ int launch_sample(const SampleArgs& a, hipStream_t s) {
     launch_sample_block<DT, 64>(a, s);
   else if (a.C <= 40000)
     launch_sample_block<DT, 256>(a, s);
-  else
+  else if (a.n > kFewRows)
     launch_sample_block<DT, 512>(a, s);
+  else
+    launch_sample_block<DT, 1024>(a, s);
   diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_sample");
