@@ -494,40 +494,52 @@ def _rows_2d(t, name, n=None, c=None):
     """(rows, columns, row stride) of a device tensor of contiguous rows."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError("%s must be a two-dimensional device tensor" % name)
-    r, w = int(t.shape[0]), int(t.shape[1])
+    r, w = t.shape
+    stride, inner = t.stride()
     if (n is not None and r != n) or (c is not None and w != c):
         raise ValueError("%s has shape %s, not (%s, %s)" % (name, tuple(t.shape), n, c))
-    if w > 1 and t.stride(1) != 1:
+    if w > 1 and inner != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    if r > 1 and t.stride(0) < w:
+    if r > 1 and stride < w:
         raise ValueError("%s has overlapping rows" % name)
-    return r, w, int(t.stride(0))
+    return r, w, stride
+
+
+_dtype_codes = None
 
 
 def _scores(x, name="scores") -> Scores:
-    import torch
-    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if x.dtype not in codes:
+    global _dtype_codes
+    if _dtype_codes is None:
+        import torch
+        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _dtype_codes.get(x.dtype)
+    if code is None:
         raise ValueError("%s must be float32, bfloat16 or float16" % name)
     n, c, stride = _rows_2d(x, name)
-    return Scores(_ptr(x), n, stride, c, codes[x.dtype])
+    return Scores(x.data_ptr(), n, stride, c, code)
 
 
 def _vector(t, name, dtype, shape, x, optional=False):
-    """Pointer of a contiguous tensor of the given type and shape on x's device."""
+    """Address of a contiguous tensor of the given type and shape on x's device."""
     if t is None and optional:
         return None
-    if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != x.device or \
-            not t.is_contiguous():
+    if t is None or t.dtype != dtype or t.shape != shape or t.device != x.device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on the scores' device"
                          % (name, dtype, tuple(shape)))
-    return _ptr(t)
+    return t.data_ptr()
 
 
-def _teacher(x, values, classes, rest) -> Teacher:
+def _workspace(ws, x):
+    """(address, bytes) of a workspace on the scores' device."""
+    if ws is None or ws.device != x.device or not ws.is_contiguous():
+        raise ValueError("ws must be a workspace from new_workspace() on the scores' device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _teacher(x, n, values, classes, rest) -> Teacher:
     import torch
-    k = int(values.shape[1]) if values.dim() == 2 else 0
-    n = int(x.shape[0])
+    k = values.shape[1] if values.dim() == 2 else 0
     return Teacher(_vector(values, "values", torch.float32, (n, k), x),
                    _vector(classes, "classes", torch.int32, (n, k), x),
                    _vector(rest, "rest", torch.float32, (n,), x, optional=True), k, 0)
@@ -536,7 +548,7 @@ def _teacher(x, values, classes, rest) -> Teacher:
 def _grad_rows(x, grad):
     if grad.dtype != x.dtype or grad.device != x.device:
         raise ValueError("grad must have the scores' type and device")
-    return _rows_2d(grad, "grad", int(x.shape[0]), int(x.shape[1]))[2]
+    return _rows_2d(grad, "grad", *x.shape)[2]
 
 
 def gbdt_top_scores(scores, k, temperature, values, classes, rest, ws, stream=None):
@@ -545,13 +557,14 @@ def gbdt_top_scores(scores, k, temperature, values, classes, rest, ws, stream=No
     the order of the scores (padded with -inf, -1), rest float32 [n] (or None),
     the mass outside the list at the temperature."""
     import torch
-    s = _scores(scores)
-    n, k = int(scores.shape[0]), int(k)
+    s, k = _scores(scores), int(k)
+    n = s.n_rows
+    wp, wb = _workspace(ws, scores)
     rc = load().gbdt_top_scores(ctypes.byref(s), k, float(temperature),
                                 _vector(values, "values", torch.float32, (n, k), scores),
                                 _vector(classes, "classes", torch.int32, (n, k), scores),
                                 _vector(rest, "rest", torch.float32, (n,), scores, optional=True),
-                                _ptr(ws), ws.numel(), _stream(stream))
+                                wp, wb, _stream(stream))
     _check(rc, "gbdt_top_scores")
 
 
@@ -560,12 +573,14 @@ def gbdt_distill_loss(scores, values, classes, rest, temperature, loss, stats, w
     float32 [n, k], classes int32 [n, k], rest float32 [n] or None): loss
     float32 [n], and stats float32 [n, 3] for gbdt_distill_grad."""
     import torch
-    s, t = _scores(scores), _teacher(scores, values, classes, rest)
-    n = int(scores.shape[0])
+    s = _scores(scores)
+    n = s.n_rows
+    t = _teacher(scores, n, values, classes, rest)
+    wp, wb = _workspace(ws, scores)
     rc = load().gbdt_distill_loss(ctypes.byref(s), ctypes.byref(t), float(temperature),
                                   _vector(loss, "loss", torch.float32, (n,), scores),
                                   _vector(stats, "stats", torch.float32, (n, 3), scores),
-                                  _ptr(ws), ws.numel(), _stream(stream))
+                                  wp, wb, _stream(stream))
     _check(rc, "gbdt_distill_loss")
 
 
@@ -573,26 +588,29 @@ def gbdt_distill_grad(scores, values, classes, rest, temperature, stats, weight,
     """Backward pass: grad (the scores' type and shape) = weight (float32 [n] or
     None) times each row's dloss/dscores, from gbdt_distill_loss's stats."""
     import torch
-    s, t = _scores(scores), _teacher(scores, values, classes, rest)
-    n = int(scores.shape[0])
+    s = _scores(scores)
+    n = s.n_rows
+    t = _teacher(scores, n, values, classes, rest)
+    wp, wb = _workspace(ws, scores)
     rc = load().gbdt_distill_grad(ctypes.byref(s), ctypes.byref(t), float(temperature),
                                   _vector(stats, "stats", torch.float32, (n, 3), scores),
                                   _vector(weight, "weight", torch.float32, (n,), scores, optional=True),
-                                  _ptr(grad), _grad_rows(scores, grad), _ptr(ws), ws.numel(),
-                                  _stream(stream))
+                                  grad.data_ptr(), _grad_rows(scores, grad), wp, wb, _stream(stream))
     _check(rc, "gbdt_distill_grad")
 
 
 def gbdt_distill_step(scores, values, classes, rest, temperature, weight, loss, grad, ws, stream=None):
     """Loss and gradient in one call: what gbdt_distill_loss and
-    gbdt_distill_grad give, from one read of the scores."""
+    gbdt_distill_grad give."""
     import torch
-    s, t = _scores(scores), _teacher(scores, values, classes, rest)
-    n = int(scores.shape[0])
+    s = _scores(scores)
+    n = s.n_rows
+    t = _teacher(scores, n, values, classes, rest)
+    wp, wb = _workspace(ws, scores)
     rc = load().gbdt_distill_step(ctypes.byref(s), ctypes.byref(t), float(temperature),
                                   _vector(weight, "weight", torch.float32, (n,), scores, optional=True),
-                                  _vector(loss, "loss", torch.float32, (n,), scores), _ptr(grad),
-                                  _grad_rows(scores, grad), _ptr(ws), ws.numel(), _stream(stream))
+                                  _vector(loss, "loss", torch.float32, (n,), scores), grad.data_ptr(),
+                                  _grad_rows(scores, grad), wp, wb, _stream(stream))
     _check(rc, "gbdt_distill_step")
 
 
@@ -603,16 +621,16 @@ def gbdt_sample_classes(scores, u, temperature, top_k, top_p, min_p, out, logp, 
     off): out int32 [n], logp float32 [n] (or None)."""
     import torch
     s = _scores(scores)
-    n = int(scores.shape[0])
-    f32 = torch.float32
-    p = Sampling(_vector(temperature, "temperature", f32, (n,), scores, optional=True),
-                 _vector(top_k, "top_k", torch.int32, (n,), scores, optional=True),
-                 _vector(top_p, "top_p", f32, (n,), scores, optional=True),
-                 _vector(min_p, "min_p", f32, (n,), scores, optional=True))
-    rc = load().gbdt_sample_classes(ctypes.byref(s), _vector(u, "u", f32, (n,), scores), ctypes.byref(p),
-                                    _vector(out, "out", torch.int32, (n,), scores),
-                                    _vector(logp, "logp", f32, (n,), scores, optional=True),
-                                    _ptr(ws), ws.numel(), _stream(stream))
+    n, f32 = (s.n_rows,), torch.float32
+    p = Sampling(_vector(temperature, "temperature", f32, n, scores, optional=True),
+                 _vector(top_k, "top_k", torch.int32, n, scores, optional=True),
+                 _vector(top_p, "top_p", f32, n, scores, optional=True),
+                 _vector(min_p, "min_p", f32, n, scores, optional=True))
+    wp, wb = _workspace(ws, scores)
+    rc = load().gbdt_sample_classes(ctypes.byref(s), _vector(u, "u", f32, n, scores), ctypes.byref(p),
+                                    _vector(out, "out", torch.int32, n, scores),
+                                    _vector(logp, "logp", f32, n, scores, optional=True),
+                                    wp, wb, _stream(stream))
     _check(rc, "gbdt_sample_classes")
 
 
