@@ -439,3 +439,101 @@ def test_device_side_checks(C):
         assert out[2].item() == -1 and np.isneginf(logp[2].item())
         for i in (0, 1, 3):
             assert out[i].item() == ref.sample(xh[i], 0.5, 1.0, 0, 1.0, 0.0)[0]
+
+
+# ------------------------------------------ rows that a first pass leaves over --
+
+def long_rows(C, seed):
+    """Rows whose first classes tell nothing, or the wrong thing, about the rest."""
+    r = np.random.default_rng(seed)
+    b = r.normal(0.0, 1.0, (10, C))
+    b[0] = np.sort(b[0])[::-1]             # the best first
+    b[1] = np.sort(b[1])                   # the best last
+    b[2, : C // 2] = -np.inf               # the first half masked
+    b[3, C // 2:] = -np.inf                # the second half masked
+    b[4, : C // 2] -= 30.0                 # the first half hopeless
+    b[5] = np.round(b[5] * 2.0) / 2.0      # a few values, each many times
+    b[6] *= 0.01                           # narrow: everything is likely
+    b[7] = 0.0                             # equal, but for a few at the end
+    b[7, C - 3:] = [1.0, 2.0, 1.0]
+    b[8, : C - 2] = -np.inf                # two left
+    b[9] *= 4.0                            # wide
+    return b
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [2500, 20011, 70001])
+def test_long_odd_rows(C, dtype):
+    say("long odd rows: C=%d %s" % (C, dtype))
+    t = torch.from_numpy(long_rows(C, C)).to(ref.TYPES[dtype])
+    x, xh = ref.place(t, 3), t.double().numpy()
+    n = x.shape[0]
+    for k in (1, 50, 256):
+        check_top(x, xh, k, 1.0)
+    tv, tc, tr = ref.records(xh, 40, C, 1.0)
+    check_distill(x, xh, tv, tc, tr, 1.0, None, dtype, pad=1)
+    f = np.float32
+    q = sampling_params(n, C, C)
+    for name, kw in [("plain", {}), ("p", dict(p=q["p"])), ("deep p", dict(p=np.full(n, 0.9995, dtype=f))),
+                     ("min_p", dict(mp=q["mp"])), ("deep min_p", dict(mp=np.full(n, 1e-4, dtype=f))),
+                     ("p, min_p", dict(p=q["p"], mp=np.full(n, 1e-3, dtype=f))),
+                     ("k", dict(k=np.full(n, 256, dtype=np.int32))),
+                     ("large k", dict(k=np.full(n, 257, dtype=np.int32), p=q["p"], mp=np.full(n, 1e-3, dtype=f))),
+                     ("cold", dict(T=np.full(n, 0.02, dtype=f))), ("hot", dict(T=np.full(n, 50.0, dtype=f)))]:
+        say(name)
+        check_sample(x, xh, q["u"], **kw)
+
+
+@pytest.mark.parametrize("n,C", [(300, 40960), (140, 66001)])
+def test_more_rows_than_workgroups_share(n, C):
+    """As many long rows as keep a workgroup each, on both sides of the row
+    counts that are split or take more threads."""
+    say("long rows: %d x %d" % (n, C))
+    x, xh = ref.rows(n, C, "bf16", C)
+    check_top(x, xh, 20, 2.0)
+    q = sampling_params(n, C, n)
+    check_sample(x, xh, q["u"], T=q["T"], p=q["p"], mp=q["mp"] * 0.01)
+    check_sample(x, xh, q["u"], k=q["k"])
+    tv, tc, tr = ref.records(xh, 20, C, 2.0)
+    check_distill(x, xh, tv, tc, tr, 2.0, None, "bf16")
+
+
+@pytest.mark.parametrize("C", [7, 500])
+def test_top_without_rest(C):
+    x, xh = ref.rows(9, C, "f16", C)
+    v, c = torch.zeros(9, 4, device=DEV), torch.zeros(9, 4, dtype=torch.int32, device=DEV)
+    ws = workspace(x)
+    g.gbdt_top_scores(x, 4, 1.0, v, c, None, ws)
+    for i in range(9):
+        wv, wc, _ = ref.top_scores(xh[i], 4, 1.0)
+        assert np.array_equal(c[i].cpu().numpy(), wc) and np.array_equal(v[i].cpu().numpy(), wv.astype(np.float32))
+
+
+@pytest.mark.parametrize("C", [9, 40, 3000, 50000])
+def test_sample_frequencies(C):
+    """Draws with evenly spread u: each class as often as its probability says,
+    to within one draw at either end of its interval."""
+    n = 4096
+    say("frequencies: C=%d" % C)
+    row = torch.zeros(C, dtype=torch.float64)
+    row[: min(C, 9)] = torch.arange(min(C, 9), dtype=torch.float64) * 0.5 + 6.0
+    x = row.float().to(DEV).expand(n, C).contiguous()
+    u = ((torch.arange(n, dtype=torch.float64) + 0.5) / n).float()
+    out, _ = run_sample(x, u.numpy(), None, None, None, None)
+    p = torch.softmax(row, 0).numpy()
+    for c in range(min(C, 9)):
+        assert abs(int((out == c).sum()) - n * p[c]) <= 2.0, c
+
+
+def test_example():
+    """Records, loss, gradient and draws as they are used together."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "distill_classes.py")
+    spec = importlib.util.spec_from_file_location("distill_classes", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses, agree = m.run(rows=2000, steps=40)
+    assert losses[-1] < 0.5 * losses[0] and all(b <= a for a, b in zip(losses, losses[1:]))
+    # (a draw from seven classes without learning would agree in one of seven)
+    assert agree > 2.0 / 7.0
