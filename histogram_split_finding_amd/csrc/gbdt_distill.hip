@@ -224,26 +224,35 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
 // block is one word (or half of one).  Thread j of the first k owns entry j
 // (and j + NT, ...) of the record; its class's gradient replaces, behind a
 // barrier, what the vector stores left there.
+//
+// With fewer than 64 threads a row, a wave holds several rows (the last one's
+// spare threads do the last row again).
+constexpr int kNarrowThreads = 16, kNarrowClasses = 256, kNarrowListed = 64;
+
 template <int DT, int NT, int MODE>
-__global__ void __launch_bounds__(NT, NT == 64 ? 6 : 8) k_distill_block(const DistillArgs a) {
+__global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill_block(const DistillArgs a) {
   using Elem = typename Score<DT>::Elem;
-  constexpr int VE = Score<DT>::kVec, BLK = kBlk<DT>, W = NT / 64;
-  constexpr int KPT = (GBDT_MAX_LISTED + NT - 1) / NT;
+  constexpr int VE = Score<DT>::kVec, BLK = kBlk<DT>, W = NT < 64 ? 1 : NT / 64;
+  constexpr int KPT = NT < 64 ? kNarrowListed / NT : (GBDT_MAX_LISTED + NT - 1) / NT;
   constexpr bool kSums = (MODE & kStats) && !(MODE & kJoin);
-  extern __shared__ uint32_t bits[];
+  extern __shared__ uint32_t all_bits[];
   __shared__ float sh_m[W], sh_t[W];
   __shared__ double sh_d[4][W];
-  const int tid = threadIdx.x, wid = tid >> 6;
+  const int tid = threadIdx.x & (NT - 1), wid = threadIdx.x >> 6;
+  const int sub = NT < 64 ? threadIdx.x / NT : 0;  // the row's place in the wave
   const float cf = exponent_scale(a.c);
   const uint32_t in_launch = a.n_parts > 1 ? blockIdx.x / (uint32_t)a.n_parts : blockIdx.x;
   const int32_t part = (int32_t)(blockIdx.x - in_launch * (uint32_t)a.n_parts);
-  const int64_t i = a.row0 + in_launch;
+  const int64_t i_all = NT < 64 ? a.row0 + int64_t(in_launch) * (64 / NT) + sub : a.row0 + in_launch;
+  const int64_t i = NT < 64 && i_all >= a.n ? a.n - 1 : i_all;
   const int32_t lo = part * a.part_len;
   const int32_t hi = a.C - lo < a.part_len ? a.C : lo + a.part_len;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
   RawBlock<DT> raw;
   if (kSums) raw = load_block<DT, NT>(xr, lo, hi);
-  for (int32_t w = tid; w < ((hi - lo + NT * BLK - 1) / (NT * BLK) * BLK + 31) / 32 * NT; w += NT) bits[w] = 0u;
+  const int32_t words = ((hi - lo + NT * BLK - 1) / (NT * BLK) * BLK + 31) / 32 * NT;
+  uint32_t* __restrict__ bits = all_bits + sub * words;
+  for (int32_t w = tid; w < words; w += NT) bits[w] = 0u;
   int32_t cls[KPT];
   float t[KPT], xj[KPT];
 #pragma unroll
@@ -320,19 +329,23 @@ __global__ void __launch_bounds__(NT, NT == 64 ? 6 : 8) k_distill_block(const Di
     m = a.stats_in[3 * i];
   }
   // the row's maxima; NaN in the record counts as an entry
-  m = wave_max(m);
-  tm = wave_max(tm);
-  if ((tid & 63) == 0) {
-    sh_m[wid] = m;
-    sh_t[wid] = tm;
+  m = group_max<NT>(m);
+  tm = group_max<NT>(tm);
+  if (NT <= 64) {
+    has = (__ballot(has) >> (sub * NT) & (~uint64_t(0) >> (64 - (NT < 64 ? NT : 64)))) != 0;
+  } else {
+    if ((tid & 63) == 0) {
+      sh_m[wid] = m;
+      sh_t[wid] = tm;
+    }
+    has = __syncthreads_or(has);
+    m = across_waves<W>(sh_m, [](float u, float v) { return __builtin_fmaxf(u, v); });
+    tm = across_waves<W>(sh_t, [](float u, float v) { return __builtin_fmaxf(u, v); });
   }
-  has = __syncthreads_or(has);
-  m = across_waves<W>(sh_m, [](float u, float v) { return __builtin_fmaxf(u, v); });
-  tm = across_waves<W>(sh_t, [](float u, float v) { return __builtin_fmaxf(u, v); });
   const double ms = m == -kInf ? 0.0 : (double)m;
   const double ts = tm == -kInf ? 0.0 : (double)tm;
   if ((MODE & kStats) && ref != m) so *= exp2_64(((double)ref - ms) * a.c);
-  if (MODE & kPart) {
+  if constexpr ((MODE & kPart) != 0) {
     so = block_sum<NT>(so, sh_d[0]);
     if (tid == 0) a.parts[i * a.n_parts + part] = PartSum{so, m, 0u};
     return;
@@ -350,12 +363,14 @@ __global__ void __launch_bounds__(NT, NT == 64 ? 6 : 8) k_distill_block(const Di
   double sum[4] = {z, kd, si, so};
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
-    sum[v] = wave_sum(sum[v]);
-    if ((tid & 63) == 0) sh_d[v][wid] = sum[v];
+    sum[v] = group_sum<NT>(sum[v]);
+    if (NT > 64 && (tid & 63) == 0) sh_d[v][wid] = sum[v];
   }
-  __syncthreads();
+  if (NT > 64) {
+    __syncthreads();
 #pragma unroll
-  for (int v = 0; v < 4; ++v) sum[v] = across_waves<W>(sh_d[v], [](double p, double q) { return p + q; });
+    for (int v = 0; v < 4; ++v) sum[v] = across_waves<W>(sh_d[v], [](double p, double q) { return p + q; });
+  }
   z = sum[0];
   kd = sum[1];
   double s_in = sum[2], s_out = sum[3];
@@ -422,10 +437,12 @@ template <int DT, int NT, int MODE>
 void launch_block(DistillArgs a, hipStream_t s) {
   constexpr int32_t kStep = NT * kBlk<DT>;
   if (a.n_parts == 1) a.part_len = (a.C + kStep - 1) / kStep * kStep;
-  const size_t lds = size_t((a.part_len / kStep * kBlk<DT> + 31) / 32) * NT * 4;
+  constexpr int kRows = NT < 64 ? 64 / NT : 1;  // of a workgroup
+  const size_t lds = size_t((a.part_len / kStep * kBlk<DT> + 31) / 32) * NT * 4 * kRows;
   for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
-    hipLaunchKernelGGL((k_distill_block<DT, NT, MODE>), dim3((unsigned)(n * a.n_parts)), dim3(NT), lds, s, a);
+    hipLaunchKernelGGL((k_distill_block<DT, NT, MODE>), dim3((unsigned)((n + kRows - 1) / kRows * a.n_parts)),
+                       dim3(kRows * NT), lds, s, a);
   }
 }
 
@@ -466,6 +483,8 @@ int launch_distill(const DistillArgs& args, hipStream_t s) {
     } else {
       launch_block<DT, 256, MODE>(a, s);
     }
+  } else if (a.C <= kNarrowClasses && a.k <= kNarrowListed) {
+    launch_block<DT, kNarrowThreads, MODE>(a, s);
   } else if (a.C <= 2048) {
     launch_block<DT, 64, MODE>(a, s);
   } else if (a.C <= 40000) {

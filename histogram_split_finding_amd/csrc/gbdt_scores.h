@@ -217,6 +217,20 @@ __device__ __forceinline__ float wave_min(float v) {
   return v;
 }
 
+// The same within groups of NT lanes (NT <= 64).
+template <int NT>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int off = (NT < 64 ? NT : 64) / 2; off > 0; off >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ double group_sum(double v) {
+#pragma unroll
+  for (int off = (NT < 64 ? NT : 64) / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
 // The waves' values sh[W] combined, in every lane (behind a barrier).
 template <int W, typename T, typename F>
 __device__ __forceinline__ T across_waves(const T* sh, F f) {
@@ -269,7 +283,7 @@ __device__ __forceinline__ RawBlock<DT> load_block(const typename Score<DT>::Ele
                                                    int32_t C) {
   constexpr int VE = Score<DT>::kVec;
   RawBlock<DT> r;
-  const int32_t c0 = base + (int32_t)threadIdx.x * VE;
+  const int32_t c0 = base + (int32_t)(threadIdx.x & (NT - 1)) * VE;
   if (base + NT * kBlk<DT> <= C) {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) r.v[j] = load_vec<DT>(row + c0 + j * NT * VE);
@@ -304,7 +318,7 @@ __device__ __forceinline__ void store_block(typename Score<DT>::Elem* __restrict
                                             const RawBlock<DT>& r) {
   constexpr int VE = Score<DT>::kVec;
   using Words = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
-  const int32_t c0 = base + (int32_t)threadIdx.x * VE;
+  const int32_t c0 = base + (int32_t)(threadIdx.x & (NT - 1)) * VE;
   if (base + NT * kBlk<DT> <= C) {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {

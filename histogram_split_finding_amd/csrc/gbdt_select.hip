@@ -860,6 +860,8 @@ __global__ void __launch_bounds__(NT, 2) k_top_rest(const TopArgs a) {
   });
 }
 
+constexpr int kSortedClasses = 64;  // rows of at most this many: one thread each
+
 // A row of at most CMAX classes in one thread: its places sorted in registers
 // (Batcher's odd-even merge network, largest first).  A place is a positive
 // FP64 number here, key and class in its last 56 bits: its order is the
@@ -1369,7 +1371,7 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rest(const SampleArgs a) {
 
 // One thread per row of at most CMAX classes, R rows a workgroup.
 template <int DT, int R, int CMAX>
-__global__ void __launch_bounds__(R, CMAX == 8 ? 6 : 3) k_sample_rows(const SampleArgs a) {
+__global__ void __launch_bounds__(R, CMAX == 8 ? 6 : CMAX <= 32 ? 3 : 1) k_sample_rows(const SampleArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x;
   const int64_t i0 = int64_t(blockIdx.x) * R, i = i0 + tid;
@@ -1465,8 +1467,10 @@ int launch_top(const TopArgs& a, hipStream_t s) {
     launch_top_rows<DT, 256, 8>(a, s);
   else if (a.C <= 16)
     launch_top_rows<DT, 128, 16>(a, s);
-  else if (a.C <= kRowsMaxClasses)
+  else if (a.C <= 32)
     launch_top_rows<DT, 64, 32>(a, s);
+  else if (a.C <= kSortedClasses)
+    launch_top_rows<DT, 64, kSortedClasses>(a, s);
   else if (a.C <= 2048)
     launch_top_block<DT, 64>(a, s);
   else if (a.C <= 40000)
@@ -1503,8 +1507,10 @@ int launch_sample(const SampleArgs& a, hipStream_t s) {
     launch_sample_rows<DT, 256, 8>(a, s);
   else if (a.C <= 16)
     launch_sample_rows<DT, 128, 16>(a, s);
-  else if (a.C <= kRowsMaxClasses)
+  else if (a.C <= 32)
     launch_sample_rows<DT, 64, 32>(a, s);
+  else if (a.C <= kSortedClasses)
+    launch_sample_rows<DT, 64, kSortedClasses>(a, s);
   else if (a.C <= 2048)
     launch_sample_block<DT, 64>(a, s);
   else if (a.C <= 40000)
