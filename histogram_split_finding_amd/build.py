@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,12 +33,23 @@ FLAGS = [
 
 
 def build(verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    """Compiles the sources side by side, then links them."""
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [HIPCC] + FLAGS + srcs + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory() as objects:
+        jobs, outs = [], []
+        for src in SOURCES:
+            out = os.path.join(objects, src + ".o")
+            cmd = [HIPCC] + [f for f in FLAGS if f != "-shared"] + ["-c", os.path.join(CSRC, src), "-o", out]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append((cmd, subprocess.Popen(cmd)))
+            outs.append(out)
+        for cmd, job in jobs:
+            if job.wait() != 0:
+                for _, other in jobs:
+                    other.wait()
+                raise subprocess.CalledProcessError(job.returncode, cmd)
+        subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC"] + outs + ["-o", tmp], check=True)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

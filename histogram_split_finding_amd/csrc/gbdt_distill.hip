@@ -89,7 +89,8 @@ __device__ __forceinline__ double row_loss(double T, double inv_T, double r, dou
 // in flight at once: the rows are few microseconds in all, one memory latency
 // each way.  The exponentials that the loss needs are in FP64 (a row's few
 // terms do not average rounding errors away, and a small loss is what is left
-// when terms of order 1 cancel).
+// when terms of order 1 cancel).  Vector instructions bound it, about 870 a row
+// of seven classes: step of 581,012 rows 22 us, 12 without its arithmetic.
 template <int DT, int R, int CMAX, int MODE>
 __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const DistillArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -217,6 +218,10 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
 // NT * kBlk) of a row that n_parts workgroups share; a first launch (kPart)
 // leaves each part's sums, a second (kJoin) adds them up.
 //
+// Memory bounds it where rows are many: step of 4,096 x 131,072 bf16 442 us
+// (4.9 TB/s of what has to move; the second read of the scores comes from the
+// last-level cache), gradient of 2,048 x 50,001 f32 152 us (5.4 TB/s).
+//
 // One pass takes the sum against a reference that is the first maximum the
 // thread meets and moves only when a score is above it by 2^20 in the
 // exponential, so a vector costs no rescaling; the second writes the gradient.
@@ -226,7 +231,8 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
 // barrier, what the vector stores left there.
 //
 // With fewer than 64 threads a row, a wave holds several rows (the last one's
-// spare threads do the last row again).
+// spare threads do the last row again): step of 300,000 rows of 100 bf16 148
+// us, 511 with a wave each.
 constexpr int kNarrowThreads = 16, kNarrowClasses = 256, kNarrowListed = 64;
 
 template <int DT, int NT, int MODE>

@@ -778,7 +778,10 @@ struct TopArgs {
   int64_t row0;  // of this launch
 };
 
-// One workgroup per row.
+// One workgroup per row.  A long row's time is its read (2,048 x 131,072 bf16:
+// 131 us, 4.1 TB/s; the FP32 exponentials alone would take 58); the threshold,
+// the ranking and the workgroup's reductions are 5 to 8 us a row, which the
+// CU's other two workgroups cover in part.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, kHotWaves<NT>) k_top_block(const TopArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -860,7 +863,9 @@ __global__ void __launch_bounds__(NT, 2) k_top_rest(const TopArgs a) {
   });
 }
 
-constexpr int kSortedClasses = 64;  // rows of at most this many: one thread each
+// Rows of at most this many classes: one thread each (300,000 rows of 100
+// classes: records 455 us, 720 with a wave a row; draws 640 and 1,134).
+constexpr int kSortedClasses = 128;
 
 // A row of at most CMAX classes in one thread: its places sorted in registers
 // (Batcher's odd-even merge network, largest first).  A place is a positive
@@ -910,6 +915,8 @@ __device__ __forceinline__ void stage_scores(const void* x, int64_t i0, int32_t 
   xs.put(rows, C, by_c, lds);
 }
 
+// One thread per row, R rows a workgroup (581,012 rows of 7 f32, k = 3: 11 us,
+// 2.9 TB/s; without the staging through LDS 27 us).
 template <int DT, int R, int CMAX>
 __global__ void __launch_bounds__(R) k_top_rows(const TopArgs a) {
   extern __shared__ float lds[];
@@ -1288,6 +1295,10 @@ __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const
   return true;
 }
 
+// FP64 bounds draws without top-k: 20 instructions a class, 57 us of 195 for
+// 1,024 x 100,003 bf16 with top-p and min-p; the rest is the row's latencies
+// (threshold, ranking, cuts: 20 us) with two workgroups a CU.  Four waves a
+// SIMD: with six the pass spills (330 us).
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
   __shared__ SelLds<NT> L;
@@ -1369,7 +1380,8 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rest(const SampleArgs a) {
   });
 }
 
-// One thread per row of at most CMAX classes, R rows a workgroup.
+// One thread per row of at most CMAX classes, R rows a workgroup (581,012 rows
+// of 7 f32, all filters: 16 us; vector instructions, half of them FP64).
 template <int DT, int R, int CMAX>
 __global__ void __launch_bounds__(R, CMAX == 8 ? 6 : CMAX <= 32 ? 3 : 1) k_sample_rows(const SampleArgs a) {
   extern __shared__ float lds[];
@@ -1394,27 +1406,34 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 6 : CMAX <= 32 ? 3 : 1) k_sampl
   }
   const bool inf = m == kInf;
   const double ms = (double)m, c_T = r.T > 0.0 ? kLog2e / r.T : 0.0;
-  double e[CMAX], all = 1.0;  // (the first one's e is 1)
-  e[0] = 1.0;
+  // (the first one's e is 1; longer rows have no registers for the others')
+  constexpr int kHeld = CMAX <= 64 ? CMAX : 1;
+  double held[kHeld], all = 1.0;
+  auto weight = [&](int c) {
+    const float v = short_score(p[c]);
+    const double x = inf ? (v == kInf ? 1.0 : 0.0) : exp2_64(((double)v - ms) * c_T);
+    return c < r.top_k && v > -kInf ? x : 0.0;
+  };
 #pragma unroll
   for (int c = 1; c < CMAX; ++c) {
-    e[c] = 0.0;
     if (c < C) {
-      const float v = short_score(p[c]);
-      const double x = inf ? (v == kInf ? 1.0 : 0.0) : exp2_64(((double)v - ms) * c_T);
-      e[c] = c < r.top_k && v > -kInf ? x : 0.0;
-      all += e[c];
+      const double e = weight(c);
+      if (kHeld > 1) held[c % kHeld] = e;
+      all += e;
     }
   }
   const double most = r.top_p < 1.0 ? r.top_p * all : kInf;
   double run = 1.0, W = 1.0;
+  int32_t n_kept = 1;
 #pragma unroll
   for (int c = 1; c < CMAX; ++c) {
     if (c < C) {
-      const bool kept = run < most && e[c] >= r.min_p && e[c] > 0.0;
-      run += e[c];
-      e[c] = kept ? e[c] : 0.0;
-      W += e[c];
+      const double e = kHeld > 1 ? held[c % kHeld] : weight(c);
+      if (run < most && e >= r.min_p && e > 0.0) {
+        W += e;
+        n_kept = c + 1;
+      }
+      run += e;
     }
   }
   const double over = r.u * W;
@@ -1424,11 +1443,12 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 6 : CMAX <= 32 ? 3 : 1) k_sampl
 #pragma unroll
   for (int c = 1; c < CMAX; ++c) {
     if (c < C) {
-      run += e[c];
+      const double e = kHeld > 1 ? held[c % kHeld] : weight(c);
       // (the last kept one where rounding leaves none)
-      const bool take = !found && e[c] > 0.0;
+      run += e;
+      const bool take = !found && c < n_kept;
       place = take ? p[c] : place;
-      ew = take ? e[c] : ew;
+      ew = take ? e : ew;
       found = found || (take && run > over);
     }
   }
@@ -1469,8 +1489,10 @@ int launch_top(const TopArgs& a, hipStream_t s) {
     launch_top_rows<DT, 128, 16>(a, s);
   else if (a.C <= 32)
     launch_top_rows<DT, 64, 32>(a, s);
+  else if (a.C <= 64)
+    launch_top_rows<DT, 64, 64>(a, s);
   else if (a.C <= kSortedClasses)
-    launch_top_rows<DT, 64, kSortedClasses>(a, s);
+    launch_top_rows<DT, 64, 128>(a, s);
   else if (a.C <= 2048)
     launch_top_block<DT, 64>(a, s);
   else if (a.C <= 40000)
@@ -1509,8 +1531,10 @@ int launch_sample(const SampleArgs& a, hipStream_t s) {
     launch_sample_rows<DT, 128, 16>(a, s);
   else if (a.C <= 32)
     launch_sample_rows<DT, 64, 32>(a, s);
+  else if (a.C <= 64)
+    launch_sample_rows<DT, 64, 64>(a, s);
   else if (a.C <= kSortedClasses)
-    launch_sample_rows<DT, 64, kSortedClasses>(a, s);
+    launch_sample_rows<DT, 64, 128>(a, s);
   else if (a.C <= 2048)
     launch_sample_block<DT, 64>(a, s);
   else if (a.C <= 40000)

@@ -708,7 +708,8 @@ typedef struct gbdt_teacher {
 } gbdt_teacher;
 
 /* Workspace bytes of every call of this section for n_rows x n_classes scores
- * (0 if a size is out of range). */
+ * (0 if a size is out of range).  Zero-filled before its first use; it serves
+ * one call at a time (calls on one stream may share it). */
 size_t gbdt_scores_workspace_bytes(int64_t n_rows, int32_t n_classes);
 
 /*
@@ -742,8 +743,8 @@ int gbdt_top_scores(const gbdt_scores* x /* host */, int32_t k, float temperatur
  *
  * gbdt_distill_loss also writes stats[n_rows][3] = (max x, sum of
  * exp((x_c - max x) / T) in S, the same outside S), which gbdt_distill_grad
- * reads: the forward and the backward pass.  gbdt_distill_step does both and
- * reads the scores once.  weight: [n_rows] or NULL (ones).  grad: the scores'
+ * reads: the forward and the backward pass.  gbdt_distill_step does both in
+ * one call and writes no statistics.  weight: [n_rows] or NULL (ones).  grad: the scores'
  * type, rows grad_stride elements apart; it must not overlap the scores.
  */
 int gbdt_distill_loss(const gbdt_scores* x /* host */, const gbdt_teacher* t /* host */,
@@ -764,7 +765,8 @@ int gbdt_distill_step(const gbdt_scores* x /* host */, const gbdt_teacher* t /* 
  * the ones with e_c >= min_p.  The drawn class is the first of the kept ones,
  * in the order, whose running e sum exceeds u times the sum over all kept ones.
  * T = 0 draws the first class of the order.  Sums and comparisons are carried
- * in 64 bits (fixed point, so they do not depend on the order of addition).
+ * in 64 bits (where the hardware chooses the order of additions, in fixed
+ * point: the same inputs give the same classes).
  * out[n_rows]: the class, or -1 for a row without a score above -inf;
  * logp[n_rows] (or NULL): log(e_c / sum over the kept ones), -inf with -1.  A score of +inf
  * has e = 1 and leaves all finite ones e = 0.

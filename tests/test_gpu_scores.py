@@ -21,7 +21,7 @@ from gpu_util import DEV, say
 
 pytestmark = pytest.mark.gpu
 
-SIZES = [1, 2, 7, 8, 9, 16, 17, 32, 33, 63, 100, 257, 1000, 4099, 8192, 8193, 20011, 70001]
+SIZES = [1, 2, 7, 8, 9, 16, 17, 32, 33, 63, 64, 65, 100, 128, 129, 257, 1000, 4099, 8192, 8193, 20011, 70001]
 
 
 def rel(x, T):
