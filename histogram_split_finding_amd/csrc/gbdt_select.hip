@@ -43,7 +43,6 @@ constexpr uint32_t kKeyNegInf = 0x007fffffu;
 // Order-preserving key of a score: larger for a larger score, the same for -0
 // and +0, that of -inf for NaN.
 __device__ __forceinline__ float canon(float x) { return x == x ? x + 0.0f : -kInf; }
-__device__ __forceinline__ float canon_max(float x) { return __builtin_fmaxf(x, -kInf); }  // (-0 stays)
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
   return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
@@ -406,7 +405,8 @@ __device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __re
       }
       if (SUM == kSum32) {
 #pragma unroll
-        for (int q = 0; q < VE; ++q) f[q] = exp2_32((canon_max(f[q]) - s.ref) * cf);
+        // (NaN, as -inf, has no mass)
+        for (int q = 0; q < VE; ++q) f[q] = exp2_32(__builtin_fmaxf((f[q] - s.ref) * cf, -200.0f));
         sum += (double)sum_of(f);
       }
       if (SUM == kSum64) {
