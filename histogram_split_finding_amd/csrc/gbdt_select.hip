@@ -113,7 +113,11 @@ struct ListLds {
   uint64_t found[4];
   float shf[2][16];
   int32_t sh32[32];
-  uint32_t n_list, kmin, kmax;
+  uint32_t n_list, kmin, kmax, n_vec;
+  // vectors with a class that reaches the threshold, and where they begin
+  static constexpr int kVectors = NT > 256 ? kList : 1;
+  alignas(16) uint32_t vec[4 * kVectors];
+  int32_t vec_at[kVectors];
 };
 template <int NT>
 struct SelLds : ListLds<NT> {
@@ -320,7 +324,10 @@ __device__ __forceinline__ Scan scan_begin(const typename Score<DT>::Elem* __res
     L.shf[0][tid >> 6] = hi;
     L.shf[1][tid >> 6] = lo;
   }
-  if (tid == 0) L.n_list = 0u;
+  if (tid == 0) {
+    L.n_list = 0u;
+    L.n_vec = 0u;
+  }
   if (BINS) {
     least = wave_min(least);
     if ((tid & 63) == 0) L.shd[tid >> 6] = (double)least;
@@ -381,6 +388,51 @@ __device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __re
   uint64_t sum_q = 0;
   const double magic = __builtin_ldexp(1.0, 52 - bits), low = -(double)(bits + 2);
   const uint64_t zero = uint64_t(__double_as_longlong(magic));
+  // the elements that reach the threshold into the list, leaving -inf
+  auto list_vector = [&](float (&f)[VE], int32_t c0) {
+#pragma unroll
+    for (int q = 0; q < VE; ++q) {
+      if (f[q] >= thr) {
+        const uint32_t at = atomicAdd(&L.n_list, 1u);
+        if (at < (uint32_t)NL) L.list[at] = place_of(f[q] + 0.0f, c0 + q);
+        f[q] = -kInf;
+      }
+    }
+  };
+  auto add = [&](float (&f)[VE]) {
+    if (SUM == kSum32) {
+#pragma unroll
+      // (NaN, as -inf, has no mass)
+      for (int q = 0; q < VE; ++q) f[q] = exp2_32(__builtin_fmaxf((f[q] - s.ref) * cf, -200.0f));
+      sum += (double)sum_of(f);
+    }
+    if (SUM == kSum64) {
+      // four at a time: enough to cover an addition's latency, in few registers
+#pragma unroll
+      for (int h = 0; h < VE; h += 4) {
+#pragma unroll
+        for (int q = h; q < h + 4; ++q)
+          sum += exp2_64_near(__builtin_fmax(((double)f[q] - ref) * cd, -1000.0));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if constexpr (SUM == kBinned) {
+      const double scale = (double)Lds::kBins / (s.bins_low > low ? s.bins_low : low);
+#pragma unroll
+      for (int h = 0; h < VE; h += 4) {
+#pragma unroll
+        for (int q = h; q < h + 4; ++q) {
+          const double y = __builtin_fmax(((double)f[q] - ref) * cd, low);
+          const uint64_t w = uint64_t(__double_as_longlong(exp2_64_near(y) + magic)) - zero;
+          sum_q += w;
+          if (w != 0)
+            atomicAdd(reinterpret_cast<unsigned long long*>(&L.hist[bin_of_exponent<Lds::kBins>(y, scale)]),
+                      (unsigned long long)w);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
   for (int32_t base = 0;;) {
     // the next block is on its way while this one is worked on
     RawBlock<DT> next;
@@ -394,52 +446,44 @@ __device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __re
       const float vm = max_of(f);
       m = __builtin_fmaxf(m, vm);
       if (vm >= thr) {
-#pragma unroll
-        for (int q = 0; q < VE; ++q) {
-          if (f[q] >= thr) {
-            const uint32_t at = atomicAdd(&L.n_list, 1u);
-            if (at < (uint32_t)NL) L.list[at] = place_of(f[q] + 0.0f, base + (j * NT + tid) * VE + q);
-            f[q] = -kInf;
+        // a wave meets such a vector every other time: what it does here has to
+        // be little, so its elements wait (with up to 256 threads a row the LDS
+        // for that would cost workgroups)
+        const int32_t c0 = base + (j * NT + tid) * VE;
+        if constexpr (NT > 256) {
+          const uint32_t at = atomicAdd(&L.n_vec, 1u);
+          if (at < (uint32_t)Lds::kVectors) {
+            __builtin_memcpy(&L.vec[4 * at], &raw.v[j], 16);
+            L.vec_at[at] = c0;
           }
+#pragma unroll
+          for (int q = 0; q < VE; ++q) f[q] = -kInf;
+        } else {
+          list_vector(f, c0);
         }
       }
-      if (SUM == kSum32) {
-#pragma unroll
-        // (NaN, as -inf, has no mass)
-        for (int q = 0; q < VE; ++q) f[q] = exp2_32(__builtin_fmaxf((f[q] - s.ref) * cf, -200.0f));
-        sum += (double)sum_of(f);
-      }
-      if (SUM == kSum64) {
-        // four at a time: enough to cover an addition's latency, in few registers
-#pragma unroll
-        for (int h = 0; h < VE; h += 4) {
-#pragma unroll
-          for (int q = h; q < h + 4; ++q)
-            sum += exp2_64_near(__builtin_fmax(((double)f[q] - ref) * cd, -1000.0));
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      if constexpr (SUM == kBinned) {
-        const double scale = (double)Lds::kBins / (s.bins_low > low ? s.bins_low : low);
-#pragma unroll
-        for (int h = 0; h < VE; h += 4) {
-#pragma unroll
-          for (int q = h; q < h + 4; ++q) {
-            const double y = __builtin_fmax(((double)f[q] - ref) * cd, low);
-            const uint64_t w = uint64_t(__double_as_longlong(exp2_64_near(y) + magic)) - zero;
-            sum_q += w;
-            if (w != 0)
-              atomicAdd(reinterpret_cast<unsigned long long*>(&L.hist[bin_of_exponent<Lds::kBins>(y, scale)]),
-                        (unsigned long long)w);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+      add(f);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (!more) break;
     base += STEP;
     raw = next;
+  }
+  if constexpr (NT > 256) {
+    __syncthreads();
+    const int32_t n_vec = (int32_t)L.n_vec;
+    if (n_vec > Lds::kVectors) {
+      if (tid == 0) L.n_list = NL + 1;
+    } else {
+      for (int32_t v = tid; v < n_vec; v += NT) {
+        Vec16<DT> e;
+        __builtin_memcpy(&e, &L.vec[4 * v], 16);
+        float f[VE];
+        unpack<DT>(e, f);
+        list_vector(f, L.vec_at[v]);
+        add(f);
+      }
+    }
   }
   m = wave_max(m);
   if ((tid & 63) == 0) L.shf[0][tid >> 6] = m;
@@ -779,7 +823,7 @@ struct TopArgs {
 };
 
 // One workgroup per row.  A long row's time is its read (2,048 x 131,072 bf16:
-// 131 us, 4.1 TB/s; the FP32 exponentials alone would take 58); the threshold,
+// 117 us, 4.6 TB/s; with each likely class listed on the spot 131); the threshold,
 // the ranking and the workgroup's reductions are 5 to 8 us a row, which the
 // CU's other two workgroups cover in part.
 template <int DT, int NT>
