@@ -823,7 +823,7 @@ struct TopArgs {
 };
 
 // One workgroup per row.  A long row's time is its read (2,048 x 131,072 bf16:
-// 117 us, 4.6 TB/s; with each likely class listed on the spot 131); the threshold,
+// 114 us, 4.7 TB/s; with each likely class listed on the spot 131); the threshold,
 // the ranking and the workgroup's reductions are 5 to 8 us a row, which the
 // CU's other two workgroups cover in part.
 template <int DT, int NT>
@@ -1339,7 +1339,7 @@ __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const
   return true;
 }
 
-// FP64 bounds draws without top-k: 20 instructions a class, 57 us of 195 for
+// FP64 bounds draws without top-k: 20 instructions a class, 57 us of 182 for
 // 1,024 x 100,003 bf16 with top-p and min-p; the rest is the row's latencies
 // (threshold, ranking, cuts: 20 us) with two workgroups a CU.  Four waves a
 // SIMD: with six the pass spills (330 us).
@@ -1520,8 +1520,9 @@ void launch_top_rows(const TopArgs& a, hipStream_t s) {
 
 // Threads for a row: a wave up to 2,048 classes, 256 up to 40,000 (draws of
 // 2,000 x 20,000 f32: 95 us with 256, 106 with 512), then 512 (records of
-// 2,048 x 131,072 bf16: 145 us with 512, 161 with 256, 229 with 1,024); at most
-// a row a CU: 1,024 (records of 32 such rows: 33 us, 38 with 512).
+// 2,048 x 131,072 bf16: 145 us with 512, 161 with 256, 229 with 1,024, before
+// likely vectors waited); at most a row a CU: 1,024 (records of 32 such rows: 33
+// us, 38 with 512).
 constexpr int64_t kFewRows = 256;
 
 template <int DT>
