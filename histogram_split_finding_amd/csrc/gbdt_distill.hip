@@ -9,7 +9,11 @@
 //                + (1 - r) log((1 - r) s / z) + r log(r s / s_out),
 // which is sum p log(p / q) with the logarithms of the sums taken out: their
 // arguments are near 1 when the student is near the teacher, so the loss keeps
-// its digits where it is small.
+// its digits where it is small.  s_out is kept as a sum against the largest
+// score outside S, m_out (v_c = exp((x_c - m_out) / T), o = sum_{not S} v, which
+// is at least 1): a student that is certain of a listed class has all others so
+// far below m that their w underflow.  s_out = o exp((m_out - m) / T), and
+//   log(r s / s_out) = log(r s / o) + (m - m_out) / T.
 //   gradient: weight T (w_c / s - p_c) in S, weight T (w_c / s)(1 - r s / s_out)
 //   outside.
 
@@ -34,8 +38,8 @@ namespace {
 constexpr int kStats = 1, kLoss = 2, kGrad = 4, kPart = 8, kJoin = 16;
 
 struct PartSum {
-  double s_out;
-  float m;
+  double o;
+  float m_out;
   uint32_t pad;
 };
 
@@ -69,16 +73,16 @@ __device__ __forceinline__ double row_rest(const DistillArgs& a, int64_t i, bool
   return r > 1.0f ? 1.0 : 0.0;
 }
 
-// The loss from the row's sums; kd = sum_j e_j ((t_j - t_max) - (x_j - m)).
-__device__ __forceinline__ double row_loss(double T, double inv_T, double r, double z, double kd, double s_in,
-                                           double s_out) {
-  const double s = s_in + s_out;
+// The loss from the row's sums; kd = sum_j e_j ((t_j - t_max) - (x_j - m)),
+// gap = m - m_out.
+__device__ __forceinline__ double row_loss(double T, double inv_T, double r, double z, double kd, double s, double o,
+                                           double gap) {
   double l = 0.0;
   if (r < 1.0) {
     const double iz = rcp_64(z);
     l += (1.0 - r) * (kd * iz * inv_T + log_64((1.0 - r) * s * iz));
   }
-  if (r > 0.0) l += s_out == 0.0 ? __builtin_inf() : r * log_64(r * s * rcp_64(s_out));
+  if (r > 0.0) l += o == 0.0 ? __builtin_inf() : r * (log_64(r * s * rcp_64(o)) + gap * inv_T);
   return T * T * l;
 }
 
@@ -119,8 +123,8 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
   }
   const bool mine = tid < rows;
   const double r = mine ? row_rest(a, i, true) : 0.0;
-  float wt = 1.0f, m = -kInf, tm = -kInf;
-  double s_in = 0.0, s_out = 0.0;
+  float wt = 1.0f, m = -kInf, m_out = -kInf, tm = -kInf;
+  double s_in = 0.0, s_out = 0.0, o = 0.0;
   if (mine && (MODE & kGrad) && a.weight != nullptr) wt = a.weight[i];
   if (mine && !(MODE & kStats)) {
     m = a.stats_in[3 * i];
@@ -132,10 +136,6 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
   float* __restrict__ tv = all_t + tid * PK;
   const int32_t* __restrict__ tc = all_c + tid * PK;
   if (mine) {
-    if (MODE & kStats) {
-#pragma unroll
-      for (int c = 0; c < CMAX; ++c) m = c < C ? __builtin_fmaxf(m, x[c]) : m;
-    }
     uint32_t in_s = 0u;
     bool has = false;
     for (int32_t j = 0; j < k; ++j) {
@@ -151,7 +151,17 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       tm = __builtin_fmaxf(tm, t);
       has = has || !(t == -kInf);
     }
+    if (MODE & kStats) {
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c) {
+        if (c < C) {
+          m = __builtin_fmaxf(m, x[c]);
+          m_out = in_s >> c & 1u ? m_out : __builtin_fmaxf(m_out, x[c]);
+        }
+      }
+    }
     const double ms = m == -kInf ? 0.0 : (double)m;
+    const double mos = m_out == -kInf ? 0.0 : (double)m_out;
     const double ts = tm == -kInf ? 0.0 : (double)tm;
     double z = 0.0, kd = 0.0;
     for (int32_t j = 0; j < k; ++j) {
@@ -164,14 +174,17 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       if (MODE & kGrad) tv[j] = (float)e;
     }
     if (MODE & kStats) {
+      const double of_m = exp2_64(((double)m_out - ms) * a.c);  // w / v
 #pragma unroll
       for (int c = 0; c < CMAX; ++c) {
         if (c < C) {
-          const double w = exp2_64(((double)x[c] - ms) * a.c);
-          if (in_s >> c & 1u) s_in += w; else s_out += w;
-          if (MODE & kGrad) x[c] = (float)w;
+          const bool in = in_s >> c & 1u;
+          const double w = exp2_64(((double)x[c] - (in ? ms : mos)) * a.c);
+          if (in) s_in += w; else o += w;
+          if (MODE & kGrad) x[c] = (float)(in ? w : w * of_m);
         }
       }
+      s_out = o * of_m;
     }
     const double s = s_in + s_out;
     const bool live = has && !(s == 0.0);
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       a.stats_out[3 * i + 1] = (float)s_in;
       a.stats_out[3 * i + 2] = (float)s_out;
     }
-    if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s_in, s_out) : 0.0f;
+    if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s, o, ms - mos) : 0.0f;
     if (MODE & kGrad) {
       const bool counts = live && !(wt == 0.0f);
       const double g = (double)wt * (double)a.T;
@@ -222,9 +235,10 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
 // (4.9 TB/s of what has to move; the second read of the scores comes from the
 // last-level cache), gradient of 2,048 x 50,001 f32 152 us (5.4 TB/s).
 //
-// One pass takes the sum against a reference that is the first maximum the
-// thread meets and moves only when a score is above it by 2^20 in the
-// exponential, so a vector costs no rescaling; the second writes the gradient.
+// One pass takes the sum outside S against a reference that is the first
+// maximum the thread meets there and moves only when a score is above it by
+// 2^20 in the exponential, so a vector costs no rescaling; the second writes the
+// gradient.
 // LDS: a bit per class (set: listed), laid out so that a thread's part of a
 // block is one word (or half of one).  Thread j of the first k owns entry j
 // (and j + NT, ...) of the record; its class's gradient replaces, behind a
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
   constexpr int KPT = NT < 64 ? kNarrowListed / NT : (GBDT_MAX_LISTED + NT - 1) / NT;
   constexpr bool kSums = (MODE & kStats) && !(MODE & kJoin);
   extern __shared__ uint32_t all_bits[];
-  __shared__ float sh_m[W], sh_t[W];
+  __shared__ float sh_m[W], sh_o[W], sh_t[W];
   __shared__ double sh_d[4][W];
   const int tid = threadIdx.x & (NT - 1), wid = threadIdx.x >> 6;
   const int sub = NT < 64 ? threadIdx.x / NT : 0;  // the row's place in the wave
@@ -295,8 +309,8 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     has = has || !(t[u] == -kInf);
   }
   __syncthreads();
-  float m = -kInf, ref = -kInf;
-  double so = 0.0;
+  float m_out = -kInf, ref = -kInf;
+  double o = 0.0;
   if (kSums) {
     for (int32_t base = lo, b = 0;; b += BLK) {
       const uint32_t in_s = bits[(b / 32) * NT + tid] >> (b % 32);
@@ -304,21 +318,21 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
       for (int j = 0; j < kVecs; ++j) {
         float f[VE];
         unpack<DT>(raw.v[j], f);
-        const float vm = max_of(f);
-        m = __builtin_fmaxf(m, vm);
-        if ((vm - ref) * cf > 20.0f) {  // (the first finite score among them)
-          so *= exp2_64(((double)ref - (double)vm) * a.c);
-          ref = vm;
-        }
         const uint32_t in_v = in_s >> (j * VE) & ((1u << VE) - 1u);
         if (in_v) {
 #pragma unroll
           for (int q = 0; q < VE; ++q) f[q] = in_v >> q & 1u ? -kInf : f[q];
         }
+        const float vm = max_of(f);
+        m_out = __builtin_fmaxf(m_out, vm);
+        if ((vm - ref) * cf > 20.0f) {  // (the first finite score among them)
+          o *= exp2_64(((double)ref - (double)vm) * a.c);
+          ref = vm;
+        }
         const float rf = ref == -kInf ? 0.0f : ref;
 #pragma unroll
         for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - rf) * cf);
-        so += (double)sum_of(f);
+        o += (double)sum_of(f);
         __builtin_amdgcn_sched_barrier(0);  // (vector by vector: fewer registers)
       }
       base += NT * BLK;
@@ -328,32 +342,44 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
   } else if (MODE & kJoin) {
     if (tid < a.n_joined) {
       const PartSum p = a.parts[i * a.n_joined + tid];
-      m = ref = p.m;
-      so = p.s_out;
+      m_out = ref = p.m_out;
+      o = p.o;
     }
-  } else {
-    m = a.stats_in[3 * i];
   }
   // the row's maxima; NaN in the record counts as an entry
-  m = group_max<NT>(m);
+  float m = -kInf;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) m = __builtin_fmaxf(m, xj[u]);
+  if (MODE & kStats) {
+    m = group_max<NT>(__builtin_fmaxf(m, m_out));
+    m_out = group_max<NT>(m_out);
+  }
   tm = group_max<NT>(tm);
   if (NT <= 64) {
     has = (__ballot(has) >> (sub * NT) & (~uint64_t(0) >> (64 - (NT < 64 ? NT : 64)))) != 0;
   } else {
     if ((tid & 63) == 0) {
-      sh_m[wid] = m;
+      if (MODE & kStats) {
+        sh_m[wid] = m;
+        sh_o[wid] = m_out;
+      }
       sh_t[wid] = tm;
     }
     has = __syncthreads_or(has);
-    m = across_waves<W>(sh_m, [](float u, float v) { return __builtin_fmaxf(u, v); });
+    if (MODE & kStats) {
+      m = across_waves<W>(sh_m, [](float u, float v) { return __builtin_fmaxf(u, v); });
+      m_out = across_waves<W>(sh_o, [](float u, float v) { return __builtin_fmaxf(u, v); });
+    }
     tm = across_waves<W>(sh_t, [](float u, float v) { return __builtin_fmaxf(u, v); });
   }
+  if (!(MODE & kStats)) m = a.stats_in[3 * i];
   const double ms = m == -kInf ? 0.0 : (double)m;
+  const double mos = m_out == -kInf ? 0.0 : (double)m_out;
   const double ts = tm == -kInf ? 0.0 : (double)tm;
-  if ((MODE & kStats) && ref != m) so *= exp2_64(((double)ref - ms) * a.c);
+  if ((MODE & kStats) && ref != m_out) o *= exp2_64(((double)ref - mos) * a.c);
   if constexpr ((MODE & kPart) != 0) {
-    so = block_sum<NT>(so, sh_d[0]);
-    if (tid == 0) a.parts[i * a.n_parts + part] = PartSum{so, m, 0u};
+    o = block_sum<NT>(o, sh_d[0]);
+    if (tid == 0) a.parts[i * a.n_parts + part] = PartSum{o, m_out, 0u};
     return;
   }
   double e[KPT], wj[KPT], z = 0.0, kd = 0.0, si = 0.0;
@@ -366,7 +392,7 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     if (!(e[u] == 0.0)) kd += e[u] * (d - dx);
     si += wj[u];
   }
-  double sum[4] = {z, kd, si, so};
+  double sum[4] = {z, kd, si, o};
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     sum[v] = group_sum<NT>(sum[v]);
@@ -379,7 +405,8 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
   }
   z = sum[0];
   kd = sum[1];
-  double s_in = sum[2], s_out = sum[3];
+  o = sum[3];
+  double s_in = sum[2], s_out = o * exp2_64(((double)m_out - ms) * a.c);
   if (!(MODE & kStats)) {
     s_in = a.stats_in[3 * i + 1];
     s_out = a.stats_in[3 * i + 2];
@@ -393,7 +420,7 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
       a.stats_out[3 * i + 1] = (float)s_in;
       a.stats_out[3 * i + 2] = (float)s_out;
     }
-    if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s_in, s_out) : 0.0f;
+    if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s, o, ms - mos) : 0.0f;
   }
   if (MODE & kGrad) {
     const float wt = a.weight != nullptr ? a.weight[i] : 1.0f;
