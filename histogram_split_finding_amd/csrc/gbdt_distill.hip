@@ -14,8 +14,8 @@
 // is at least 1): a student that is certain of a listed class has all others so
 // far below m that their w underflow.  s_out = o exp((m_out - m) / T), and
 //   log(r s / s_out) = log(r s / o) + (m - m_out) / T.
-//   gradient: weight T (w_c / s - p_c) in S, weight T (w_c / s)(1 - r s / s_out)
-//   outside.
+//   gradient: weight T (w_c / s - p_c) in S, weight T v_c (a / s - r / o) outside,
+//   a = exp((m_out - m) / T): every factor is at most 1, whatever the gap.
 
 #include <hip/hip_runtime.h>
 
@@ -86,6 +86,11 @@ __device__ __forceinline__ double row_loss(double T, double inv_T, double r, dou
   return T * T * l;
 }
 
+// a / s - r / o; 0 without mass outside S.
+__device__ __forceinline__ double outside_factor(double a_s, double r, double o) {
+  return o > 0.0 ? a_s - r * rcp_64(o) : (o == 0.0 ? 0.0 : o);
+}
+
 // One thread per row of at most CMAX classes, R rows a workgroup; k <= C.  Rows,
 // records and gradients pass through LDS, so that global memory sees whole
 // lines (a thread's own row is a stride of 4 C bytes from its neighbours'), in
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
   const bool mine = tid < rows;
   const double r = mine ? row_rest(a, i, true) : 0.0;
   float wt = 1.0f, m = -kInf, m_out = -kInf, tm = -kInf;
-  double s_in = 0.0, s_out = 0.0, o = 0.0;
+  double s_in = 0.0, s_out = 0.0, o = 0.0, of_m = 0.0;
   if (mine && (MODE & kGrad) && a.weight != nullptr) wt = a.weight[i];
   if (mine && !(MODE & kStats)) {
     m = a.stats_in[3 * i];
@@ -174,14 +179,14 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       if (MODE & kGrad) tv[j] = (float)e;
     }
     if (MODE & kStats) {
-      const double of_m = exp2_64(((double)m_out - ms) * a.c);  // w / v
+      of_m = exp2_64(((double)m_out - ms) * a.c);  // w / v
 #pragma unroll
       for (int c = 0; c < CMAX; ++c) {
         if (c < C) {
           const bool in = in_s >> c & 1u;
           const double w = exp2_64(((double)x[c] - (in ? ms : mos)) * a.c);
           if (in) s_in += w; else o += w;
-          if (MODE & kGrad) x[c] = (float)(in ? w : w * of_m);
+          if (MODE & kGrad) x[c] = (float)w;
         }
       }
       s_out = o * of_m;
@@ -197,9 +202,10 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
     if (MODE & kGrad) {
       const bool counts = live && !(wt == 0.0f);
       const double g = (double)wt * (double)a.T;
-      const double share = s_out > 0.0 ? 1.0 - r * s * rcp_64(s_out) : (s_out == 0.0 ? 0.0 : s_out);
       const double inv = rcp_64(s);
-      const float in = (float)inv, out = (float)(g * share * inv);
+      double share = s_out > 0.0 ? (1.0 - r * s * rcp_64(s_out)) * inv : (s_out == 0.0 ? 0.0 : s_out);
+      if (MODE & kStats) share = outside_factor(of_m * inv, r, o);
+      const float in = (float)inv, out = (float)(g * share);
       const float cf = exponent_scale(a.c), mf = (float)ms;
 #pragma unroll
       for (int c = 0; c < CMAX; ++c) {
@@ -406,7 +412,8 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
   z = sum[0];
   kd = sum[1];
   o = sum[3];
-  double s_in = sum[2], s_out = o * exp2_64(((double)m_out - ms) * a.c);
+  const double of_m = exp2_64(((double)m_out - ms) * a.c);
+  double s_in = sum[2], s_out = o * of_m;
   if (!(MODE & kStats)) {
     s_in = a.stats_in[3 * i + 1];
     s_out = a.stats_in[3 * i + 2];
@@ -426,10 +433,11 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     const float wt = a.weight != nullptr ? a.weight[i] : 1.0f;
     const bool counts = live && !(wt == 0.0f);
     const double g = (double)wt * (double)a.T;
-    const double share = s_out > 0.0 ? 1.0 - r * s * rcp_64(s_out) : (s_out == 0.0 ? 0.0 : s_out);
     const double inv = rcp_64(s);
-    const float scale = (float)(g * share * inv);
-    const float mf = (float)ms;
+    double share = s_out > 0.0 ? (1.0 - r * s * rcp_64(s_out)) * inv : (s_out == 0.0 ? 0.0 : s_out);
+    if (MODE & kStats) share = outside_factor(of_m * inv, r, o);
+    const float scale = (float)(g * share);
+    const float mf = (float)(MODE & kStats ? mos : ms);
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
     for (int32_t base = lo; base < hi; base += NT * BLK) {
       RawBlock<DT> o;

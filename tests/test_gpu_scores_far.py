@@ -152,3 +152,27 @@ def test_loss(n, C, dtype, T):
     got = loss.double().cpu().numpy()
     assert np.all(np.abs(got - want) <= tol), (got - want, tol)
     assert g.gbdt_read_error(ws) == 0
+
+
+def check_grad(got, case, T, dtype, beyond):
+    _, x, tv, tc, tr, weight = case
+    _, want, q, p, away = reference(x, tv, tc, tr, T, weight)
+    e = ((3 * (spread(x, tc, T) + beyond) + 8) * 2.0 ** -24)[:, None]
+    tiny = {"f32": 1e-36, "bf16": 1e-36, "f16": 2.0 ** -25}[dtype]
+    tol = np.abs(weight)[:, None] * T * (q + p + away) * 2 * e + ref.EPS[dtype] / 2 * np.abs(want) + tiny
+    got = got.double().cpu().numpy()
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), [(GAPS[i % len(GAPS)], tr[i], got[i, c], want[i, c]) for i, c in np.argwhere(bad)[:5]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [COLD, 1.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,C", SHAPES)
+def test_step_gradient(n, C, dtype, T):
+    print("far step: %d x %d %s T=%s" % (n, C, dtype, T), flush=True)
+    case = far_rows(n, C, dtype, T, C)
+    g, xd, (tvd, tcd, trd, wd), ws, loss, stats, grad = on_device(case)
+    g.gbdt_distill_step(xd, tvd, tcd, trd, T, wd, loss, grad, ws)
+    check_grad(grad, case, T, dtype, 0.0)
+    assert g.gbdt_read_error(ws) == 0
