@@ -86,9 +86,19 @@ __device__ __forceinline__ double row_loss(double T, double inv_T, double r, dou
   return T * T * l;
 }
 
-// a / s - r / o; 0 without mass outside S.
-__device__ __forceinline__ double outside_factor(double a_s, double r, double o) {
-  return o > 0.0 ? a_s - r * rcp_64(o) : (o == 0.0 ? 0.0 : o);
+// Statistics are FP32.  Below its normal numbers s_out has lost digits, or is 0:
+// the gradient then takes m_out and o from the scores again.  Otherwise s_out =
+// o 2^e with o in [1/2, 1) serves: v = w 2^-e = exp2((x - m) c + up), up = -e.
+constexpr float kLeastStat = 0x1p-126f;
+__device__ __forceinline__ void stat_sum(float s_out, double& o, float& up) {
+  const uint32_t b = __float_as_uint(s_out);
+  o = (double)__uint_as_float((b & 0x7fffffu) | 0x3f000000u);
+  up = (float)(126 - (int32_t)(b >> 23));
+}
+
+// a / s - r / o = (s_out / s - r) / o; 0 without mass outside S.
+__device__ __forceinline__ double outside_factor(double s_out_s, double r, double o) {
+  return o > 0.0 ? (s_out_s - r) * rcp_64(o) : (o == 0.0 ? 0.0 : o);
 }
 
 // One thread per row of at most CMAX classes, R rows a workgroup; k <= C.  Rows,
@@ -129,7 +139,7 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
   const bool mine = tid < rows;
   const double r = mine ? row_rest(a, i, true) : 0.0;
   float wt = 1.0f, m = -kInf, m_out = -kInf, tm = -kInf;
-  double s_in = 0.0, s_out = 0.0, o = 0.0, of_m = 0.0;
+  double s_in = 0.0, s_out = 0.0, o = 0.0;
   if (mine && (MODE & kGrad) && a.weight != nullptr) wt = a.weight[i];
   if (mine && !(MODE & kStats)) {
     m = a.stats_in[3 * i];
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       }
     }
     const double ms = m == -kInf ? 0.0 : (double)m;
-    const double mos = m_out == -kInf ? 0.0 : (double)m_out;
+    double mos = m_out == -kInf ? 0.0 : (double)m_out;
     const double ts = tm == -kInf ? 0.0 : (double)tm;
     double z = 0.0, kd = 0.0;
     for (int32_t j = 0; j < k; ++j) {
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       if (MODE & kGrad) tv[j] = (float)e;
     }
     if (MODE & kStats) {
-      of_m = exp2_64(((double)m_out - ms) * a.c);  // w / v
+      const double of_m = exp2_64(((double)m_out - ms) * a.c);  // w / v
 #pragma unroll
       for (int c = 0; c < CMAX; ++c) {
         if (c < C) {
@@ -203,15 +213,29 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
       const bool counts = live && !(wt == 0.0f);
       const double g = (double)wt * (double)a.T;
       const double inv = rcp_64(s);
-      double share = s_out > 0.0 ? (1.0 - r * s * rcp_64(s_out)) * inv : (s_out == 0.0 ? 0.0 : s_out);
-      if (MODE & kStats) share = outside_factor(of_m * inv, r, o);
-      const float in = (float)inv, out = (float)(g * share);
-      const float cf = exponent_scale(a.c), mf = (float)ms;
+      float up = 0.0f;  // v = exp2((x - m_out) c + up)
+      if (!(MODE & kStats)) {
+        if (r > 0.0 && (float)s_out < kLeastStat) {
+#pragma unroll 1
+          for (int c = 0; c < C; ++c) m_out = in_s >> c & 1u ? m_out : __builtin_fmaxf(m_out, x[c]);
+          mos = m_out == -kInf ? 0.0 : (double)m_out;
+#pragma unroll 1
+          for (int c = 0; c < C; ++c) o += in_s >> c & 1u ? 0.0 : exp2_64(((double)x[c] - mos) * a.c);
+        } else {
+          stat_sum((float)s_out, o, up);
+          mos = ms;
+        }
+      }
+      const float in = (float)inv, out = (float)(g * outside_factor(s_out * inv, r, o));
+      const float cf = exponent_scale(a.c), mf = (float)ms, mof = (float)mos;
 #pragma unroll
       for (int c = 0; c < CMAX; ++c) {
         if (c < C) {
-          const float w = MODE & kStats ? x[c] : exp2_32((x[c] - mf) * cf);
-          x[c] = counts ? w * (in_s >> c & 1u ? in : out) : 0.0f;
+          const bool in_c = in_s >> c & 1u;
+          const float w = MODE & kStats
+                              ? x[c]
+                              : exp2_32(__builtin_fmaf(x[c] - (in_c ? mf : mof), cf, in_c ? 0.0f : up));
+          x[c] = counts ? w * (in_c ? in : out) : 0.0f;
         }
       }
       if (counts) {
@@ -279,6 +303,8 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
   const int32_t words = ((hi - lo + NT * BLK - 1) / (NT * BLK) * BLK + 31) / 32 * NT;
   uint32_t* __restrict__ bits = all_bits + sub * words;
   for (int32_t w = tid; w < words; w += NT) bits[w] = 0u;
+  const double r = row_rest(a, i, tid == 0);
+  const float wt = (MODE & kGrad) && a.weight != nullptr ? a.weight[i] : 1.0f;
   int32_t cls[KPT];
   float t[KPT], xj[KPT];
 #pragma unroll
@@ -300,23 +326,37 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     }
   }
   __syncthreads();
+  // word and bit of the e-th class: (block, vector, thread, element)
+  auto place_of = [](int32_t e, int32_t& bit) {
+    const int32_t in = e % (NT * BLK), blk = e / (NT * BLK);
+    bit = blk * BLK % 32 + in / (NT * VE) * VE + in % VE;
+    return blk * BLK / 32 * NT + in / VE % NT;
+  };
+  // the bits of the record's classes in [from, to)
+  auto mark_listed = [&](int32_t from, int32_t to) {
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      if (cls[u] >= from && cls[u] < to) {
+        int32_t bit;
+        const int32_t word = place_of(cls[u] - from, bit);
+        if (atomicOr(&bits[word], 1u << bit) >> bit & 1u) dev_error(a.err, GBDT_E_ARG);
+      }
+    }
+  };
+  mark_listed(lo, hi);
   float tm = -kInf;
   bool has = false;
 #pragma unroll
   for (int u = 0; u < KPT; ++u) {
-    if (cls[u] >= lo && cls[u] < hi) {
-      // (block, vector, thread, element) of the class
-      const int32_t e = cls[u] - lo, in = e % (NT * BLK), blk = e / (NT * BLK);
-      const int32_t bit = blk * BLK % 32 + in / (NT * VE) * VE + in % VE;
-      const int32_t word = blk * BLK / 32 * NT + in / VE % NT;
-      if (atomicOr(&bits[word], 1u << bit) >> bit & 1u) dev_error(a.err, GBDT_E_ARG);
-    }
     tm = __builtin_fmaxf(tm, t[u]);
     has = has || !(t[u] == -kInf);
   }
   __syncthreads();
-  float m_out = -kInf, ref = -kInf;
+  float m = -kInf, m_out = -kInf, ref = -kInf;
   double o = 0.0;
+  // of a gradient from statistics: v = exp2((x - mf) c + up), and its sum
+  float mf = 0.0f, up = 0.0f;
+  double s_in = 0.0, s_out = 0.0, o_stat = 0.0;
   if (kSums) {
     for (int32_t base = lo, b = 0;; b += BLK) {
       const uint32_t in_s = bits[(b / 32) * NT + tid] >> (b % 32);
@@ -351,12 +391,52 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
       m_out = ref = p.m_out;
       o = p.o;
     }
+  } else {
+    s_in = a.stats_in[3 * i + 1];
+    s_out = a.stats_in[3 * i + 2];
+    m = a.stats_in[3 * i];
+    stat_sum((float)s_out, o_stat, up);
+    mf = m;
+    const bool lost = r > 0.0 && !(wt == 0.0f) && (float)s_out < kLeastStat;
+    if (NT <= 64 ? __any(lost) : lost) {
+      // All threads of a row, and all rows of a wave, come here together; a part
+      // at a time, as the bits have room for one; class by class: few registers
+      // for what few rows need.
+      double again = 0.0, mos = 0.0;
+      for (int pass = 0; pass < 2; ++pass) {
+        for (int32_t from = 0; from < a.C; from += a.part_len) {
+          const int32_t to = a.C - from < a.part_len ? a.C : from + a.part_len;
+          __syncthreads();
+          for (int32_t w = tid; w < (a.part_len / (NT * BLK) * BLK + 31) / 32 * NT; w += NT) bits[w] = 0u;
+          __syncthreads();
+          mark_listed(from, to);
+          __syncthreads();
+#pragma unroll 1
+          for (int32_t c = from + tid; c < to; c += NT) {
+            int32_t bit;
+            const int32_t word = place_of(c - from, bit);
+            if (bits[word] >> bit & 1u) continue;
+            const float v = Score<DT>::to_f32(xr[c]);
+            if (pass == 0) m_out = __builtin_fmaxf(m_out, v); else again += exp2_64(((double)v - mos) * a.c);
+          }
+        }
+        if (pass == 0) {
+          m_out = NT <= 64 ? group_max<NT>(m_out) : block_max<NT>(m_out, sh_o);
+          mos = m_out == -kInf ? 0.0 : (double)m_out;
+        }
+      }
+      again = NT <= 64 ? group_sum<NT>(again) : block_sum<NT>(again, sh_d[0]);
+      if (lost) {
+        o_stat = again;
+        up = 0.0f;
+        mf = (float)mos;
+      }
+    }
   }
   // the row's maxima; NaN in the record counts as an entry
-  float m = -kInf;
-#pragma unroll
-  for (int u = 0; u < KPT; ++u) m = __builtin_fmaxf(m, xj[u]);
   if (MODE & kStats) {
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) m = __builtin_fmaxf(m, xj[u]);
     m = group_max<NT>(__builtin_fmaxf(m, m_out));
     m_out = group_max<NT>(m_out);
   }
@@ -378,7 +458,6 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     }
     tm = across_waves<W>(sh_t, [](float u, float v) { return __builtin_fmaxf(u, v); });
   }
-  if (!(MODE & kStats)) m = a.stats_in[3 * i];
   const double ms = m == -kInf ? 0.0 : (double)m;
   const double mos = m_out == -kInf ? 0.0 : (double)m_out;
   const double ts = tm == -kInf ? 0.0 : (double)tm;
@@ -411,14 +490,14 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
   }
   z = sum[0];
   kd = sum[1];
-  o = sum[3];
-  const double of_m = exp2_64(((double)m_out - ms) * a.c);
-  double s_in = sum[2], s_out = o * of_m;
-  if (!(MODE & kStats)) {
-    s_in = a.stats_in[3 * i + 1];
-    s_out = a.stats_in[3 * i + 2];
+  if (MODE & kStats) {
+    o = sum[3];
+    s_in = sum[2];
+    s_out = o * exp2_64(((double)m_out - ms) * a.c);
+    mf = (float)mos;
+  } else {
+    o = o_stat;
   }
-  const double r = row_rest(a, i, tid == 0);
   const double s = s_in + s_out;
   const bool live = has && !(s == 0.0);
   if (tid == 0 && part == 0) {
@@ -430,17 +509,13 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     if (MODE & kLoss) a.loss[i] = live ? (float)row_loss(a.T, a.inv_T, r, z, kd, s, o, ms - mos) : 0.0f;
   }
   if (MODE & kGrad) {
-    const float wt = a.weight != nullptr ? a.weight[i] : 1.0f;
     const bool counts = live && !(wt == 0.0f);
     const double g = (double)wt * (double)a.T;
     const double inv = rcp_64(s);
-    double share = s_out > 0.0 ? (1.0 - r * s * rcp_64(s_out)) * inv : (s_out == 0.0 ? 0.0 : s_out);
-    if (MODE & kStats) share = outside_factor(of_m * inv, r, o);
-    const float scale = (float)(g * share);
-    const float mf = (float)(MODE & kStats ? mos : ms);
+    const float scale = (float)(g * outside_factor(s_out * inv, r, o));
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
     for (int32_t base = lo; base < hi; base += NT * BLK) {
-      RawBlock<DT> o;
+      RawBlock<DT> out;
       if (counts) {
         raw = load_block<DT, NT>(xr, base, hi);
 #pragma unroll
@@ -448,14 +523,15 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
           float f[VE];
           unpack<DT>(raw.v[j], f);
 #pragma unroll
-          for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - mf) * cf) * scale;
-          o.v[j] = pack<DT>(f);
+          for (int q = 0; q < VE; ++q)
+            f[q] = exp2_32(MODE & kStats ? (f[q] - mf) * cf : __builtin_fmaf(f[q] - mf, cf, up)) * scale;
+          out.v[j] = pack<DT>(f);
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
-        o = RawBlock<DT>{};
+        out = RawBlock<DT>{};
       }
-      store_block<DT, NT>(gr, base, hi, o);
+      store_block<DT, NT>(gr, base, hi, out);
     }
     __syncthreads();
     if (counts) {
@@ -517,7 +593,7 @@ int launch_distill(const DistillArgs& args, hipStream_t s) {
     const int32_t parts = (steps + per - 1) / per;
     a.part_len = per * kPartStep;
     a.n_parts = a.n_joined = parts;
-    if (MODE & kStats) {
+    if constexpr ((MODE & kStats) != 0) {
       launch_block<DT, 256, kStats | kPart>(a, s);
       if (!(MODE & kGrad)) a.n_parts = 1;
       launch_block<DT, 256, MODE | kJoin>(a, s);

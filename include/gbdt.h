@@ -743,8 +743,10 @@ int gbdt_top_scores(const gbdt_scores* x /* host */, int32_t k, float temperatur
  *
  * gbdt_distill_loss also writes stats[n_rows][3] = (max x, sum of
  * exp((x_c - max x) / T) in S, the same outside S), which gbdt_distill_grad
- * reads: the forward and the backward pass.  gbdt_distill_step does both in
- * one call and writes no statistics.  weight: [n_rows] or NULL (ones).  grad: the scores'
+ * reads: the forward and the backward pass.  (Where the sum outside S is below
+ * FP32's normal numbers, some 87 T under the maximum, gbdt_distill_grad takes
+ * it from the scores again.)  gbdt_distill_step does both in one call and writes
+ * no statistics.  weight: [n_rows] or NULL (ones).  grad: the scores'
  * type, rows grad_stride elements apart; it must not overlap the scores.
  */
 int gbdt_distill_loss(const gbdt_scores* x /* host */, const gbdt_teacher* t /* host */,

@@ -176,3 +176,17 @@ def test_step_gradient(n, C, dtype, T):
     g.gbdt_distill_step(xd, tvd, tcd, trd, T, wd, loss, grad, ws)
     check_grad(grad, case, T, dtype, 0.0)
     assert g.gbdt_read_error(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [COLD, 1.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,C", SHAPES)
+def test_gradient_from_statistics(n, C, dtype, T):
+    print("far gradient: %d x %d %s T=%s" % (n, C, dtype, T), flush=True)
+    case = far_rows(n, C, dtype, T, C)
+    g, xd, (tvd, tcd, trd, wd), ws, loss, stats, grad = on_device(case)
+    g.gbdt_distill_loss(xd, tvd, tcd, trd, T, loss, stats, ws)
+    g.gbdt_distill_grad(xd, tvd, tcd, trd, T, stats, wd, grad, ws)
+    check_grad(grad, case, T, dtype, 88.0)
+    assert g.gbdt_read_error(ws) == 0
