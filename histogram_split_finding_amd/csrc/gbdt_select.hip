@@ -447,8 +447,10 @@ __device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __re
       m = __builtin_fmaxf(m, vm);
       if (vm >= thr) {
         // a wave meets such a vector every other time: what it does here has to
-        // be little, so its elements wait (with up to 256 threads a row the LDS
-        // for that would cost workgroups)
+        // be little, so its likely elements wait (with up to 256 threads a row
+        // the LDS for that would cost workgroups).  The others are added here and
+        // not by the thread that lists them, which the atomic chooses: the order
+        // of the additions is always the same.
         const int32_t c0 = base + (j * NT + tid) * VE;
         if constexpr (NT > 256) {
           const uint32_t at = atomicAdd(&L.n_vec, 1u);
@@ -457,7 +459,7 @@ __device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __re
             L.vec_at[at] = c0;
           }
 #pragma unroll
-          for (int q = 0; q < VE; ++q) f[q] = -kInf;
+          for (int q = 0; q < VE; ++q) f[q] = f[q] >= thr ? -kInf : f[q];
         } else {
           list_vector(f, c0);
         }
@@ -481,7 +483,6 @@ __device__ __forceinline__ void scan_blocks(const typename Score<DT>::Elem* __re
         float f[VE];
         unpack<DT>(e, f);
         list_vector(f, L.vec_at[v]);
-        add(f);
       }
     }
   }
