@@ -547,7 +547,9 @@ template <int DT, int R, int CMAX, int MODE>
 void launch_rows(const DistillArgs& a, hipStream_t s) {
   const size_t lds = size_t(R) * 4 * ((a.C | 1) + 2 * (a.k | 1));
   const dim3 grid((unsigned)((a.n + R - 1) / R));
+  diag_begin(kDiagDistill, s);
   hipLaunchKernelGGL((k_distill_rows<DT, R, CMAX, MODE>), grid, dim3(R), lds, s, a);
+  diag_end(s);
 }
 
 template <int DT, int NT, int MODE>
@@ -558,8 +560,10 @@ void launch_block(DistillArgs a, hipStream_t s) {
   const size_t lds = size_t((a.part_len / kStep * kBlk<DT> + 31) / 32) * NT * 4 * kRows;
   for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    diag_begin(kDiagDistill, s);
     hipLaunchKernelGGL((k_distill_block<DT, NT, MODE>), dim3((unsigned)((n + kRows - 1) / kRows * a.n_parts)),
                        dim3(kRows * NT), lds, s, a);
+    diag_end(s);
   }
 }
 
@@ -579,7 +583,6 @@ int launch_distill(const DistillArgs& args, hipStream_t s) {
   a.part_len = 0;
   constexpr int32_t kPartStep = 256 * kBlk<DT>;
   const int32_t steps = (a.C + kPartStep - 1) / kPartStep;
-  diag_begin(kDiagDistill, s);
   const bool short_rows = a.C <= kRowsMaxClasses && a.k <= a.C;
   if (short_rows && a.C <= 8) {
     launch_rows<DT, 64, 8, MODE>(a, s);
@@ -609,7 +612,6 @@ int launch_distill(const DistillArgs& args, hipStream_t s) {
   } else {
     launch_block<DT, 1024, MODE>(a, s);
   }
-  diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_distill");
 }

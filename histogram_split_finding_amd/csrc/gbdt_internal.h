@@ -321,7 +321,7 @@ int update_predictions(double* pred, const gbdt_matrix* X, const gbdt_node* node
 enum DiagKind {
   kDiagGradMax = 1, kDiagGradQ, kDiagPlan, kDiagHist, kDiagHistReduce, kDiagSubtract, kDiagFind,
   kDiagTreeInit, kDiagLevel, kDiagPartition, kDiagUpdate, kDiagPack, kDiagBin, kDiagPredict,
-  kDiagBounds
+  kDiagBounds, kDiagTopScores, kDiagDistill, kDiagSample
 };
 void diag_begin(int kind, hipStream_t s);
 void diag_end(hipStream_t s);

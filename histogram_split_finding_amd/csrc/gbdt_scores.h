@@ -356,9 +356,6 @@ struct RowDiv {
   __device__ __forceinline__ int32_t operator()(int32_t e) const { return int32_t(__umul24((uint32_t)e, inv) >> 20); }
 };
 
-// Records of the diagnostics, after the kinds of gbdt_internal.h.
-constexpr int kDiagTopScores = kDiagBounds + 1, kDiagDistill = kDiagBounds + 2, kDiagSample = kDiagBounds + 3;
-
 constexpr int64_t kMaxRowGrid = 1 << 20;  // rows of one launch, at most
 // Rows are shared by several workgroups when there are at most kSplitRows of
 // them: about kSplitGrid workgroups in all.

@@ -1505,18 +1505,24 @@ template <int DT, int NT>
 void launch_top_block(TopArgs a, hipStream_t s) {
   for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    diag_begin(kDiagTopScores, s);
     hipLaunchKernelGGL((k_top_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
+    diag_end(s);
   }
   // (a row of one block that fits the list is always finished)
   if (a.C <= ListLds<NT>::kList && a.C <= NT * kBlk<DT>) return;
   const dim3 rest((unsigned)(a.n < kRestGrid ? a.n : kRestGrid));
   constexpr int RT = NT < 256 ? NT : 256;
+  diag_begin(kDiagTopScores, s);
   hipLaunchKernelGGL((k_top_rest<DT, RT>), rest, dim3(RT), 0, s, a);
+  diag_end(s);
 }
 template <int DT, int R, int CMAX>
 void launch_top_rows(const TopArgs& a, hipStream_t s) {
   const size_t lds = size_t(R) * 4 * ((a.C | 1) + 2 * (a.k | 1));
+  diag_begin(kDiagTopScores, s);
   hipLaunchKernelGGL((k_top_rows<DT, R, CMAX>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
+  diag_end(s);
 }
 
 // Threads for a row: a wave up to 2,048 classes, 256 up to 40,000 (draws of
@@ -1528,7 +1534,6 @@ constexpr int64_t kFewRows = 256;
 
 template <int DT>
 int launch_top(const TopArgs& a, hipStream_t s) {
-  diag_begin(kDiagTopScores, s);
   if (a.C <= 8)
     launch_top_rows<DT, 256, 8>(a, s);
   else if (a.C <= 16)
@@ -1547,7 +1552,6 @@ int launch_top(const TopArgs& a, hipStream_t s) {
     launch_top_block<DT, 512>(a, s);
   else
     launch_top_block<DT, 1024>(a, s);
-  diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_top");
 }
@@ -1556,21 +1560,26 @@ template <int DT, int NT>
 void launch_sample_block(SampleArgs a, hipStream_t s) {
   for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    diag_begin(kDiagSample, s);
     hipLaunchKernelGGL((k_sample_block<DT, NT>), dim3((unsigned)n), dim3(NT), 0, s, a);
+    diag_end(s);
   }
   const dim3 rest((unsigned)(a.n < kRestGrid ? a.n : kRestGrid));
   constexpr int RT = NT < 256 ? NT : 256;
+  diag_begin(kDiagSample, s);
   hipLaunchKernelGGL((k_sample_rest<DT, RT>), rest, dim3(RT), 0, s, a);
+  diag_end(s);
 }
 template <int DT, int R, int CMAX>
 void launch_sample_rows(const SampleArgs& a, hipStream_t s) {
   const size_t lds = size_t(R) * 4 * (a.C | 1);
+  diag_begin(kDiagSample, s);
   hipLaunchKernelGGL((k_sample_rows<DT, R, CMAX>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
+  diag_end(s);
 }
 
 template <int DT>
 int launch_sample(const SampleArgs& a, hipStream_t s) {
-  diag_begin(kDiagSample, s);
   if (a.C <= 8)
     launch_sample_rows<DT, 256, 8>(a, s);
   else if (a.C <= 16)
@@ -1589,7 +1598,6 @@ int launch_sample(const SampleArgs& a, hipStream_t s) {
     launch_sample_block<DT, 512>(a, s);
   else
     launch_sample_block<DT, 1024>(a, s);
-  diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_sample");
 }

@@ -361,8 +361,8 @@ int gbdt_feature_bounds(const float* raw, int64_t n_rows, const gbdt_features* f
  * 2 gradient grid, 3 tile planner, 4 histogram, 5 histogram partial reduce,
  * 6 subtraction, 7 split search, 8 tree init, 9 level bookkeeping,
  * 10 partition, 11 prediction update, 12 packing, 13 binning, 14 ensemble
- * prediction, 15 bin bounds.  One process-wide record;
- * not for concurrent use from several threads.
+ * prediction, 15 bin bounds, 16 top scores, 17 distillation, 18 class draws.
+ * One process-wide record; not for concurrent use from several threads.
  */
 int gbdt_diag_enable(int32_t capacity);
 int gbdt_diag_disable(void);
