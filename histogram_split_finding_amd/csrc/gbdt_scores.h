@@ -251,10 +251,6 @@ __device__ __forceinline__ float block_max(float v, float* sh) {
   __syncthreads();
   return r;
 }
-template <int NT>
-__device__ __forceinline__ float block_min(float v, float* sh) {
-  return -block_max<NT>(-v, sh);
-}
 template <int NT, typename T>
 __device__ __forceinline__ T block_sum(T v, T* sh) {
   v = wave_sum(v);
@@ -348,7 +344,10 @@ __device__ __forceinline__ float sum_of(const float (&f)[N]) {
   return a + ((f[4 % N] + f[5 % N]) + (f[6 % N] + f[7 % N]));
 }
 
-// Quotients e / C of e < 2^13 for C <= 32 (e * (inv C - 2^20) < 2^20).
+// Quotients e / C by a product with inv = ceil(2^20 / C), right as long as
+// e (inv C - 2^20) < 2^20, where the bracket is at most C - 1.
+template <int R, int CMAX>  // e below R C, C up to CMAX
+constexpr bool kRowDivExact = (R * CMAX - 1) * (CMAX - 1) < 1 << 20;
 struct RowDiv {
   uint32_t inv;
   __device__ explicit RowDiv(int32_t C) : inv(((1u << 20) + (uint32_t)C - 1u) / (uint32_t)C) {}
@@ -368,6 +367,7 @@ __device__ __forceinline__ float exponent_scale(double c) { return c < 3.0e38 ? 
 // by all threads in whole lines, and laid down in LDS rows of width | 1 words.
 template <int R, int CMAX, typename T>
 struct Staged {
+  static_assert(kRowDivExact<R, CMAX>, "the quotients of these rows are not exact");
   T v[CMAX];
   template <typename LoadFlat, typename LoadAt>
   __device__ __forceinline__ void load(int32_t rows, int32_t width, bool flat, const RowDiv& div, LoadFlat at_flat,
