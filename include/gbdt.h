@@ -735,10 +735,10 @@ int gbdt_top_scores(const gbdt_scores* x /* host */, int32_t k, float temperatur
  * student's.  Its gradient, times the row's weight,
  *   in S:       weight T (q_c - p_c)
  *   outside S:  weight T q_c (1 - r / q_r).
- * A row whose record lists no class with a value above -inf, and a row without
- * a score above -inf, has loss 0 and gradient 0; a row of weight 0 has gradient
+ * A row whose record lists no class with a value above -inf, and a row whose
+ * scores are all -inf, has loss 0 and gradient 0; a row of weight 0 has gradient
  * 0 whatever its scores.  Other rows with a NaN (or +inf) score or value have
- * NaN results.  A class with p_j > 0 and q_j = 0 makes the loss +inf and leaves
+ * NaN results, also where all scores are NaN.  A class with p_j > 0 and q_j = 0 makes the loss +inf and leaves
  * the gradient finite.
  *
  * gbdt_distill_loss also writes stats[n_rows][3] = (max x, sum of

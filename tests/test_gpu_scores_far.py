@@ -190,3 +190,42 @@ def test_gradient_from_statistics(n, C, dtype, T):
     g.gbdt_distill_grad(xd, tvd, tcd, trd, T, stats, wd, grad, ws)
     check_grad(grad, case, T, dtype, 88.0)
     assert g.gbdt_read_error(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [7, 60, 1000, 9001, 70001])
+def test_rows_of_nan(C, dtype):
+    """Loss and both gradients: NaN for rows with a NaN or +inf score, a row of
+    NaN alone among them, 0 for masked rows and rows of weight 0."""
+    print("NaN rows: C=%d %s" % (C, dtype), flush=True)
+    n = 12
+    case = far_rows(n, C, dtype, 1.0, C + 1)
+    t, x, tv, tc, tr, weight = case
+    listed = tc[:, 1]
+    outside = [int(np.setdiff1d(np.arange(C), tc[i])[0]) for i in range(n)]
+    tr[:] = 0.25
+    t[0] = float("nan")
+    t[1, int(listed[1])] = float("nan")
+    t[2, outside[2]] = float("nan")
+    t[3, int(listed[3])] = float("inf")
+    t[4, outside[4]] = float("inf")
+    t[5], weight[5] = float("nan"), 0.0
+    t[6] = float("-inf")
+    t[7, int(listed[7])], weight[7] = float("inf"), 0.0
+    g, xd, (tvd, tcd, trd, wd), ws, loss, stats, grad = on_device(case)
+    step_loss, step_grad = torch.full_like(loss, 7.0), torch.full_like(grad, 7.0)
+    g.gbdt_distill_loss(xd, tvd, tcd, trd, 1.0, loss, stats, ws)
+    g.gbdt_distill_grad(xd, tvd, tcd, trd, 1.0, stats, wd, grad, ws)
+    g.gbdt_distill_step(xd, tvd, tcd, trd, 1.0, wd, step_loss, step_grad, ws)
+    assert g.gbdt_read_error(ws) == 0
+    for l, d in ((loss, grad), (step_loss, step_grad)):
+        l, d = l.cpu(), d.cpu()
+        for i in (0, 1, 2, 3, 4, 5, 7):
+            assert bool(l[i].isnan()), i
+        for i in (0, 1, 2, 3, 4):
+            assert bool(d[i].isnan().any()), i
+        assert l[6].item() == 0.0
+        for i in (5, 6, 7):
+            assert bool((d[i] == 0).all()), i
+        assert bool(l[8:].isfinite().all()) and bool(d[8:].isfinite().all())
