@@ -326,19 +326,15 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     }
   }
   __syncthreads();
-  // word and bit of the e-th class: (block, vector, thread, element)
-  auto place_of = [](int32_t e, int32_t& bit) {
-    const int32_t in = e % (NT * BLK), blk = e / (NT * BLK);
-    bit = blk * BLK % 32 + in / (NT * VE) * VE + in % VE;
-    return blk * BLK / 32 * NT + in / VE % NT;
-  };
   // the bits of the record's classes in [from, to)
   auto mark_listed = [&](int32_t from, int32_t to) {
 #pragma unroll
     for (int u = 0; u < KPT; ++u) {
       if (cls[u] >= from && cls[u] < to) {
-        int32_t bit;
-        const int32_t word = place_of(cls[u] - from, bit);
+        // (block, vector, thread, element) of the class
+        const int32_t e = cls[u] - from, in = e % (NT * BLK), blk = e / (NT * BLK);
+        const int32_t bit = blk * BLK % 32 + in / (NT * VE) * VE + in % VE;
+        const int32_t word = blk * BLK / 32 * NT + in / VE % NT;
         if (atomicOr(&bits[word], 1u << bit) >> bit & 1u) dev_error(a.err, GBDT_E_ARG);
       }
     }
@@ -400,7 +396,7 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
     const bool lost = r > 0.0 && !(wt == 0.0f) && (float)s_out < kLeastStat;
     if (NT <= 64 ? __any(lost) : lost) {
       // All threads of a row, and all rows of a wave, come here together; a part
-      // at a time, as the bits have room for one; class by class: few registers
+      // at a time, as the bits have room for one; vector by vector: few registers
       // for what few rows need.
       double again = 0.0, mos = 0.0;
       for (int pass = 0; pass < 2; ++pass) {
@@ -412,12 +408,18 @@ __global__ void __launch_bounds__(NT < 64 ? 64 : NT, NT <= 64 ? 6 : 8) k_distill
           mark_listed(from, to);
           __syncthreads();
 #pragma unroll 1
-          for (int32_t c = from + tid; c < to; c += NT) {
-            int32_t bit;
-            const int32_t word = place_of(c - from, bit);
-            if (bits[word] >> bit & 1u) continue;
-            const float v = Score<DT>::to_f32(xr[c]);
-            if (pass == 0) m_out = __builtin_fmaxf(m_out, v); else again += exp2_64(((double)v - mos) * a.c);
+          for (int32_t c = from + tid * VE, b = 0; c - tid * VE < to; c += NT * VE, b += VE) {
+            float f[VE];
+            load_chunk<DT>(xr, c, to, f);
+            const uint32_t in_v = bits[b / 32 * NT + tid] >> b % 32 & ((1u << VE) - 1u);
+#pragma unroll
+            for (int q = 0; q < VE; ++q) f[q] = in_v >> q & 1u ? -kInf : f[q];
+            if (pass == 0) {
+              m_out = __builtin_fmaxf(m_out, max_of(f));
+            } else {
+#pragma unroll
+              for (int q = 0; q < VE; ++q) again += exp2_64(((double)f[q] - mos) * a.c);
+            }
           }
         }
         if (pass == 0) {
