@@ -108,8 +108,8 @@ __device__ __forceinline__ double outside_factor(double s_out_s, double r, doubl
 // in flight at once: the rows are few microseconds in all, one memory latency
 // each way.  The exponentials that the loss needs are in FP64 (a row's few
 // terms do not average rounding errors away, and a small loss is what is left
-// when terms of order 1 cancel).  Vector instructions bound it, about 870 a row
-// of seven classes: step of 581,012 rows 22 us, 12 without its arithmetic.
+// when terms of order 1 cancel).  Vector instructions bound it, about 940 a row
+// of seven classes: step of 581,012 rows 23 us, 12 without its arithmetic.
 template <int DT, int R, int CMAX, int MODE>
 __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const DistillArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
 // NT * kBlk) of a row that n_parts workgroups share; a first launch (kPart)
 // leaves each part's sums, a second (kJoin) adds them up.
 //
-// Memory bounds it where rows are many: step of 4,096 x 131,072 bf16 442 us
+// Memory bounds it where rows are many: step of 4,096 x 131,072 bf16 443 us
 // (4.9 TB/s of what has to move; the second read of the scores comes from the
 // last-level cache), gradient of 2,048 x 50,001 f32 152 us (5.4 TB/s).
 //
@@ -275,8 +275,12 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_distill_rows(const Dis
 // barrier, what the vector stores left there.
 //
 // With fewer than 64 threads a row, a wave holds several rows (the last one's
-// spare threads do the last row again): step of 300,000 rows of 100 bf16 148
-// us, 511 with a wave each.
+// spare threads do the last row again): step of 300,000 rows of 100 bf16 152
+// us, 520 with a wave each.
+//
+// A gradient from statistics reads a row three times where the sum outside has
+// to be taken again: 2,048 x 50,001 f32 with all rows 200 T apart 262 us, 168
+// with none.
 constexpr int kNarrowThreads = 16, kNarrowClasses = 256, kNarrowListed = 64;
 
 template <int DT, int NT, int MODE>
@@ -572,12 +576,13 @@ void launch_block(DistillArgs a, hipStream_t s) {
 // Threads for a row: a wave up to 2,048 classes (no barrier waits for others),
 // 1,024 threads where a row is long enough to be read twice from memory: then
 // fewer rows are between their two reads at a time, and more of them are still
-// in the last-level cache (step, 4,096 x 131,072 bf16: 444 us with 1,024
-// threads, 496 with 512, 588 with 256; grad, 2,048 x 50,001 f32: 152, 161, 164).
+// in the last-level cache (step, 4,096 x 131,072 bf16: 445 us with 1,024
+// threads, 485 with 512, 578 with 256; grad, 2,048 x 50,001 f32: 155, 163, 166;
+// the loss alone, which reads once, 2,048 x 131,072 bf16: 105, 100, 101).
 // In between 256: more rows side by side hide the rows' own latencies (loss,
-// 1,000 x 32,003 f16: 20 us with 256 threads, 22 with 512, 34 with 1,024).
-// Few rows are split: 1 x 131,072 f32 takes 12 us with 32 workgroups and 26 with
-// one, 64 rows bf16 18 and 25; at 128 rows both take 27.
+// 1,000 x 32,003 f16: 21 us with 256 threads, 23 with 512, 35 with 1,024).
+// Few rows are split: 1 x 131,072 f32 takes 13 us with 32 workgroups and 28 with
+// one, 64 rows bf16 19 and 27; at 128 rows both take 28.
 template <int DT, int MODE>
 int launch_distill(const DistillArgs& args, hipStream_t s) {
   DistillArgs a = args;

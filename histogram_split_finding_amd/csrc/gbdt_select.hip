@@ -773,6 +773,12 @@ __device__ int32_t list_from(const typename Score<DT>::Elem* __restrict__ xr, in
 // the first one would cost that registers, and every row is done faster by a
 // kernel that has them.)  Each workgroup looks after the rows blockIdx.x +
 // j gridDim.x, a thread a row at a time, and lists the unfinished in LDS.
+//
+// Such rows are slow, and there are calls that have no others: a top-k above
+// GBDT_MAX_LISTED, and in rows of 513 to 2,048 classes a k that their at most 256
+// vectors cannot separate (above C / 8 in 16 bits; in f32 above C / 4 up to 1,024
+// classes, C / 8 - 32 in longer rows), so that all classes are listed: records of
+// 50,000 x 1,000 bf16 with k = 200 take 17.5 ms.
 constexpr int32_t kUnfinished = -2;
 constexpr int64_t kRestGrid = 256;
 
@@ -824,7 +830,7 @@ struct TopArgs {
 };
 
 // One workgroup per row.  A long row's time is its read (2,048 x 131,072 bf16:
-// 114 us, 4.7 TB/s; with each likely class listed on the spot 131); the threshold,
+// 118 us, 4.6 TB/s; with each likely class listed on the spot 131); the threshold,
 // the ranking and the workgroup's reductions are 5 to 8 us a row, which the
 // CU's other two workgroups cover in part.
 template <int DT, int NT>
@@ -1340,10 +1346,10 @@ __device__ __forceinline__ bool sample_row(const SampleArgs& a, int64_t i, const
   return true;
 }
 
-// FP64 bounds draws without top-k: 20 instructions a class, 57 us of 182 for
+// FP64 bounds draws without top-k: 20 instructions a class, 57 us of 191 for
 // 1,024 x 100,003 bf16 with top-p and min-p; the rest is the row's latencies
 // (threshold, ranking, cuts: 20 us) with two workgroups a CU.  Four waves a
-// SIMD: with six the pass spills (330 us).
+// SIMD: with six the pass spills (314 us).
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 4) k_sample_block(const SampleArgs a) {
   __shared__ SelLds<NT> L;
@@ -1526,10 +1532,10 @@ void launch_top_rows(const TopArgs& a, hipStream_t s) {
 }
 
 // Threads for a row: a wave up to 2,048 classes, 256 up to 40,000 (draws of
-// 2,000 x 20,000 f32: 95 us with 256, 106 with 512), then 512 (records of
-// 2,048 x 131,072 bf16: 145 us with 512, 161 with 256, 229 with 1,024, before
-// likely vectors waited); at most a row a CU: 1,024 (records of 32 such rows: 33
-// us, 38 with 512).
+// 2,000 x 20,000 f32: 95 us with 256, 104 with 512), then 512 (records of
+// 2,048 x 131,072 bf16: 126 us with 512, 147 with 256, 209 with 1,024); at most
+// a row a CU: 1,024 (records of 32 such rows: 29 us, 31 with 512; 64 draws of
+// 65,536 f32: 51 and 58).
 constexpr int64_t kFewRows = 256;
 
 template <int DT>
