@@ -87,6 +87,21 @@ class Sampling(ctypes.Structure):
     _fields_ = [("temperature", vp), ("top_k", vp), ("top_p", vp), ("min_p", vp)]
 
 
+class Policy(ctypes.Structure):
+    _fields_ = [("old_logp", vp), ("ref_logp", vp), ("advantage", vp), ("weight", vp),
+                ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("kl", ctypes.c_double)]
+
+
+class Pairs(ctypes.Structure):
+    _fields_ = [("offsets", vp), ("ref_logp", vp), ("weight", vp), ("n_pairs", i32), ("average", i32),
+                ("beta", ctypes.c_double), ("smoothing", ctypes.c_double)]
+
+
+class Routing(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_double), ("k", i32), ("score", i32), ("renormalise", i32),
+                ("n_groups", i32), ("groups_kept", i32), ("group_top", i32)]
+
+
 class GrowBuffers(ctypes.Structure):
     _fields_ = [("pp", Rows * 2), ("q", vp), ("hist_g", vp), ("hist_cnt", vp), ("splits", vp),
                 ("lists", vp), ("ctrl", vp), ("ws", vp), ("ws_bytes", ctypes.c_size_t),
@@ -159,6 +174,21 @@ def load():
         "gbdt_distill_step": (ctypes.c_int, [P(Scores), P(Teacher), ctypes.c_float, vp, vp, vp, i64, vp,
                                              ctypes.c_size_t, vp]),
         "gbdt_sample_classes": (ctypes.c_int, [P(Scores), vp, P(Sampling), vp, vp, vp, ctypes.c_size_t, vp]),
+        "gbdt_class_logp": (ctypes.c_int, [P(Scores), vp, ctypes.c_double, vp, vp, vp, ctypes.c_size_t, vp]),
+        "gbdt_class_logp_grad": (ctypes.c_int, [P(Scores), vp, ctypes.c_double, vp, vp, vp, i64, vp,
+                                                ctypes.c_size_t, vp]),
+        "gbdt_policy_loss": (ctypes.c_int, [P(Scores), vp, ctypes.c_double, P(Policy), vp, vp, vp, vp, vp,
+                                            ctypes.c_size_t, vp]),
+        "gbdt_policy_step": (ctypes.c_int, [P(Scores), vp, ctypes.c_double, P(Policy), vp, vp, vp, i64, vp,
+                                            ctypes.c_size_t, vp]),
+        "gbdt_preference_workspace_bytes": (ctypes.c_size_t, [i64, i32]),
+        "gbdt_preference_loss": (ctypes.c_int, [P(Scores), vp, ctypes.c_double, P(Pairs), vp, vp, vp, vp, vp, vp,
+                                                ctypes.c_size_t, vp]),
+        "gbdt_preference_step": (ctypes.c_int, [P(Scores), vp, ctypes.c_double, P(Pairs), vp, vp, vp, i64, vp,
+                                                ctypes.c_size_t, vp]),
+        "gbdt_route_classes": (ctypes.c_int, [P(Scores), P(Routing), vp, vp, vp, vp, ctypes.c_size_t, vp]),
+        "gbdt_route_grad": (ctypes.c_int, [P(Scores), P(Routing), vp, vp, vp, i64, vp, ctypes.c_size_t, vp]),
+        "gbdt_route_lists": (ctypes.c_int, [vp, i64, i32, vp, vp, vp, vp, ctypes.c_size_t, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -632,6 +662,199 @@ def gbdt_sample_classes(scores, u, temperature, top_k, top_p, min_p, out, logp, 
                                     _vector(logp, "logp", f32, n, scores, optional=True),
                                     wp, wb, _stream(stream))
     _check(rc, "gbdt_sample_classes")
+
+
+# --------------------------------------------- learning from drawn classes --
+
+def _here(x):
+    """Refuses tensors of a device that is not the current one: its stream would not be theirs."""
+    import torch
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        raise ValueError("tensors on %s, but the current device is cuda:%d" % (x.device, torch.cuda.current_device()))
+
+
+def _rows_of(scores, classes, ws):
+    """(Scores, rows, address of classes, workspace address, workspace bytes)"""
+    import torch
+    s = _scores(scores)
+    _here(scores)
+    return (s, (s.n_rows,), _vector(classes, "classes", torch.int32, (s.n_rows,), scores)) + _workspace(ws, scores)
+
+
+def gbdt_class_logp(scores, classes, temperature, logp, stats, ws, stream=None):
+    """logp float32 [n]: log softmax(scores / temperature) of one class a row
+    (classes int32 [n], below 0: padding), and stats float32 [n, 2] (or None) for
+    gbdt_class_logp_grad."""
+    import torch
+    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    rc = load().gbdt_class_logp(ctypes.byref(s), cp, float(temperature),
+                                _vector(logp, "logp", torch.float32, n, scores),
+                                _vector(stats, "stats", torch.float32, n + (2,), scores, optional=True),
+                                wp, wb, _stream(stream))
+    _check(rc, "gbdt_class_logp")
+
+
+def gbdt_class_logp_grad(scores, classes, temperature, stats, dlogp, grad, ws, stream=None):
+    """Backward pass of the log-probabilities, and of the losses below: grad (the
+    scores' type and shape) from dlogp float32 [n] and the forward pass's stats."""
+    import torch
+    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    rc = load().gbdt_class_logp_grad(ctypes.byref(s), cp, float(temperature),
+                                     _vector(stats, "stats", torch.float32, n + (2,), scores),
+                                     _vector(dlogp, "dlogp", torch.float32, n, scores), grad.data_ptr(),
+                                     _grad_rows(scores, grad), wp, wb, _stream(stream))
+    _check(rc, "gbdt_class_logp_grad")
+
+
+def _policy(x, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl) -> Policy:
+    import torch
+    f32 = torch.float32
+    return Policy(_vector(old_logp, "old_logp", f32, n, x), _vector(ref_logp, "ref_logp", f32, n, x, optional=True),
+                  _vector(advantage, "advantage", f32, n, x), _vector(weight, "weight", f32, n, x, optional=True),
+                  float(clip_low), float(clip_high), float(kl))
+
+
+def gbdt_policy_loss(scores, classes, temperature, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl,
+                     loss, logp, dlogp, stats, ws, stream=None):
+    """Forward pass of the clipped policy loss with a KL term.  Per row, float32
+    [n]: old_logp, ref_logp (or None: no KL term), advantage, weight (or None);
+    out: loss, logp (or None), dlogp = weight times dloss/dlogp, stats [n, 2]."""
+    import torch
+    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p = _policy(scores, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
+    f32 = torch.float32
+    rc = load().gbdt_policy_loss(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
+                                 _vector(loss, "loss", f32, n, scores),
+                                 _vector(logp, "logp", f32, n, scores, optional=True),
+                                 _vector(dlogp, "dlogp", f32, n, scores),
+                                 _vector(stats, "stats", f32, n + (2,), scores), wp, wb, _stream(stream))
+    _check(rc, "gbdt_policy_loss")
+
+
+def gbdt_policy_step(scores, classes, temperature, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl,
+                     loss, logp, grad, ws, stream=None):
+    """Loss and gradient in one call: what gbdt_policy_loss and
+    gbdt_class_logp_grad give."""
+    import torch
+    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p = _policy(scores, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
+    rc = load().gbdt_policy_step(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
+                                 _vector(loss, "loss", torch.float32, n, scores),
+                                 _vector(logp, "logp", torch.float32, n, scores, optional=True), grad.data_ptr(),
+                                 _grad_rows(scores, grad), wp, wb, _stream(stream))
+    _check(rc, "gbdt_policy_step")
+
+
+def gbdt_preference_workspace_bytes(n_rows: int, n_classes: int) -> int:
+    return int(load().gbdt_preference_workspace_bytes(int(n_rows), int(n_classes)))
+
+
+def _pairs(x, n, offsets, ref_logp, weight, beta, smoothing, average):
+    """(Pairs, pairs)"""
+    import torch
+    cuts = offsets.numel()
+    if cuts % 2 != 1:
+        raise ValueError("offsets must have 2 pairs + 1 elements")
+    f32, pairs = torch.float32, cuts // 2
+    return Pairs(_vector(offsets, "offsets", torch.int64, (cuts,), x),
+                 _vector(ref_logp, "ref_logp", f32, n, x, optional=True),
+                 _vector(weight, "weight", f32, (pairs,), x, optional=True), pairs, int(bool(average)),
+                 float(beta), float(smoothing)), pairs
+
+
+def gbdt_preference_loss(scores, classes, temperature, offsets, ref_logp, weight, beta, smoothing, average, loss,
+                         rewards, logp, dlogp, stats, ws, stream=None):
+    """Forward pass of the preference loss of pairs of row sequences (offsets int64
+    [2 pairs + 1]; ref_logp float32 [n] or None, weight float32 [pairs] or None):
+    loss float32 [pairs], rewards float32 [pairs, 2] (or None), and of the rows in
+    sequences logp, dlogp float32 [n], stats float32 [n, 2]."""
+    import torch
+    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p, pairs = _pairs(scores, n, offsets, ref_logp, weight, beta, smoothing, average)
+    f32 = torch.float32
+    rc = load().gbdt_preference_loss(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
+                                     _vector(loss, "loss", f32, (pairs,), scores),
+                                     _vector(rewards, "rewards", f32, (pairs, 2), scores, optional=True),
+                                     _vector(logp, "logp", f32, n, scores), _vector(dlogp, "dlogp", f32, n, scores),
+                                     _vector(stats, "stats", f32, n + (2,), scores), wp, wb, _stream(stream))
+    _check(rc, "gbdt_preference_loss")
+
+
+def gbdt_preference_step(scores, classes, temperature, offsets, ref_logp, weight, beta, smoothing, average, loss,
+                         rewards, grad, ws, stream=None):
+    """Loss and gradient in one call; the gradient of rows in no sequence stays as
+    it is.  ws: of gbdt_preference_workspace_bytes()."""
+    import torch
+    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p, pairs = _pairs(scores, n, offsets, ref_logp, weight, beta, smoothing, average)
+    rc = load().gbdt_preference_step(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
+                                     _vector(loss, "loss", torch.float32, (pairs,), scores),
+                                     _vector(rewards, "rewards", torch.float32, (pairs, 2), scores, optional=True),
+                                     grad.data_ptr(), _grad_rows(scores, grad), wp, wb, _stream(stream))
+    _check(rc, "gbdt_preference_step")
+
+
+# -------------------------------------------------------- routing to experts --
+
+MAX_EXPERTS = 1024
+MAX_ROUTED = 32
+
+
+def make_routing(k, sigmoid=False, renormalise=True, scale=1.0, n_groups=1, groups_kept=1, group_top=1) -> Routing:
+    return Routing(float(scale), int(k), int(bool(sigmoid)), int(bool(renormalise)), int(n_groups), int(groups_kept),
+                   int(group_top))
+
+
+def gbdt_route_classes(scores, routing, bias, classes, weights, ws, stream=None):
+    """The experts of each row of `scores` ([n, experts]) by `routing` (from
+    make_routing): classes int32 [n, k], ended by -1 where experts are out of
+    service, weights float32 [n, k]; bias float32 [experts] (or None) is added for
+    the choice alone."""
+    import torch
+    s = _scores(scores)
+    _here(scores)
+    shape = (s.n_rows, routing.k)
+    wp, wb = _workspace(ws, scores)
+    rc = load().gbdt_route_classes(ctypes.byref(s), ctypes.byref(routing),
+                                   _vector(bias, "bias", torch.float32, (s.n_classes,), scores, optional=True),
+                                   _vector(classes, "classes", torch.int32, shape, scores),
+                                   _vector(weights, "weights", torch.float32, shape, scores), wp, wb,
+                                   _stream(stream))
+    _check(rc, "gbdt_route_classes")
+
+
+def gbdt_route_grad(scores, routing, classes, dweights, grad, ws, stream=None):
+    """Backward pass of the routing weights: grad (the scores' type and shape) from
+    dweights float32 [n, k], the choice held fixed."""
+    import torch
+    s = _scores(scores)
+    _here(scores)
+    shape = (s.n_rows, routing.k)
+    wp, wb = _workspace(ws, scores)
+    rc = load().gbdt_route_grad(ctypes.byref(s), ctypes.byref(routing),
+                                _vector(classes, "classes", torch.int32, shape, scores),
+                                _vector(dweights, "dweights", torch.float32, shape, scores), grad.data_ptr(),
+                                _grad_rows(scores, grad), wp, wb, _stream(stream))
+    _check(rc, "gbdt_route_grad")
+
+
+def gbdt_route_lists(classes, n_experts, offsets, order, place, ws, stream=None):
+    """The experts' lists of places of `classes` (int32, any shape, contiguous):
+    expert e's are order[offsets[e]:offsets[e + 1]], ascending; offsets int32
+    [n_experts + 1], order int32 [places], place int32 (classes' shape, or None),
+    where each place stands in order, or -1."""
+    import torch
+    i32t, places = torch.int32, classes.numel()
+    if not classes.is_cuda:
+        raise ValueError("classes must be a device tensor")
+    _here(classes)
+    wp, wb = _workspace(ws, classes)
+    rc = load().gbdt_route_lists(_vector(classes, "classes", i32t, classes.shape, classes), places, int(n_experts),
+                                 _vector(offsets, "offsets", i32t, (int(n_experts) + 1,), classes),
+                                 _vector(order, "order", i32t, (places,), classes),
+                                 _vector(place, "place", i32t, classes.shape, classes, optional=True), wp, wb,
+                                 _stream(stream))
+    _check(rc, "gbdt_route_lists")
 
 
 # ------------------------------------------------------------ training run --

@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libgbdt_hip.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["gbdt_kernels.hip", "gbdt_driver.hip", "gbdt_predict.hip", "gbdt_distill.hip", "gbdt_select.hip"]
+SOURCES = ["gbdt_kernels.hip", "gbdt_driver.hip", "gbdt_predict.hip", "gbdt_distill.hip", "gbdt_select.hip",
+           "gbdt_policy.hip", "gbdt_route.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

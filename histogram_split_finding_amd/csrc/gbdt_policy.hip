@@ -1,0 +1,850 @@
+// Learning from drawn classes: the log-probability of a class of each row with
+// its gradient, the clipped policy loss with a KL term, and the preference loss
+// of pairs of row sequences.
+//
+// Of a row x with class a, at temperature T, with the other classes' largest
+// score m = max_{c != a} x_c and their sum against it, o = sum_{c != a} v_c,
+// v_c = exp((x_c - m) / T), which is at least 1:
+//   the logarithm of the odds against a:  L = (m - x_a) / T + log o,
+//   log p_a = -log(1 + e^L),   1 - p_a = 1 / (1 + e^-L),   p_c = (1 - p_a) v_c / o.
+// Nothing cancels or underflows on the way: a policy that is all but certain of
+// a keeps its log p_a, and its gradient, which is 1 - p_a times values of order 1,
+// to the last digit.  With d the loss's slope in log p_a, and k = (1 - p_a) d / T,
+//   gradient: k at a, -k v_c / o at the others.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <string>
+
+#include "gbdt.h"
+#include "gbdt_device.h"
+#include "gbdt_internal.h"
+#include "gbdt_scores.h"
+
+#pragma clang fp contract(off)
+
+namespace gbdt {
+
+namespace {
+
+// Where a launch takes the sums of its rows from: the scores, the statistics of
+// an earlier call, or the parts that a first launch left (kParts writes them).
+constexpr int kSums = 0, kStats = 1, kParts = 2, kJoin = 3;
+
+struct PartSum {
+  double o;
+  float m;
+  uint32_t pad;
+};
+
+struct LogpArgs {
+  const void* x;
+  int64_t n, ld;
+  const int32_t* cls;
+  int32_t C, n_parts, part_len, last;  // last: of range
+  const int64_t* range;                // rows [range[0], range[last]) only, or NULL: all
+  double c, inv_T;                     // log2(e) / T, 1 / T
+  const float *old_logp, *ref_logp, *adv, *weight;
+  double low, high, kl;  // borders of the ratio
+  float *loss, *logp, *dlogp;
+  float* stats;
+  void* grad;
+  int64_t ldg;
+  int32_t* err;
+  PartSum* parts;     // [n][n_parts]
+  uint32_t* tickets;  // [n], zero between calls
+  int64_t row0;       // of this launch
+};
+
+// The rows of the call, and one of them.
+struct Span {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ Span row_span(const LogpArgs& a) {
+  if (a.range == nullptr) return {0, a.n};
+  int64_t lo = a.range[0], hi = a.range[a.last];
+  lo = lo < 0 ? 0 : lo > a.n ? a.n : lo;
+  hi = hi < lo ? lo : hi > a.n ? a.n : hi;
+  return {lo, hi};
+}
+
+__device__ __forceinline__ int32_t row_class(const LogpArgs& a, int64_t i, bool report) {
+  const int32_t k = a.cls[i];
+  if (k < a.C) return k < 0 ? -1 : k;
+  if (report) dev_error(a.err, GBDT_E_RANGE);
+  return -1;
+}
+
+// e^y for any y (overflow: inf; NaN stays).
+__device__ __forceinline__ double exp_64(double y) {
+  const double z = y * kLog2e;
+  return z > 1023.0 ? __builtin_inf() : exp2_64(z);
+}
+
+// log(1 + e) for 0 <= e <= 1.
+__device__ __forceinline__ double log1p_64(double e) { return e < 0x1p-20 ? e - 0.5 * e * e : log_64(1.0 + e); }
+
+// A row's end: what its sums say about its class.
+struct RowEnd {
+  bool live;     // the row counts
+  double logp, against;  // log p_a, 1 - p_a
+};
+__device__ __forceinline__ RowEnd row_end(double inv_T, bool named, double m, double o, double xa) {
+  RowEnd r;
+  r.live = named && !(o == 0.0 && xa == -__builtin_inf());
+  double L = (m - xa) * inv_T + log_64(o);
+  if (o == 0.0) L = -__builtin_inf();
+  if (xa == __builtin_inf() || xa != xa) L = __builtin_nan("");
+  const double e = exp2_64(-__builtin_fabs(L) * kLog2e);
+  const double inv = rcp_64(1.0 + e);
+  r.logp = L != L ? L : (L < 0.0 ? -log1p_64(e) : -(L + log1p_64(e)));
+  r.against = L != L ? L : (L < 0.0 ? e * inv : inv);
+  return r;
+}
+
+// The clipped policy loss of a row and its slope in logp.  ratio and A: NaN stays,
+// A = 0 leaves nothing whatever the ratio.  q = e^y - y - 1, by its series where
+// the terms cancel.
+struct PolicyRow {
+  double loss, slope;
+};
+__device__ __forceinline__ PolicyRow policy_row(const LogpArgs& a, double logp, float old_logp, float ref_logp,
+                                                float advantage) {
+  const double A = advantage, ratio = exp_64(logp - (double)old_logp);
+  const double by = A == 0.0 ? 0.0 : ratio * A;
+  const double kept = ratio < a.low ? a.low : (ratio > a.high ? a.high : ratio);
+  const double cut = A == 0.0 ? 0.0 : kept * A;
+  PolicyRow r;
+  r.loss = -(by < cut || by != by ? by : cut);
+  const bool clipped = (A > 0.0 && ratio > a.high) || (A < 0.0 && ratio < a.low);
+  r.slope = clipped ? 0.0 : -by;
+  if (a.ref_logp != nullptr) {
+    const double y = (double)ref_logp - logp;
+    double q, em1;
+    if (__builtin_fabs(y) < 0x1p-5) {
+      double p = __builtin_fma(y, 1.0 / 40320.0, 1.0 / 5040.0);
+      p = __builtin_fma(y, p, 1.0 / 720.0);
+      p = __builtin_fma(y, p, 1.0 / 120.0);
+      p = __builtin_fma(y, p, 1.0 / 24.0);
+      p = __builtin_fma(y, p, 1.0 / 6.0);
+      q = y * y * __builtin_fma(y, p, 0.5);
+      em1 = y + q;
+    } else {
+      em1 = exp_64(y) - 1.0;
+      q = y == __builtin_inf() ? y : em1 - y;
+    }
+    r.loss += a.kl * q;
+    r.slope -= a.kl * em1;
+  }
+  return r;
+}
+
+struct RowIn {
+  float old_logp, ref_logp, adv, weight, dlogp;
+};
+template <int FROM>
+__device__ __forceinline__ RowIn row_in(const LogpArgs& a, int64_t i) {
+  RowIn r = {0.0f, 0.0f, 0.0f, 1.0f, 0.0f};
+  if (FROM == kStats) {
+    r.dlogp = a.dlogp[i];
+  } else if (a.adv != nullptr) {
+    r.old_logp = a.old_logp[i];
+    r.adv = a.adv[i];
+    if (a.ref_logp != nullptr) r.ref_logp = a.ref_logp[i];
+    if (a.weight != nullptr) r.weight = a.weight[i];
+  }
+  return r;
+}
+
+// Writes what a row has to say (`write`: by this thread) and returns what its
+// gradient is made of: mine at the class, scale v at the others; both 0 for a row
+// that leaves the scores alone.
+struct RowGrad {
+  bool any;
+  float mine, scale;
+};
+template <int FROM>
+__device__ __forceinline__ RowGrad row_out(const LogpArgs& a, int64_t i, bool write, bool named, const RowIn& in,
+                                           float m, double o, float xa) {
+  const RowEnd e = row_end(a.inv_T, named, m, o, xa);
+  double slope = in.dlogp;
+  if (FROM != kStats) {
+    PolicyRow p = {0.0, 0.0};
+    if (a.adv != nullptr) p = policy_row(a, e.logp, in.old_logp, in.ref_logp, in.adv);
+    slope = in.weight == 0.0f ? 0.0 : p.slope * (double)in.weight;
+    if (!e.live || xa == -kInf) slope = 0.0;
+    if (write) {
+      if (a.logp != nullptr) a.logp[i] = e.live ? (float)e.logp : 0.0f;
+      if (a.stats != nullptr) {
+        a.stats[2 * i] = e.live ? m : 0.0f;
+        a.stats[2 * i + 1] = e.live ? (float)o : 0.0f;
+      }
+      if (a.adv != nullptr) {
+        if (a.loss != nullptr) a.loss[i] = e.live ? (float)p.loss : 0.0f;
+        if (a.dlogp != nullptr) a.dlogp[i] = (float)slope;
+      }
+    }
+  }
+  RowGrad g;
+  g.any = e.live && xa != -kInf && slope != 0.0;
+  const double k = slope * a.inv_T * e.against;
+  g.mine = (float)k;
+  g.scale = o == 0.0 ? 0.0f : (float)(-k * rcp_64(o));
+  return g;
+}
+
+// The class's element of a vector of classes c0, c0 + 1, ...
+template <int VE>
+__device__ __forceinline__ void set_class(float (&f)[VE], int32_t cls, int32_t c0, float v) {
+  const uint32_t at = (uint32_t)(cls - c0);
+  if (at < (uint32_t)VE) {
+#pragma unroll
+    for (int q = 0; q < VE; ++q) f[q] = at == (uint32_t)q ? v : f[q];
+  }
+}
+
+// One thread per row of at most CMAX classes, R rows a workgroup; rows and
+// gradients pass through LDS in rows of C | 1 words, so that memory sees whole
+// lines.  The exponentials are in FP64: a row's few terms do not average rounding
+// errors away, and a ratio next to the clip's border decides about the row.
+template <int DT, int R, int CMAX, int FROM>
+__global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_logp_short(const LogpArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  extern __shared__ float lds[];
+  const Span span = row_span(a);
+  const int tid = threadIdx.x;
+  const int64_t i0 = span.lo + int64_t(blockIdx.x) * R, i = i0 + tid;
+  if (i0 >= span.hi) return;
+  const int32_t rows = (int32_t)(span.hi - i0 < R ? span.hi - i0 : R);
+  const int32_t C = a.C, P = C | 1;
+  const RowDiv by_c(C);
+  const Elem* __restrict__ xg = static_cast<const Elem*>(a.x) + i0 * a.ld;
+  const bool mine = tid < rows;
+  {
+    Staged<R, CMAX, float> xs;
+    xs.load(
+        rows, C, a.ld == C, by_c, [&](int32_t e) { return Score<DT>::to_f32(xg[(uint32_t)e]); },
+        [&](int32_t row, int32_t c) { return Score<DT>::to_f32(xg[row * a.ld + c]); });
+    xs.put(rows, C, by_c, lds);
+  }
+  int32_t cls = -1;
+  RowIn in = {};
+  float m = -kInf;
+  double o = 0.0;
+  if (mine) {
+    cls = row_class(a, i, true);
+    in = row_in<FROM>(a, i);
+    if (FROM == kStats) {
+      m = a.stats[2 * i];
+      o = a.stats[2 * i + 1];
+    }
+  }
+  __syncthreads();
+  float* __restrict__ x = lds + tid * P;
+  if (mine) {
+    const bool named = cls >= 0;
+    const float xa = named ? x[cls] : 0.0f;
+    if (FROM != kStats) {
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c)
+        if (c < C) m = c == cls ? m : __builtin_fmaxf(m, x[c]);
+      const double base = m == -kInf ? 0.0 : (double)m;
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c) {
+        if (c < C) {
+          const double v = exp2_64(((double)x[c] - base) * a.c);
+          o += c == cls ? 0.0 : v;
+          x[c] = (float)v;
+        }
+      }
+    }
+    const RowGrad g = row_out<FROM>(a, i, true, named, in, m, o, xa);
+    if (a.grad != nullptr) {
+      const float cf = exponent_scale(a.c), mf = m == -kInf ? 0.0f : m;
+#pragma unroll
+      for (int c = 0; c < CMAX; ++c) {
+        if (c < C) {
+          const float v = FROM != kStats ? x[c] : exp2_32((x[c] - mf) * cf);
+          x[c] = !g.any ? 0.0f : (c == cls ? g.mine : v * g.scale);
+        }
+      }
+    }
+  }
+  if (a.grad != nullptr) {
+    __syncthreads();
+    Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i0 * a.ldg;
+    unstage<R, CMAX>(
+        rows, C, a.ldg == C, by_c, lds, [&](int32_t e, float v) { gr[(uint32_t)e] = Score<DT>::from_f32(v); },
+        [&](int32_t row, int32_t c, float v) { gr[row * a.ldg + c] = Score<DT>::from_f32(v); });
+  }
+}
+
+// NT lanes for a row that their V vectors of 16 bytes each hold whole: one read,
+// and the maximum before the exponentials (in FP64, as above).
+template <int DT, int NT, int V, int FROM>
+__global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec;
+  const Span span = row_span(a);
+  const int lane = threadIdx.x & (NT - 1);
+  const int64_t wave0 = span.lo + a.row0 + (int64_t(blockIdx.x) * 256 + (threadIdx.x & ~63)) / NT;
+  if (wave0 >= span.hi) return;
+  const int64_t i_all = wave0 + (threadIdx.x & 63) / NT;
+  const bool mine = i_all < span.hi;
+  const int64_t i = mine ? i_all : span.hi - 1;
+  const int32_t C = a.C, c0 = lane * VE;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  Vec16<DT> raw[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) raw[j] = load_tail<DT>(xr, c0 + j * NT * VE, C);
+  const int32_t cls = row_class(a, i, mine && lane == 0);
+  const bool named = cls >= 0;
+  const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
+  const RowIn in = row_in<FROM>(a, i);
+  float m = -kInf;
+  double o = 0.0;
+  if (FROM == kStats) {
+    m = a.stats[2 * i];
+    o = a.stats[2 * i + 1];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      unpack<DT>(raw[j], f);
+      set_class<VE>(f, cls, c0 + j * NT * VE, -kInf);
+      m = __builtin_fmaxf(m, max_of(f));
+    }
+    m = group_max<NT>(m);
+    const double base = m == -kInf ? 0.0 : (double)m;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j > 0 && j * NT * VE >= C) break;
+      float f[VE];
+      unpack<DT>(raw[j], f);
+      set_class<VE>(f, cls, c0 + j * NT * VE, -kInf);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) o += exp2_64(((double)f[q] - base) * a.c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    o = group_sum<NT>(o);
+  }
+  const RowGrad g = row_out<FROM>(a, i, mine && lane == 0, named, in, m, o, xa);
+  if (a.grad != nullptr && mine) {
+    Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
+    const float cf = exponent_scale(a.c), mf = m == -kInf ? 0.0f : m;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j > 0 && j * NT * VE >= C) break;
+      float f[VE];
+      unpack<DT>(raw[j], f);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = g.any ? exp2_32((f[q] - mf) * cf) * g.scale : 0.0f;
+      if (g.any) set_class<VE>(f, cls, c0 + j * NT * VE, g.mine);
+      store_tail<DT>(gr, c0 + j * NT * VE, C, pack<DT>(f));
+    }
+  }
+}
+
+// One workgroup per row, or per part of one: part_len classes (a multiple of
+// NT * kBlk) of a row that n_parts workgroups share.  The sum is taken against a
+// reference that is the first maximum the thread meets and moves only when a
+// score is above it by 2^20 in the exponential; a second read writes the gradient.
+// Parts leave their sums behind; where no gradient follows, the last workgroup of
+// a row to arrive adds them up, else a second launch does.
+template <int DT, int NT, int FROM>
+__global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec, BLK = kBlk<DT>, W = NT / 64;
+  __shared__ float sh_m[W];
+  __shared__ double sh_o[W];
+  __shared__ int sh_last;
+  const Span span = row_span(a);
+  const int tid = threadIdx.x;
+  const float cf = exponent_scale(a.c);
+  const uint32_t in_launch = a.n_parts > 1 ? blockIdx.x / (uint32_t)a.n_parts : blockIdx.x;
+  const int32_t part = (int32_t)(blockIdx.x - in_launch * (uint32_t)a.n_parts);
+  const int64_t row = a.row0 + in_launch, i = span.lo + row;
+  if (i >= span.hi) return;
+  const int32_t lo = part * a.part_len;
+  const int32_t hi = a.C - lo < a.part_len ? a.C : lo + a.part_len;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  const int32_t cls = row_class(a, i, tid == 0 && part == 0);
+  const bool named = cls >= 0;
+  float m = -kInf;
+  double o = 0.0;
+  if ((FROM == kSums || FROM == kParts) && named) {
+    float ref = -kInf;
+    const int32_t c0 = tid * VE;
+    for (int32_t base = lo; base < hi; base += NT * BLK) {
+      const RawBlock<DT> raw = load_block<DT, NT>(xr, base, hi);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        float f[VE];
+        unpack<DT>(raw.v[j], f);
+        set_class<VE>(f, cls, base + c0 + j * NT * VE, -kInf);
+        const float vm = max_of(f);
+        m = __builtin_fmaxf(m, vm);
+        if ((vm - ref) * cf > 20.0f) {  // (the first finite score among them)
+          o *= exp2_64(((double)ref - (double)vm) * a.c);
+          ref = vm;
+        }
+        const float rf = ref == -kInf ? 0.0f : ref;
+#pragma unroll
+        for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - rf) * cf);
+        o += (double)sum_of(f);
+        __builtin_amdgcn_sched_barrier(0);  // (vector by vector: fewer registers)
+      }
+    }
+    const float mine = m;
+    m = block_max<NT>(m, sh_m);
+    if (ref != m && mine != -kInf) o *= exp2_64(((double)ref - (double)m) * a.c);
+    o = block_sum<NT>(o, sh_o);
+  }
+  if constexpr (FROM == kParts) {
+    PartSum* __restrict__ parts = a.parts + row * a.n_parts;
+    if (tid == 0) {
+      __hip_atomic_store(&parts[part].o, o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&parts[part].m, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (a.grad != nullptr) return;
+    if (tid == 0) {
+      const uint32_t before = __hip_atomic_fetch_add(&a.tickets[row], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      sh_last = before == (uint32_t)a.n_parts - 1u;
+    }
+    __syncthreads();
+    if (!sh_last) return;
+    if (tid == 0) __hip_atomic_store(&a.tickets[row], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if constexpr (FROM == kJoin || FROM == kParts) {
+    PartSum* __restrict__ parts = a.parts + row * a.n_parts;
+    float part_m = -kInf;
+    double part_o = 0.0;
+    if (tid < a.n_parts) {  // (at most 64 parts, as many as a row has steps of the split)
+      part_o = __hip_atomic_load(&parts[tid].o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      part_m = __hip_atomic_load(&parts[tid].m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    m = block_max<NT>(part_m, sh_m);
+    if (part_m != m && part_m != -kInf) part_o *= exp2_64(((double)part_m - (double)m) * a.c);
+    o = block_sum<NT>(part_o, sh_o);
+  } else if constexpr (FROM == kStats) {
+    m = a.stats[2 * i];
+    o = a.stats[2 * i + 1];
+  }
+  const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
+  const bool write = tid == 0 && (FROM == kParts || part == 0);
+  const RowGrad g = row_out<FROM>(a, i, write, named, row_in<FROM>(a, i), m, o, xa);
+  if (FROM != kParts && a.grad != nullptr) {
+    const float mf = m == -kInf ? 0.0f : m;
+    Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
+    for (int32_t base = lo; base < hi; base += NT * BLK) {
+      RawBlock<DT> out = {};
+      if (g.any) {
+        const RawBlock<DT> raw = load_block<DT, NT>(xr, base, hi);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+          float f[VE];
+          unpack<DT>(raw.v[j], f);
+#pragma unroll
+          for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - mf) * cf) * g.scale;
+          set_class<VE>(f, cls, base + tid * VE + j * NT * VE, g.mine);
+          out.v[j] = pack<DT>(f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      store_block<DT, NT>(gr, base, hi, out);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- pairs --
+
+struct PairArgs {
+  const int64_t* offsets;
+  const float *ref_logp, *weight;
+  double beta, smoothing;
+  int64_t n;
+  int32_t n_pairs, average;
+  const float *logp, *stats;
+  float *loss, *rewards, *dlogp;
+  int32_t* err;
+};
+
+// One workgroup per pair: the two sequences' sums of logp - ref over the rows that
+// count (statistics other than (0, 0)), in FP64 in a fixed order, then the slope of
+// each row.
+constexpr int kPairThreads = 256;
+__global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
+  __shared__ double sh[2][2][kPairThreads / 64];
+  const int tid = threadIdx.x, wid = tid >> 6;
+  const int64_t p = blockIdx.x;
+  int64_t cut[3];
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < 3; ++u) {
+    const int64_t v = a.offsets[2 * p + u];
+    const int64_t from = u == 0 ? 0 : cut[u - 1];
+    cut[u] = v < from ? from : v > a.n ? a.n : v;
+    bad = bad || cut[u] != v;
+  }
+  if (bad && tid == 0) dev_error(a.err, GBDT_E_RANGE);
+  double sum[2], count[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    sum[s] = 0.0;
+    int64_t rows = 0;
+    for (int64_t i = cut[s] + tid; i < cut[s + 1]; i += kPairThreads) {
+      if (a.stats[2 * i] == 0.0f && a.stats[2 * i + 1] == 0.0f) continue;
+      sum[s] += (double)a.logp[i] - (a.ref_logp == nullptr ? 0.0 : (double)a.ref_logp[i]);
+      ++rows;
+    }
+    sum[s] = wave_sum(sum[s]);
+    count[s] = wave_sum((double)rows);
+    if ((tid & 63) == 0) {
+      sh[s][0][wid] = sum[s];
+      sh[s][1][wid] = count[s];
+    }
+  }
+  __syncthreads();
+  double per[2], reward[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    sum[s] = across_waves<kPairThreads / 64>(sh[s][0], [](double u, double v) { return u + v; });
+    count[s] = across_waves<kPairThreads / 64>(sh[s][1], [](double u, double v) { return u + v; });
+    per[s] = a.average && count[s] > 1.0 ? 1.0 / count[s] : 1.0;
+    reward[s] = a.beta * sum[s] * per[s];
+  }
+  // (1 - e) log(1 + e^-z) + e log(1 + e^z), and its slope
+  const double z = reward[0] - reward[1], e = a.smoothing;
+  const double near = exp_64(-__builtin_fabs(z)), inv = 1.0 / (1.0 + near), tail = log1p_64(near);
+  const double up = z < 0.0 ? near * inv : inv, down = z < 0.0 ? inv : near * inv;  // 1 / (1 + e^-z), 1 / (1 + e^z)
+  const double lose = (z < 0.0 ? -z : 0.0) + tail, win = (z > 0.0 ? z : 0.0) + tail;
+  double loss = (1.0 - e) * lose + (e == 0.0 ? 0.0 : e * win);
+  double slope = e * up - (1.0 - e) * down;
+  if (z != z) loss = slope = z;
+  if (tid == 0) {
+    if (a.loss != nullptr) a.loss[p] = (float)loss;
+    if (a.rewards != nullptr) {
+      a.rewards[2 * p] = (float)reward[0];
+      a.rewards[2 * p + 1] = (float)reward[1];
+    }
+  }
+  const float wt = a.weight == nullptr ? 1.0f : a.weight[p];
+  slope = wt == 0.0f ? 0.0 : slope * (double)wt * a.beta;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const float d = (float)((s == 0 ? slope : -slope) * per[s]);
+    for (int64_t i = cut[s] + tid; i < cut[s + 1]; i += kPairThreads) {
+      const bool counts = !(a.stats[2 * i] == 0.0f && a.stats[2 * i + 1] == 0.0f) && a.logp[i] != -kInf;
+      a.dlogp[i] = counts ? d : 0.0f;
+    }
+  }
+}
+
+// -------------------------------------------------------------------- host --
+
+template <int DT, int R, int CMAX, int FROM>
+void launch_short(const LogpArgs& a, hipStream_t s) {
+  const size_t lds = size_t(R) * 4 * (a.C | 1);
+  diag_begin(kDiagClassLogp, s);
+  hipLaunchKernelGGL((k_logp_short<DT, R, CMAX, FROM>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
+  diag_end(s);
+}
+
+template <int DT, int NT, int V, int FROM>
+void launch_wave(LogpArgs a, hipStream_t s) {
+  constexpr int64_t kRows = 256 / NT;
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid * kRows) {
+    const int64_t left = (a.n - a.row0 + kRows - 1) / kRows;
+    diag_begin(kDiagClassLogp, s);
+    hipLaunchKernelGGL((k_logp_wave<DT, NT, V, FROM>), dim3((unsigned)(left < kMaxRowGrid ? left : kMaxRowGrid)),
+                       dim3(256), 0, s, a);
+    diag_end(s);
+  }
+}
+
+template <int DT, int NT, int FROM>
+void launch_block(LogpArgs a, hipStream_t s) {
+  constexpr int32_t kStep = NT * kBlk<DT>;
+  if (a.n_parts == 1) a.part_len = (a.C + kStep - 1) / kStep * kStep;
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
+    const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
+    diag_begin(kDiagClassLogp, s);
+    hipLaunchKernelGGL((k_logp_block<DT, NT, FROM>), dim3((unsigned)(n * a.n_parts)), dim3(NT), 0, s, a);
+    diag_end(s);
+  }
+}
+
+// Threads for a row as the distillation has them: one up to 32 classes, up to a
+// wave while its registers hold the row, then a workgroup, 1,024 threads where
+// rows are long enough to be read twice from memory; few long rows are split.
+template <int DT, int FROM>
+int launch_logp(LogpArgs a, hipStream_t s) {
+  constexpr int VE = Score<DT>::kVec;
+  constexpr int32_t kPartStep = 256 * kBlk<DT>;
+  a.n_parts = 1;
+  a.part_len = 0;
+  const int32_t vecs = (a.C + VE - 1) / VE, steps = (a.C + kPartStep - 1) / kPartStep;
+  if (a.C <= 8) {
+    launch_short<DT, 64, 8, FROM>(a, s);
+  } else if (a.C <= 16) {
+    launch_short<DT, 128, 16, FROM>(a, s);
+  } else if (a.C <= kRowsMaxClasses) {
+    launch_short<DT, 64, 32, FROM>(a, s);
+  } else if (vecs <= 8) {
+    launch_wave<DT, 8, 1, FROM>(a, s);
+  } else if (vecs <= 16) {
+    launch_wave<DT, 8, 2, FROM>(a, s);
+  } else if (vecs <= 32) {
+    launch_wave<DT, 8, 4, FROM>(a, s);
+  } else if (vecs <= 64) {
+    launch_wave<DT, 16, 4, FROM>(a, s);
+  } else if (vecs <= 128) {
+    launch_wave<DT, 32, 4, FROM>(a, s);
+  } else if (vecs <= 256) {
+    launch_wave<DT, 64, 4, FROM>(a, s);
+  } else if (DT == GBDT_DTYPE_F32 && vecs <= 512) {
+    launch_wave<DT, 64, 8, FROM>(a, s);
+  } else if (a.n <= kSplitRows && steps >= 4) {
+    const int32_t want = (int32_t)(kSplitGrid / a.n);
+    const int32_t per = (steps + want - 1) / want;
+    a.part_len = per * kPartStep;
+    a.n_parts = (steps + per - 1) / per;
+    if constexpr (FROM == kSums) {
+      launch_block<DT, 256, kParts>(a, s);
+      if (a.grad != nullptr) launch_block<DT, 256, kJoin>(a, s);
+    } else {
+      launch_block<DT, 256, FROM>(a, s);
+    }
+  } else if (a.C <= 40000) {
+    launch_block<DT, 256, FROM>(a, s);
+  } else {
+    launch_block<DT, 1024, FROM>(a, s);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_logp");
+}
+
+template <int FROM>
+int launch_logp(int32_t dtype, const LogpArgs& a, hipStream_t s) {
+  switch (dtype) {
+    case GBDT_DTYPE_F32: return launch_logp<GBDT_DTYPE_F32, FROM>(a, s);
+    case GBDT_DTYPE_BF16: return launch_logp<GBDT_DTYPE_BF16, FROM>(a, s);
+    default: return launch_logp<GBDT_DTYPE_F16, FROM>(a, s);
+  }
+}
+
+int check_logp(const gbdt_scores* x, double temperature) {
+  const int rc = check_scores(x);
+  if (rc) return rc;
+  if (!(temperature >= 1e-30) || !(temperature <= 1e30)) return fail(GBDT_E_ARG, "temperature out of [1e-30, 1e30]");
+  return GBDT_OK;
+}
+
+LogpArgs logp_args(const gbdt_scores& x, const int32_t* classes, double temperature, void* ws) {
+  LogpArgs a = {};
+  a.x = x.data;
+  a.n = x.n_rows;
+  a.ld = x.row_stride;
+  a.C = x.n_classes;
+  a.cls = classes;
+  a.c = kLog2e / temperature;
+  a.inv_T = 1.0 / temperature;
+  a.err = &static_cast<WsCtrl*>(ws)->err;
+  a.parts = reinterpret_cast<PartSum*>(static_cast<char*>(ws) + sizeof(WsCtrl));
+  a.tickets = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + sizeof(WsCtrl) + kScoresPartBytes);
+  return a;
+}
+
+int check_policy(const gbdt_policy* p) {
+  if (!p) return fail(GBDT_E_ARG, "policy is null");
+  if (!(p->clip_low >= 0.0) || !(p->clip_low <= 1.0)) return fail(GBDT_E_ARG, "clip_low out of [0, 1]");
+  if (!(p->clip_high >= 0.0)) return fail(GBDT_E_ARG, "clip_high must be >= 0");
+  if (!(p->kl >= 0.0) || !std::isfinite(p->kl)) return fail(GBDT_E_ARG, "kl must be finite and >= 0");
+  return GBDT_OK;
+}
+
+int policy(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_policy* p, float* loss,
+           float* logp, float* dlogp, float* stats, void* grad, int64_t grad_stride, bool step, void* ws,
+           size_t ws_bytes, hipStream_t s) {
+  int rc = check_logp(x, temperature);
+  if (!rc) rc = check_policy(p);
+  if (rc) return rc;
+  if (x->n_rows == 0) return GBDT_OK;
+  if (!classes || !p->old_logp || !p->advantage) return fail(GBDT_E_ARG, "classes, old_logp or advantage is null");
+  if (!loss) return fail(GBDT_E_ARG, "loss is null");
+  if (!step && (!dlogp || !stats)) return fail(GBDT_E_ARG, "dlogp or stats is null");
+  if (step) rc = check_grad(*x, grad, grad_stride);
+  if (!rc) rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  LogpArgs a = logp_args(*x, classes, temperature, ws);
+  a.old_logp = p->old_logp;
+  a.ref_logp = p->kl == 0.0 ? nullptr : p->ref_logp;
+  a.adv = p->advantage;
+  a.weight = p->weight;
+  a.low = 1.0 - p->clip_low;
+  a.high = 1.0 + p->clip_high;
+  a.kl = p->kl;
+  a.loss = loss;
+  a.logp = logp;
+  a.dlogp = dlogp;
+  a.stats = stats;
+  a.grad = grad;
+  a.ldg = grad_stride;
+  return launch_logp<kSums>(x->dtype, a, s);
+}
+
+int check_pairs(const gbdt_pairs* p) {
+  if (!p) return fail(GBDT_E_ARG, "pairs is null");
+  if (p->n_pairs < 0 || p->n_pairs > 1 << 29) return fail(GBDT_E_ARG, "n_pairs out of [0, 2^29]");
+  if (!std::isfinite(p->beta)) return fail(GBDT_E_ARG, "beta must be finite");
+  if (!(p->smoothing >= 0.0) || !(p->smoothing < 0.5)) return fail(GBDT_E_ARG, "smoothing out of [0, 1/2)");
+  return GBDT_OK;
+}
+
+int launch_pairs(const gbdt_pairs& p, int64_t n_rows, const float* logp, const float* stats, float* loss,
+                 float* rewards, float* dlogp, void* ws, hipStream_t s) {
+  PairArgs a = {};
+  a.offsets = p.offsets;
+  a.ref_logp = p.ref_logp;
+  a.weight = p.weight;
+  a.beta = p.beta;
+  a.smoothing = p.smoothing;
+  a.n = n_rows;
+  a.n_pairs = p.n_pairs;
+  a.average = p.average;
+  a.logp = logp;
+  a.stats = stats;
+  a.loss = loss;
+  a.rewards = rewards;
+  a.dlogp = dlogp;
+  a.err = &static_cast<WsCtrl*>(ws)->err;
+  diag_begin(kDiagPairs, s);
+  hipLaunchKernelGGL(k_pairs, dim3((unsigned)p.n_pairs), dim3(kPairThreads), 0, s, a);
+  diag_end(s);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_pairs");
+}
+
+}  // namespace
+
+int check_grad(const gbdt_scores& x, const void* grad, int64_t grad_stride) {
+  if (!grad) return fail(GBDT_E_ARG, "grad is null");
+  if (x.n_rows > 1 && grad_stride < x.n_classes) return fail(GBDT_E_SHAPE, "grad_stride smaller than n_classes");
+  const uintptr_t es = x.dtype == GBDT_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(grad) % es) return fail(GBDT_E_ARG, "grad is misaligned");
+  return GBDT_OK;
+}
+
+}  // namespace gbdt
+
+using namespace gbdt;
+
+extern "C" {
+
+int gbdt_class_logp(const gbdt_scores* x, const int32_t* classes, double temperature, float* logp, float* stats,
+                    void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_logp(x, temperature);
+  if (rc) return rc;
+  if (x->n_rows == 0) return GBDT_OK;
+  if (!classes || !logp) return fail(GBDT_E_ARG, "classes or logp is null");
+  rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  LogpArgs a = logp_args(*x, classes, temperature, ws);
+  a.logp = logp;
+  a.stats = stats;
+  return launch_logp<kSums>(x->dtype, a, reinterpret_cast<hipStream_t>(stream));
+}
+
+int gbdt_class_logp_grad(const gbdt_scores* x, const int32_t* classes, double temperature, const float* stats,
+                         const float* dlogp, void* grad, int64_t grad_stride, void* ws, size_t ws_bytes,
+                         void* stream) {
+  int rc = check_logp(x, temperature);
+  if (rc) return rc;
+  if (x->n_rows == 0) return GBDT_OK;
+  if (!classes || !stats || !dlogp) return fail(GBDT_E_ARG, "classes, stats or dlogp is null");
+  rc = check_grad(*x, grad, grad_stride);
+  if (!rc) rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  LogpArgs a = logp_args(*x, classes, temperature, ws);
+  a.stats = const_cast<float*>(stats);  // (read only, as dlogp)
+  a.dlogp = const_cast<float*>(dlogp);
+  a.grad = grad;
+  a.ldg = grad_stride;
+  return launch_logp<kStats>(x->dtype, a, reinterpret_cast<hipStream_t>(stream));
+}
+
+int gbdt_policy_loss(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_policy* p,
+                     float* loss, float* logp, float* dlogp, float* stats, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return policy(x, classes, temperature, p, loss, logp, dlogp, stats, nullptr, 0, false, ws, ws_bytes,
+                reinterpret_cast<hipStream_t>(stream));
+}
+
+int gbdt_policy_step(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_policy* p,
+                     float* loss, float* logp, void* grad, int64_t grad_stride, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return policy(x, classes, temperature, p, loss, logp, nullptr, nullptr, grad, grad_stride, true, ws, ws_bytes,
+                reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t gbdt_preference_workspace_bytes(int64_t n_rows, int32_t n_classes) {
+  const size_t rows = gbdt_scores_workspace_bytes(n_rows, n_classes);
+  // a row's logp, slope and statistics
+  return rows == 0 ? 0 : (rows + 255) / 256 * 256 + size_t(n_rows) * 16;
+}
+
+int gbdt_preference_loss(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_pairs* p,
+                         float* loss, float* rewards, float* logp, float* dlogp, float* stats, void* ws,
+                         size_t ws_bytes, void* stream) {
+  int rc = check_logp(x, temperature);
+  if (!rc) rc = check_pairs(p);
+  if (rc) return rc;
+  if (p->n_pairs == 0) return GBDT_OK;
+  if (!p->offsets || !loss) return fail(GBDT_E_ARG, "offsets or loss is null");
+  if (x->n_rows > 0) {
+    if (!classes) return fail(GBDT_E_ARG, "classes is null");
+    if (!logp || !dlogp || !stats) return fail(GBDT_E_ARG, "logp, dlogp or stats is null");
+  }
+  rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (x->n_rows > 0) {
+    LogpArgs a = logp_args(*x, classes, temperature, ws);
+    a.range = p->offsets;
+    a.last = 2 * p->n_pairs;
+    a.logp = logp;
+    a.stats = stats;
+    rc = launch_logp<kSums>(x->dtype, a, s);
+    if (rc) return rc;
+  }
+  return launch_pairs(*p, x->n_rows, logp, stats, loss, rewards, dlogp, ws, s);
+}
+
+int gbdt_preference_step(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_pairs* p,
+                         float* loss, float* rewards, void* grad, int64_t grad_stride, void* ws, size_t ws_bytes,
+                         void* stream) {
+  int rc = check_logp(x, temperature);
+  if (!rc) rc = check_pairs(p);
+  if (rc) return rc;
+  if (p->n_pairs == 0) return GBDT_OK;
+  if (x->n_rows > 0) rc = check_grad(*x, grad, grad_stride);
+  if (rc) return rc;
+  if (ws_bytes < gbdt_preference_workspace_bytes(x->n_rows, x->n_classes))
+    return fail(GBDT_E_ARG, "workspace smaller than gbdt_preference_workspace_bytes()");
+  const size_t rows = (gbdt_scores_workspace_bytes(x->n_rows, x->n_classes) + 255) / 256 * 256;
+  float* logp = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
+  float *dlogp = logp + x->n_rows, *stats = dlogp + x->n_rows;
+  rc = gbdt_preference_loss(x, classes, temperature, p, loss, rewards, logp, dlogp, stats, ws, ws_bytes, stream);
+  if (rc || x->n_rows == 0) return rc;
+  LogpArgs a = logp_args(*x, classes, temperature, ws);
+  a.range = p->offsets;
+  a.last = 2 * p->n_pairs;
+  a.stats = stats;
+  a.dlogp = dlogp;
+  a.grad = grad;
+  a.ldg = grad_stride;
+  return launch_logp<kStats>(x->dtype, a, reinterpret_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

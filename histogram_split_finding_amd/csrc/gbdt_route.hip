@@ -1,0 +1,698 @@
+// Rows sent to experts: the choice of k experts a row with their weights, the
+// weights' gradient, and the experts' lists of places.
+//
+// With s the softmax or sigmoid values of a row's scores, J the chosen experts and
+// d_j = dweight_j:
+//   weight_j = scale s_j / N,  N = sum_J s or 1,
+//   ds_j = scale (d_j - [renormalised] sum_J d s / N) / N,
+//   sigmoid:  dx_j = ds_j s_j (1 - s_j),
+//   softmax:  dx_c = s_c ([c in J] ds_c - sum_J ds s), whose second sum is 0 where
+// the weights are renormalised: then, as with sigmoid values, the gradient is 0
+// outside J.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <string>
+
+#include "gbdt.h"
+#include "gbdt_device.h"
+#include "gbdt_internal.h"
+#include "gbdt_scores.h"
+
+#pragma clang fp contract(off)
+
+namespace gbdt {
+
+namespace {
+
+constexpr int kRouteThreads = 256;
+constexpr float kMaxF32 = 3.40282346638528859812e38f;
+
+struct RouteArgs {
+  const void* x;
+  int64_t n, ld;
+  int32_t E, k;
+  int32_t sigmoid, renorm, by_value;
+  int32_t groups, kept, top, group_size;
+  int32_t per_lane;   // experts of a lane, at most EPL
+  int32_t log_lanes;  // lanes of a group of experts, as a power of two
+  double scale;
+  const float* bias;
+  int32_t* classes;
+  float* weights;
+  const float* dweights;
+  void* grad;
+  int64_t ldg;
+  int32_t* err;
+};
+
+// A score as the softmax has it: NaN is out of service, +inf the largest number.
+__device__ __forceinline__ float in_service(float f) { return f == f ? __builtin_fminf(f, kMaxF32) : -kInf; }
+
+// A lane's value from another one of its row of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
+  return __hiloint2double(hi, lo);
+}
+// The largest value of NT neighbouring lanes, in all of them; no NaN among them.
+template <int NT>
+__device__ __forceinline__ double lanes_max(double v) {
+  if constexpr (NT >= 2) v = __builtin_fmax(v, dpp_f64<0xB1>(v));   // quad_perm 1, 0, 3, 2
+  if constexpr (NT >= 4) v = __builtin_fmax(v, dpp_f64<0x4E>(v));   // quad_perm 2, 3, 0, 1
+  if constexpr (NT >= 8) v = __builtin_fmax(v, dpp_f64<0x141>(v));  // row_half_mirror
+  if constexpr (NT >= 16) v = __builtin_fmax(v, dpp_f64<0x140>(v)); // row_mirror
+  if constexpr (NT >= 32) v = __builtin_fmax(v, __shfl_xor(v, 16, 64));
+  if constexpr (NT >= 64) v = __builtin_fmax(v, __shfl_xor(v, 32, 64));
+  return v;
+}
+
+__device__ __forceinline__ double sigmoid_64(float x) {
+  const double e = exp2_64(-(double)__builtin_fabsf(x) * kLog2e);
+  const double inv = rcp_64(1.0 + e);
+  return x < 0.0f ? e * inv : inv;
+}
+
+// NT lanes a row, EPL experts a lane at most, neighbours, and no lane with experts of
+// two groups: of equal values the first is in the lowest lane that has one.  The
+// choice takes k rounds: the row's largest value by lane moves, the lane that has
+// it by a ballot.
+template <int DT, int NT, int EPL>
+__global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec, V = (EPL + VE - 1) / VE;
+  constexpr int kRows = kRouteThreads / NT;
+  __shared__ int32_t all_chosen[kRows][GBDT_MAX_ROUTED];
+  const int lane = threadIdx.x & (NT - 1), sub = threadIdx.x / NT;
+  const int first_lane = (threadIdx.x & 63) & ~(NT - 1);  // of the row, in the wave
+  const int64_t row = int64_t(blockIdx.x) * kRows + sub;
+  const bool mine = row < a.n;
+  const int64_t i = mine ? row : a.n - 1;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  int32_t* __restrict__ chosen = all_chosen[sub];
+  const int32_t group = lane >> a.log_lanes, within = lane & ((1 << a.log_lanes) - 1);
+  const int32_t group_end = (group + 1) * a.group_size;
+  int32_t e0 = group * a.group_size + within * a.per_lane, e1 = e0 + a.per_lane;
+  e1 = e1 < group_end ? e1 : group_end;
+  if (group >= a.groups || e0 >= e1) e0 = e1 = 0;
+  const int32_t count = e1 - e0;
+  float x[V * VE];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float f[VE];
+    load_chunk<DT>(xr, e0 + j * VE, e1, f);
+#pragma unroll
+    for (int q = 0; q < VE; ++q) x[j * VE + q] = f[q] == f[q] ? f[q] : -kInf;
+  }
+  // the softmax's maximum and sum
+  double top_x = 0.0, total = 1.0;
+  if (!a.sigmoid && (a.by_value || !a.renorm)) {
+    float m = -kInf;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) m = __builtin_fmaxf(m, x[e]);
+    m = __builtin_fminf(group_max<NT>(m), kMaxF32);
+    top_x = m == -kInf ? 0.0 : (double)m;
+  }
+  double v[EPL];
+  if (a.sigmoid) {
+    if (a.by_value) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[e] = sigmoid_64(x[e]);
+    }
+  } else if (a.by_value || !a.renorm) {
+    total = 0.0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      v[e] = exp2_64(((double)__builtin_fminf(x[e], kMaxF32) - top_x) * kLog2e);
+      total += v[e];
+    }
+    total = group_sum<NT>(total);
+    const double inv = total > 0.0 ? 1.0 / total : 0.0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) v[e] *= inv;
+    total = inv;
+  }
+  if (a.by_value) {
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)
+        if (e < count) v[e] += (double)a.bias[e0 + e];
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) v[e] = x[e] > -kInf && v[e] == v[e] ? v[e] : -__builtin_inf();
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) v[e] = (double)x[e];
+  }
+  if (a.groups > 1) {
+    // a group's two largest: of a lane's, then of its lanes'
+    double t1 = -__builtin_inf(), t2 = t1;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      t2 = __builtin_fmax(t2, __builtin_fmin(t1, v[e]));
+      t1 = __builtin_fmax(t1, v[e]);
+    }
+    for (int off = 1; off < 1 << a.log_lanes; off <<= 1) {
+      const double o1 = __shfl_xor(t1, off, 64), o2 = __shfl_xor(t2, off, 64);
+      t2 = __builtin_fmax(__builtin_fmax(t2, o2), __builtin_fmin(t1, o1));
+      t1 = __builtin_fmax(t1, o1);
+    }
+    double rank = t1;
+    if (a.top == 2 && t2 > -__builtin_inf()) rank = t1 + t2;
+    rank = rank == rank ? rank : -__builtin_inf();
+    int32_t before = 0;  // groups ahead of this one
+    for (int32_t g = 0; g < a.groups; ++g) {
+      const double other = __shfl(rank, first_lane + (g << a.log_lanes), 64);
+      before += other > rank || (other == rank && g < group);
+    }
+    if (before >= a.kept) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[e] = -__builtin_inf();
+    }
+  }
+  // (classes -1 where nothing is left)
+  for (int32_t j = lane; j < a.k; j += NT) chosen[j] = -1;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  for (int32_t j = 0; j < a.k; ++j) {
+    double best = v[0];
+#pragma unroll
+    for (int e = 1; e < EPL; ++e) best = __builtin_fmax(best, v[e]);
+    const double top = lanes_max<NT>(best);
+    const bool has = best == top && top > -__builtin_inf();
+    const uint64_t who = __ballot(has) >> first_lane & (~uint64_t(0) >> (64 - NT));
+    if (has && lane == __ffsll((unsigned long long)who) - 1) {
+      int32_t at = EPL;
+#pragma unroll
+      for (int e = EPL - 1; e >= 0; --e) at = v[e] == top ? e : at;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[e] = e == at ? -__builtin_inf() : v[e];
+      chosen[j] = e0 + at;
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  // the weights of places lane, lane + NT, ...
+  constexpr int kMost = (GBDT_MAX_ROUTED + NT - 1) / NT;
+  double s[kMost], sum = 0.0;
+  int32_t cls[kMost];
+  float xc[kMost], m = -kInf;
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    const int32_t j = lane + u * NT;
+    cls[u] = j < a.k ? chosen[j] : -1;
+    xc[u] = -kInf;
+    if (cls[u] >= 0) xc[u] = __builtin_fminf(Score<DT>::to_f32(xr[cls[u]]), kMaxF32);
+    m = __builtin_fmaxf(m, xc[u]);
+  }
+  if (!a.sigmoid && a.renorm) {
+    // of the chosen alone: against the largest of them
+    m = group_max<NT>(m);
+    top_x = m == -kInf ? 0.0 : (double)m;
+    total = 1.0;
+  }
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    s[u] = 0.0;
+    if (cls[u] >= 0)
+      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - top_x) * kLog2e) * total;
+    sum += s[u];
+  }
+  double by = a.scale;
+  if (a.renorm) {
+    sum = group_sum<NT>(sum);
+    by = sum > 0.0 ? a.scale / sum : 0.0;
+  }
+  if (mine) {
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+      const int32_t j = lane + u * NT;
+      if (j < a.k) {
+        a.classes[row * a.k + j] = cls[u];
+        a.weights[row * a.k + j] = (float)(s[u] * by);
+      }
+    }
+  }
+}
+
+// NT lanes a row that their V vectors of 16 bytes each hold whole.  A word per
+// expert in LDS says which place of the list has it.
+template <int DT, int NT, int V>
+__global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec, kRows = kRouteThreads / NT, W = NT * V * VE;
+  constexpr int kMost = (GBDT_MAX_ROUTED + NT - 1) / NT;
+  __shared__ uint32_t all_place[kRows][W / 4];  // a byte per expert
+  __shared__ float all_value[kRows][GBDT_MAX_ROUTED];
+  const int lane = threadIdx.x & (NT - 1), sub = threadIdx.x / NT;
+  const int64_t row = int64_t(blockIdx.x) * kRows + sub;
+  const bool mine = row < a.n;
+  const int64_t i = mine ? row : a.n - 1;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  uint32_t* __restrict__ place = all_place[sub];
+  float* __restrict__ value = all_value[sub];
+  const int32_t E = a.E, c0 = lane * VE;
+  const bool whole = !a.sigmoid && !a.renorm;  // all experts have a gradient
+  int32_t cls[kMost];
+  float xc[kMost], d[kMost];
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    const int32_t j = lane + u * NT;
+    cls[u] = -1;
+    d[u] = 0.0f;
+    if (j < a.k) cls[u] = a.classes[i * a.k + j];
+    if (cls[u] >= E) {
+      if (mine) dev_error(a.err, GBDT_E_RANGE);
+      cls[u] = -1;
+    }
+    if (cls[u] >= 0) d[u] = a.dweights[i * a.k + j];
+  }
+  Vec16<DT> raw[V];
+  float m = -kInf;
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) raw[j] = load_tail<DT>(xr, c0 + j * NT * VE, E);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int q = 0; q < VE / 4; ++q) place[(j * NT + lane) * (VE / 4) + q] = 0u;
+  }
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    xc[u] = -kInf;
+    if (cls[u] >= 0) xc[u] = in_service(Score<DT>::to_f32(xr[cls[u]]));
+    m = __builtin_fmaxf(m, xc[u]);
+  }
+  double total = 1.0;
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      unpack<DT>(raw[j], f);
+      m = __builtin_fmaxf(m, __builtin_fminf(max_of(f), kMaxF32));  // (NaN stays out)
+    }
+  }
+  m = group_max<NT>(m);
+  const float base = m == -kInf ? 0.0f : m, c = (float)kLog2e;
+  if (whole) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      unpack<DT>(raw[j], f);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = exp2_32((in_service(f[q]) - base) * c);
+      sum += sum_of(f);
+    }
+    total = group_sum<NT>((double)sum);
+    total = total > 0.0 ? 1.0 / total : 0.0;
+  }
+  double s[kMost], part[2] = {0.0, 0.0};
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    s[u] = 0.0;
+    if (cls[u] >= 0 && !(xc[u] == -kInf)) {
+      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - (double)base) * kLog2e) * total;
+      part[0] += s[u];
+      part[1] += s[u] * (double)d[u];
+    }
+  }
+  part[0] = group_sum<NT>(part[0]);
+  part[1] = group_sum<NT>(part[1]);
+  const double by = a.renorm ? (part[0] > 0.0 ? a.scale / part[0] : (part[0] == 0.0 ? 0.0 : part[0])) : a.scale;
+  const double mean = a.renorm ? (part[0] > 0.0 ? part[1] / part[0] : 0.0) : 0.0;
+  const double pull = whole ? by * part[1] : 0.0;  // sum ds s
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    const int32_t j = lane + u * NT;
+    if (cls[u] >= 0) {
+      const double ds = by * ((double)d[u] - mean) - pull;
+      value[j] = (float)(s[u] == 0.0 ? 0.0 : s[u] * (a.sigmoid ? 1.0 - s[u] : 1.0) * ds);
+      uint32_t* word = place + cls[u] / 4;
+      const int shift = cls[u] % 4 * 8;
+      if (atomicOr(word, (uint32_t)(j + 1) << shift) >> shift & 0xffu && mine) dev_error(a.err, GBDT_E_ARG);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (!mine) return;
+  Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
+  const float others = (float)(-pull * total);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int32_t e0 = c0 + j * NT * VE;
+    if (e0 >= E) break;
+    float f[VE];
+    if (whole) {
+      unpack<DT>(raw[j], f);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = exp2_32((in_service(f[q]) - base) * c) * others;
+    } else {
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = 0.0f;
+    }
+#pragma unroll
+    for (int w = 0; w < VE / 4; ++w) {
+      const uint32_t at = place[(j * NT + lane) * (VE / 4) + w];
+      if (at) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t p = at >> (8 * q) & 0xffu;
+          // (two places that met in one byte: an error already, but none out of bounds)
+          if (p) f[w * 4 + q] = value[(p - 1u) & (GBDT_MAX_ROUTED - 1)];
+        }
+      }
+    }
+    store_tail<DT>(gr, e0, E, pack<DT>(f));
+  }
+}
+
+// ------------------------------------------------------------------- lists --
+
+struct ListArgs {
+  const int32_t* classes;
+  int64_t n;
+  int32_t E, blocks;
+  int64_t chunk;  // places of a workgroup
+  uint32_t* counts;  // [blocks][E]
+  int32_t *offsets, *order, *place, *err;
+};
+
+__device__ __forceinline__ int32_t listed_class(const ListArgs& a, int64_t p, bool report) {
+  const int32_t c = a.classes[p];
+  if (c >= a.E && report) dev_error(a.err, GBDT_E_RANGE);
+  return c >= a.E ? -1 : c;
+}
+
+constexpr int kCountThreads = 256;
+__global__ void __launch_bounds__(kCountThreads) k_list_count(const ListArgs a) {
+  __shared__ uint32_t count[GBDT_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < a.E; e += kCountThreads) count[e] = 0u;
+  __syncthreads();
+  const int64_t lo = int64_t(blockIdx.x) * a.chunk, hi = a.n - lo < a.chunk ? a.n : lo + a.chunk;
+  for (int64_t p = lo + threadIdx.x; p < hi; p += kCountThreads) {
+    const int32_t c = listed_class(a, p, false);
+    if (c >= 0) atomicAdd(&count[c], 1u);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kCountThreads) a.counts[int64_t(blockIdx.x) * a.E + e] = count[e];
+}
+
+// Each workgroup adds up the counts itself (of all workgroups: where the experts'
+// lists begin; of those before it: where its own part of each list does), then takes
+// its places in order: a wave's 64 at a time, each behind the places before it of
+// the same expert, which the wave finds by a ballot per bit of the expert.
+template <int NT>
+__global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
+  constexpr int W = NT / 64, EPT = (GBDT_MAX_EXPERTS + NT - 1) / NT;
+  __shared__ uint32_t next[W][GBDT_MAX_EXPERTS];
+  __shared__ int32_t sh[32];
+  const int tid = threadIdx.x, wid = tid >> 6, lane = tid & 63;
+  const int64_t lo = int64_t(blockIdx.x) * a.chunk, hi = a.n - lo < a.chunk ? a.n : lo + a.chunk;
+  const int64_t share = (a.chunk + W * 64 - 1) / (W * 64) * 64;
+  const int64_t from_all = lo + wid * share, from = from_all < hi ? from_all : hi;
+  const int64_t to = hi - from < share ? hi : from + share;
+  for (int w = 0; w < W; ++w)
+    for (int e = tid; e < a.E; e += NT) next[w][e] = 0u;
+  __syncthreads();
+  for (int64_t p = from + lane; p < to; p += 64) {
+    const int32_t c = listed_class(a, p, true);
+    if (c >= 0) atomicAdd(&next[wid][c], 1u);
+  }
+  __syncthreads();
+  // experts tid * EPT ..: all workgroups' counts, and those before this one
+  int32_t all[EPT], before[EPT], sum = 0;
+#pragma unroll
+  for (int u = 0; u < EPT; ++u) {
+    const int e = tid * EPT + u;
+    all[u] = before[u] = 0;
+    if (e < a.E) {
+      if (a.blocks == 1) {
+        for (int w = 0; w < W; ++w) all[u] += next[w][e];
+      } else {
+#pragma unroll 8
+        for (int b = 0; b < a.blocks; ++b) {
+          const int32_t v = a.counts[int64_t(b) * a.E + e];
+          all[u] += v;
+          before[u] += b < (int)blockIdx.x ? v : 0;
+        }
+      }
+    }
+    sum += all[u];
+  }
+  int32_t total;
+  int32_t at = block_exclusive_scan(sum, &total, sh);
+#pragma unroll
+  for (int u = 0; u < EPT; ++u) {
+    const int e = tid * EPT + u;
+    if (e < a.E) {
+      if (blockIdx.x == 0) a.offsets[e] = at;
+      int32_t pos = at + before[u];
+      for (int w = 0; w < W; ++w) {
+        const uint32_t c = next[w][e];
+        next[w][e] = pos;
+        pos += c;
+      }
+    }
+    at += all[u];
+  }
+  if (blockIdx.x == 0 && tid == 0) a.offsets[a.E] = total;
+  __syncthreads();
+  int bits = 0;
+  while (1 << bits < a.E) ++bits;
+  for (int64_t p0 = from; p0 < to; p0 += 64) {
+    const int64_t p = p0 + lane;
+    const int32_t c = p < to ? listed_class(a, p, false) : -1;
+    uint64_t same = __ballot(c >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot(c >> b & 1);
+      same &= c >> b & 1 ? set : ~set;
+    }
+    int32_t pos = -1;
+    if (c >= 0) {
+      const int ahead = __popcll(same & ((uint64_t(1) << lane) - 1));
+      pos = (int32_t)next[wid][c] + ahead;
+      a.order[pos] = (int32_t)p;
+    }
+    // (a wave's LDS accesses keep their order: all reads above come before this write)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (c >= 0 && lane == 63 - __clzll((long long)same)) next[wid][c] = (uint32_t)(pos + 1);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (a.place != nullptr && p < to) a.place[p] = pos;
+  }
+}
+
+// -------------------------------------------------------------------- host --
+
+template <int DT, int NT, int EPL>
+void launch_route(const RouteArgs& a, hipStream_t s) {
+  constexpr int64_t kRows = kRouteThreads / NT;
+  diag_begin(kDiagRoute, s);
+  hipLaunchKernelGGL((k_route<DT, NT, EPL>), dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kRouteThreads), 0, s,
+                     a);
+  diag_end(s);
+}
+
+template <int DT, int NT, int V>
+void launch_route_grad(const RouteArgs& a, hipStream_t s) {
+  constexpr int64_t kRows = kRouteThreads / NT;
+  diag_begin(kDiagRoute, s);
+  hipLaunchKernelGGL((k_route_grad<DT, NT, V>), dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kRouteThreads), 0, s,
+                     a);
+  diag_end(s);
+}
+
+// The lanes of a row: as many as its experts need at EPL each, and at least one a
+// group; a group has a power of two of them.
+template <int NT, int EPL>
+bool route_fits(RouteArgs& a) {
+  int32_t log_lanes = 0, groups = 1;
+  while (groups < a.groups) groups *= 2;
+  if (groups > NT) return false;
+  while (groups << (log_lanes + 1) <= NT) ++log_lanes;
+  const int32_t lanes = 1 << log_lanes, per = (a.group_size + lanes - 1) / lanes;
+  if (per > EPL) return false;
+  a.log_lanes = log_lanes;
+  a.per_lane = per;
+  return true;
+}
+
+template <int DT>
+int route_rows(RouteArgs a, hipStream_t s) {
+  if (route_fits<4, 8>(a)) {
+    launch_route<DT, 4, 8>(a, s);
+  } else if (route_fits<8, 8>(a)) {
+    launch_route<DT, 8, 8>(a, s);
+  } else if (route_fits<16, 8>(a)) {
+    launch_route<DT, 16, 8>(a, s);
+  } else if (route_fits<16, 16>(a)) {
+    launch_route<DT, 16, 16>(a, s);
+  } else if (route_fits<32, 16>(a)) {
+    launch_route<DT, 32, 16>(a, s);
+  } else if (route_fits<64, 16>(a)) {
+    launch_route<DT, 64, 16>(a, s);
+  } else {
+    // (3, 5, 9, 17, 33 and a few more groups leave lanes over; a lane then has up to 31 experts)
+    route_fits<64, 32>(a);
+    launch_route<DT, 64, 32>(a, s);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_route");
+}
+
+template <int DT>
+int route_grad_rows(const RouteArgs& a, hipStream_t s) {
+  constexpr int VE = Score<DT>::kVec;
+  const int32_t vecs = (a.E + VE - 1) / VE;
+  if (vecs <= 8) {
+    launch_route_grad<DT, 8, 1>(a, s);
+  } else if (vecs <= 16) {
+    launch_route_grad<DT, 8, 2>(a, s);
+  } else if (vecs <= 32) {
+    launch_route_grad<DT, 8, 4>(a, s);
+  } else if (vecs <= 64) {
+    launch_route_grad<DT, 16, 4>(a, s);
+  } else if (vecs <= 128) {
+    launch_route_grad<DT, 32, 4>(a, s);
+  } else {
+    launch_route_grad<DT, 64, 4>(a, s);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_route_grad");
+}
+
+int check_routing(const gbdt_scores& x, const gbdt_routing* r) {
+  if (!r) return fail(GBDT_E_ARG, "routing is null");
+  if (x.n_classes > GBDT_MAX_EXPERTS) return fail(GBDT_E_UNSUPPORTED, "n_classes above GBDT_MAX_EXPERTS");
+  if (r->score != GBDT_ROUTE_SOFTMAX && r->score != GBDT_ROUTE_SIGMOID)
+    return fail(GBDT_E_ARG, "score is not a GBDT_ROUTE_*");
+  if (!std::isfinite(r->scale)) return fail(GBDT_E_ARG, "scale must be finite");
+  if (r->k < 1 || r->k > GBDT_MAX_ROUTED) return fail(GBDT_E_ARG, "k out of [1, GBDT_MAX_ROUTED]");
+  if (r->n_groups < 1 || r->n_groups > GBDT_MAX_EXPERT_GROUPS)
+    return fail(GBDT_E_ARG, "n_groups out of [1, GBDT_MAX_EXPERT_GROUPS]");
+  if (r->groups_kept < 1 || r->groups_kept > r->n_groups) return fail(GBDT_E_ARG, "groups_kept out of [1, n_groups]");
+  if (r->group_top != 1 && r->group_top != 2) return fail(GBDT_E_ARG, "group_top is not 1 or 2");
+  if (x.n_classes % r->n_groups) return fail(GBDT_E_SHAPE, "n_groups does not divide n_classes");
+  if (r->k > x.n_classes / r->n_groups * r->groups_kept)
+    return fail(GBDT_E_SHAPE, "k above the experts of the kept groups");
+  return GBDT_OK;
+}
+
+RouteArgs route_args(const gbdt_scores& x, const gbdt_routing& r, void* ws) {
+  RouteArgs a = {};
+  a.x = x.data;
+  a.n = x.n_rows;
+  a.ld = x.row_stride;
+  a.E = x.n_classes;
+  a.k = r.k;
+  a.sigmoid = r.score == GBDT_ROUTE_SIGMOID;
+  a.renorm = r.renormalise != 0;
+  a.groups = r.n_groups;
+  a.kept = r.groups_kept;
+  a.top = r.group_top;
+  a.group_size = x.n_classes / r.n_groups;
+  a.scale = r.scale;
+  a.err = &static_cast<WsCtrl*>(ws)->err;
+  return a;
+}
+
+}  // namespace
+
+}  // namespace gbdt
+
+using namespace gbdt;
+
+extern "C" {
+
+int gbdt_route_classes(const gbdt_scores* x, const gbdt_routing* r, const float* bias, int32_t* classes,
+                       float* weights, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_scores(x);
+  if (!rc) rc = check_routing(*x, r);
+  if (rc) return rc;
+  if (x->n_rows == 0) return GBDT_OK;
+  if (!classes || !weights) return fail(GBDT_E_ARG, "classes or weights is null");
+  rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  RouteArgs a = route_args(*x, *r, ws);
+  a.bias = bias;
+  a.classes = classes;
+  a.weights = weights;
+  a.by_value = bias != nullptr || (r->n_groups > 1 && r->group_top == 2);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (x->dtype) {
+    case GBDT_DTYPE_F32: return route_rows<GBDT_DTYPE_F32>(a, s);
+    case GBDT_DTYPE_BF16: return route_rows<GBDT_DTYPE_BF16>(a, s);
+    default: return route_rows<GBDT_DTYPE_F16>(a, s);
+  }
+}
+
+int gbdt_route_grad(const gbdt_scores* x, const gbdt_routing* r, const int32_t* classes, const float* dweights,
+                    void* grad, int64_t grad_stride, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_scores(x);
+  if (!rc) rc = check_routing(*x, r);
+  if (rc) return rc;
+  if (x->n_rows == 0) return GBDT_OK;
+  if (!classes || !dweights) return fail(GBDT_E_ARG, "classes or dweights is null");
+  rc = check_grad(*x, grad, grad_stride);
+  if (!rc) rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  RouteArgs a = route_args(*x, *r, ws);
+  a.classes = const_cast<int32_t*>(classes);  // (read only)
+  a.dweights = dweights;
+  a.grad = grad;
+  a.ldg = grad_stride;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (x->dtype) {
+    case GBDT_DTYPE_F32: return route_grad_rows<GBDT_DTYPE_F32>(a, s);
+    case GBDT_DTYPE_BF16: return route_grad_rows<GBDT_DTYPE_BF16>(a, s);
+    default: return route_grad_rows<GBDT_DTYPE_F16>(a, s);
+  }
+}
+
+int gbdt_route_lists(const int32_t* classes, int64_t n_places, int32_t n_experts, int32_t* offsets, int32_t* order,
+                     int32_t* place, void* ws, size_t ws_bytes, void* stream) {
+  if (n_places < 0 || n_places > INT32_MAX) return fail(GBDT_E_ARG, "n_places out of [0, 2^31)");
+  if (n_experts < 1 || n_experts > GBDT_MAX_EXPERTS) return fail(GBDT_E_ARG, "n_experts out of [1, GBDT_MAX_EXPERTS]");
+  if (!offsets) return fail(GBDT_E_ARG, "offsets is null");
+  if (n_places > 0 && (!classes || !order)) return fail(GBDT_E_ARG, "classes or order is null");
+  gbdt_scores x = {};
+  x.n_classes = n_experts;
+  const int rc = check_scores_ws(x, ws, ws_bytes);
+  if (rc) return rc;
+  ListArgs a = {};
+  a.classes = classes;
+  a.n = n_places;
+  a.E = n_experts;
+  a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + sizeof(WsCtrl));
+  a.offsets = offsets;
+  a.order = order;
+  a.place = place;
+  a.err = &static_cast<WsCtrl*>(ws)->err;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  constexpr int64_t kAlone = 4096, kChunk = 1024, kMostBlocks = 256;
+  static_assert(kMostBlocks * GBDT_MAX_EXPERTS * 4 <= kScoresPartBytes, "the counts fit the workspace");
+  a.blocks = 1;
+  a.chunk = n_places;
+  if (n_places > kAlone) {
+    a.chunk = (n_places + kMostBlocks - 1) / kMostBlocks;
+    if (a.chunk < kChunk) a.chunk = kChunk;
+    a.blocks = (int32_t)((n_places + a.chunk - 1) / a.chunk);
+    diag_begin(kDiagRouteLists, s);
+    hipLaunchKernelGGL(k_list_count, dim3(a.blocks), dim3(kCountThreads), 0, s, a);
+    diag_end(s);
+  }
+  diag_begin(kDiagRouteLists, s);
+  hipLaunchKernelGGL(k_list_place<512>, dim3(a.blocks), dim3(512), 0, s, a);
+  diag_end(s);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_list_place");
+}
+
+}  // extern "C"

@@ -415,11 +415,14 @@ __device__ __forceinline__ void unstage(int32_t rows, int32_t width, bool flat, 
 }
 
 // Workspace of the row calls: the control block, then partial results of rows
-// that several workgroups share.
+// that several workgroups share, then a counter for each such row, zero between
+// calls (the last workgroup of a row to arrive sets it back).
 constexpr size_t kScoresPartBytes = size_t(1) << 20;
+constexpr size_t kScoresTicketBytes = kSplitRows * 4;
 
 // Host checks shared by the entry points.
 int check_scores(const gbdt_scores* x);
 int check_scores_ws(const gbdt_scores& x, const void* ws, size_t ws_bytes);
+int check_grad(const gbdt_scores& x, const void* grad, int64_t grad_stride);
 
 }  // namespace gbdt

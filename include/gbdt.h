@@ -788,6 +788,176 @@ int gbdt_sample_classes(const gbdt_scores* x /* host */, const float* u,
                         const gbdt_sampling* p /* host */, int32_t* out, float* logp, void* ws,
                         size_t ws_bytes, void* stream);
 
+/* ------------------------------------------- learning from drawn classes -- */
+
+/*
+ * Log-probabilities of one class of each row, at temperature T (1e-30 to 1e30),
+ *   logp_i = log softmax(x_i / T)[classes[i]],
+ * and what the backward pass needs: stats[n_rows][2] = (m, o), m the largest
+ * score of the row's other classes and o the sum of their exp((x_c - m) / T).
+ * classes: device, [n_rows].  A row COUNTS unless its class is below 0 (padding),
+ * is n_classes or more (recorded as GBDT_E_RANGE), or all its scores are -inf:
+ * a row that does not count has logp 0, stats (0, 0), and, below, loss 0 and
+ * gradient 0.  A class of score -inf in a row with others has logp -inf and its
+ * row gradient 0.  Other rows with a NaN or +inf score have NaN results.  A row
+ * whose class is the only one left has logp 0, stats (-inf, 0) and gradient 0.
+ * stats may be NULL in gbdt_class_logp.
+ *
+ * gbdt_class_logp_grad: with dlogp[n_rows] the derivative of some loss by each
+ * logp, grad = dlogp_i dlogp_i/dx: dlogp_i / T times (1 at the class, else 0) -
+ * softmax(x_i / T).  A row of dlogp 0 has gradient 0 whatever its scores.  grad:
+ * the scores' type, rows grad_stride elements apart; it must not overlap the
+ * scores.
+ */
+int gbdt_class_logp(const gbdt_scores* x /* host */, const int32_t* classes, double temperature,
+                    float* logp, float* stats, void* ws, size_t ws_bytes, void* stream);
+int gbdt_class_logp_grad(const gbdt_scores* x /* host */, const int32_t* classes, double temperature,
+                         const float* stats, const float* dlogp, void* grad, int64_t grad_stride,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Clipped policy loss with a KL term, a row of scores and its drawn class each:
+ * r = exp(logp - old_logp) against the policy that drew the class, A the
+ * advantage, y = ref_logp - logp against a reference policy,
+ *   loss = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl (e^y - y - 1),
+ *   slope = d loss / d logp = -[r A counts] r A + kl (1 - e^y),
+ * where r A counts unless A > 0 and r > 1 + clip_high, or A < 0 and
+ * r < 1 - clip_low.  A = 0 makes the first term 0 whatever r.  Rows that do not
+ * count, classes of score -inf, NaN and +inf scores are as above.
+ * old_logp, ref_logp, advantage, weight: device, [n_rows]; ref_logp may be NULL (no
+ * KL term), weight may be NULL (ones); a row of weight 0 has slope and gradient 0
+ * whatever the others.  clip_low in [0, 1], clip_high >= 0, kl finite and >= 0.
+ * Host struct holding device pointers.
+ *
+ * gbdt_policy_loss writes loss (not weighted), logp (may be NULL), dlogp = weight
+ * times slope, and stats: the forward pass; gbdt_class_logp_grad with these is the
+ * backward pass.  gbdt_policy_step does both in one call (logp may be NULL).
+ */
+typedef struct gbdt_policy {
+  const float* old_logp;
+  const float* ref_logp;
+  const float* advantage;
+  const float* weight;
+  double clip_low, clip_high, kl;
+} gbdt_policy;
+
+int gbdt_policy_loss(const gbdt_scores* x /* host */, const int32_t* classes, double temperature,
+                     const gbdt_policy* p /* host */, float* loss, float* logp, float* dlogp,
+                     float* stats, void* ws, size_t ws_bytes, void* stream);
+int gbdt_policy_step(const gbdt_scores* x /* host */, const int32_t* classes, double temperature,
+                     const gbdt_policy* p /* host */, float* loss, float* logp, void* grad,
+                     int64_t grad_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Preference loss of pairs of row sequences.  offsets (device, [2 n_pairs + 1],
+ * ascending, in [0, n_rows]): sequence s is the rows offsets[s] <= i < offsets[s + 1];
+ * pair p prefers sequence 2 p to sequence 2 p + 1.  Over the rows of a sequence
+ * that count,
+ *   S = sum (logp - ref_logp),  with average != 0 divided by their number,
+ *   reward = beta S (0 for a sequence with none),  z = reward_2p - reward_2p+1,
+ *   loss_p = -(1 - smoothing) log sigmoid(z) - smoothing log sigmoid(-z),
+ * and dlogp of a row is weight_p times the derivative of loss_p by its logp.
+ * ref_logp: device, [n_rows], or NULL (0).  weight: device, [n_pairs], or NULL
+ * (ones); a pair of weight 0 has slopes 0.  A logp of -inf makes its reward -inf
+ * and leaves the other rows' slopes finite; two rewards of the same infinity, as a
+ * NaN, make the pair NaN.  beta finite, smoothing in [0, 1/2).  Offsets that
+ * descend or leave [0, n_rows] are recorded as GBDT_E_RANGE, and the outputs are
+ * then unspecified.  Host struct holding device pointers.
+ *
+ * gbdt_preference_loss writes loss[n_pairs], rewards[n_pairs][2] (may be NULL),
+ * and logp, dlogp, stats of the rows in sequences; rows before the first and
+ * behind the last stay as they are, and are not read.  gbdt_class_logp_grad with these
+ * is the backward pass (give it dlogp 0 for rows in no sequence).
+ * gbdt_preference_step does both in one call, and leaves the gradient of rows in
+ * no sequence as it is; it takes a workspace of gbdt_preference_workspace_bytes().
+ */
+typedef struct gbdt_pairs {
+  const int64_t* offsets;
+  const float* ref_logp;
+  const float* weight;
+  int32_t n_pairs; /* 0 .. 2^29 */
+  int32_t average;
+  double beta, smoothing;
+} gbdt_pairs;
+
+size_t gbdt_preference_workspace_bytes(int64_t n_rows, int32_t n_classes);
+int gbdt_preference_loss(const gbdt_scores* x /* host */, const int32_t* classes, double temperature,
+                         const gbdt_pairs* p /* host */, float* loss, float* rewards, float* logp,
+                         float* dlogp, float* stats, void* ws, size_t ws_bytes, void* stream);
+int gbdt_preference_step(const gbdt_scores* x /* host */, const int32_t* classes, double temperature,
+                         const gbdt_pairs* p /* host */, float* loss, float* rewards, void* grad,
+                         int64_t grad_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------ routing to experts -- */
+
+/*
+ * Rows sent to k experts each: the classes of a row of router scores are the
+ * experts (other ensembles, say, that answer for some rows).
+ *   value s_e = softmax_e(x) or 1 / (1 + exp(-x_e)),
+ *   choice value v_e = s_e + bias_e where there is a bias or group_top is 2
+ *     (with n_groups above 1), else the score x_e itself,
+ * both in 64 bits.  The experts come in n_groups groups of n_classes / n_groups
+ * neighbours; a group's rank is its largest choice value, or with group_top 2 the
+ * sum of its two largest (of one, if it has one); the groups_kept groups of highest
+ * rank (equal ranks: the first) stay.  Of these the k experts of largest choice
+ * value, descending (equal values: the lower expert), are chosen.  The bias plays
+ * no part in the weights:
+ *   weight_j = scale s_j / (sum of the chosen s_j if renormalise, else 1),
+ * 0 where that sum is 0.  An expert of score -inf or NaN, or of a choice value that
+ * is -inf or NaN, is out of service; where fewer than k are left, the list ends in
+ * class -1 with weight 0.  A score of +inf counts as the largest FP32 number in a
+ * softmax.
+ * Host struct.  k up to min(GBDT_MAX_ROUTED, n_classes / n_groups * groups_kept),
+ * n_classes up to GBDT_MAX_EXPERTS, n_groups a divisor of n_classes and at most
+ * 64, group_top 1 or 2, scale finite.
+ */
+#define GBDT_MAX_EXPERTS 1024
+#define GBDT_MAX_ROUTED 32
+#define GBDT_MAX_EXPERT_GROUPS 64
+#define GBDT_ROUTE_SOFTMAX 0
+#define GBDT_ROUTE_SIGMOID 1
+
+typedef struct gbdt_routing {
+  double scale;
+  int32_t k;
+  int32_t score; /* GBDT_ROUTE_* */
+  int32_t renormalise;
+  int32_t n_groups, groups_kept, group_top;
+} gbdt_routing;
+
+/* classes, weights: device, [n_rows][k].  bias: device, [n_classes], or NULL. */
+int gbdt_route_classes(const gbdt_scores* x /* host */, const gbdt_routing* r /* host */,
+                       const float* bias, int32_t* classes, float* weights, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * The backward pass: grad (the scores' type, rows grad_stride elements apart, not
+ * overlapping them) = the derivative of sum_j dweights_j weight_j by the scores, the
+ * choice held fixed; dweights: device, [n_rows][k].  classes as gbdt_route_classes
+ * wrote them; one below 0 is padding (its dweight is not read), one of n_classes or
+ * more is recorded as GBDT_E_RANGE and taken as padding, one listed twice in a row
+ * is recorded as GBDT_E_ARG, and that row's gradient is unspecified.  Experts of
+ * score -inf or NaN have gradient 0; NaN dweights make the gradients NaN that they
+ * reach.  Groups and bias play no part.
+ */
+int gbdt_route_grad(const gbdt_scores* x /* host */, const gbdt_routing* r /* host */,
+                    const int32_t* classes, const float* dweights, void* grad, int64_t grad_stride,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The experts' lists of places: of classes[n_places] (device; n_rows k of them as
+ * gbdt_route_classes wrote them), the places p with classes[p] = e, ascending, are
+ * order[offsets[e]] .. order[offsets[e + 1] - 1], and place[p] is where p stands in
+ * order, -1 for a class below 0 (a stable partition of the places, as
+ * gbdt_partition_rows has it of rows).  Entries of order from offsets[n_experts] on
+ * stay as they are.  offsets: device, [n_experts + 1]; order, place (may be NULL):
+ * device, [n_places].  A class of n_experts or more is recorded as GBDT_E_RANGE and
+ * taken as -1.  n_places up to 2^31 - 1.  ws: gbdt_scores_workspace_bytes(n, n_experts)
+ * bytes for any n.
+ */
+int gbdt_route_lists(const int32_t* classes, int64_t n_places, int32_t n_experts, int32_t* offsets,
+                     int32_t* order, int32_t* place, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
