@@ -217,9 +217,12 @@ def _ptr(t):
 
 
 def _stream(stream=None):
+    """The stream's handle; None: of the current stream (asked for by handle: a
+    Stream object costs 3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def make_params(max_depth, reg_lambda=1.0, gamma=0.0, min_child_weight=0.0, learning_rate=0.3,
@@ -554,7 +557,8 @@ def _vector(t, name, dtype, shape, x, optional=False):
     """Address of a contiguous tensor of the given type and shape on x's device."""
     if t is None and optional:
         return None
-    if t is None or t.dtype != dtype or t.shape != shape or t.device != x.device or not t.is_contiguous():
+    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != x.get_device() or \
+            not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on the scores' device"
                          % (name, dtype, tuple(shape)))
     return t.data_ptr()
@@ -562,7 +566,7 @@ def _vector(t, name, dtype, shape, x, optional=False):
 
 def _workspace(ws, x):
     """(address, bytes) of a workspace on the scores' device."""
-    if ws is None or ws.device != x.device or not ws.is_contiguous():
+    if ws is None or ws.get_device() != x.get_device() or not ws.is_contiguous():
         raise ValueError("ws must be a workspace from new_workspace() on the scores' device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -576,7 +580,7 @@ def _teacher(x, n, values, classes, rest) -> Teacher:
 
 
 def _grad_rows(x, grad):
-    if grad.dtype != x.dtype or grad.device != x.device:
+    if grad.dtype != x.dtype or grad.get_device() != x.get_device():
         raise ValueError("grad must have the scores' type and device")
     return _rows_2d(grad, "grad", *x.shape)[2]
 
@@ -669,7 +673,7 @@ def gbdt_sample_classes(scores, u, temperature, top_k, top_p, min_p, out, logp, 
 def _here(x):
     """Refuses tensors of a device that is not the current one: its stream would not be theirs."""
     import torch
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
+    if x.is_cuda and x.get_device() != torch._C._cuda_getDevice():
         raise ValueError("tensors on %s, but the current device is cuda:%d" % (x.device, torch.cuda.current_device()))
 
 

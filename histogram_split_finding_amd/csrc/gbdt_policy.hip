@@ -460,20 +460,25 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
 // ------------------------------------------------------------------- pairs --
 
 struct PairArgs {
+  const void* x;
+  int64_t n, ld;
+  const int32_t* cls;
+  double inv_T;
   const int64_t* offsets;
   const float *ref_logp, *weight;
   double beta, smoothing;
-  int64_t n;
   int32_t n_pairs, average;
-  const float *logp, *stats;
+  const float* stats;
   float *loss, *rewards, *dlogp;
   int32_t* err;
 };
 
 // One workgroup per pair: the two sequences' sums of logp - ref over the rows that
 // count (statistics other than (0, 0)), in FP64 in a fixed order, then the slope of
-// each row.
+// each row.  logp is taken from the statistics again: its FP32 value is off by up to
+// 2^-24 |logp|, some 10 times what o is, and the sums are small differences of many.
 constexpr int kPairThreads = 256;
+template <int DT>
 __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
   __shared__ double sh[2][2][kPairThreads / 64];
   const int tid = threadIdx.x, wid = tid >> 6;
@@ -488,14 +493,19 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
     bad = bad || cut[u] != v;
   }
   if (bad && tid == 0) dev_error(a.err, GBDT_E_RANGE);
+  auto counts = [&](int64_t i) { return !(a.stats[2 * i] == 0.0f && a.stats[2 * i + 1] == 0.0f); };
+  auto score = [&](int64_t i) {  // (of a row that counts: its class is in range)
+    return Score<DT>::to_f32(static_cast<const typename Score<DT>::Elem*>(a.x)[i * a.ld + a.cls[i]]);
+  };
   double sum[2], count[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     sum[s] = 0.0;
     int64_t rows = 0;
     for (int64_t i = cut[s] + tid; i < cut[s + 1]; i += kPairThreads) {
-      if (a.stats[2 * i] == 0.0f && a.stats[2 * i + 1] == 0.0f) continue;
-      sum[s] += (double)a.logp[i] - (a.ref_logp == nullptr ? 0.0 : (double)a.ref_logp[i]);
+      if (!counts(i)) continue;
+      const RowEnd e = row_end(a.inv_T, true, a.stats[2 * i], a.stats[2 * i + 1], score(i));
+      sum[s] += e.logp - (a.ref_logp == nullptr ? 0.0 : (double)a.ref_logp[i]);
       ++rows;
     }
     sum[s] = wave_sum(sum[s]);
@@ -535,8 +545,7 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
   for (int s = 0; s < 2; ++s) {
     const float d = (float)((s == 0 ? slope : -slope) * per[s]);
     for (int64_t i = cut[s] + tid; i < cut[s + 1]; i += kPairThreads) {
-      const bool counts = !(a.stats[2 * i] == 0.0f && a.stats[2 * i + 1] == 0.0f) && a.logp[i] != -kInf;
-      a.dlogp[i] = counts ? d : 0.0f;
+      a.dlogp[i] = counts(i) && score(i) != -kInf ? d : 0.0f;
     }
   }
 }
@@ -694,6 +703,12 @@ int policy(const gbdt_scores* x, const int32_t* classes, double temperature, con
   return launch_logp<kSums>(x->dtype, a, s);
 }
 
+// The preference step's workspace: that of the rows, then each row's statistics and
+// slope.
+constexpr size_t preference_rows_at() {
+  return (sizeof(WsCtrl) + kScoresPartBytes + kScoresTicketBytes + 255) / 256 * 256;
+}
+
 int check_pairs(const gbdt_pairs* p) {
   if (!p) return fail(GBDT_E_ARG, "pairs is null");
   if (p->n_pairs < 0 || p->n_pairs > 1 << 29) return fail(GBDT_E_ARG, "n_pairs out of [0, 2^29]");
@@ -702,28 +717,75 @@ int check_pairs(const gbdt_pairs* p) {
   return GBDT_OK;
 }
 
-int launch_pairs(const gbdt_pairs& p, int64_t n_rows, const float* logp, const float* stats, float* loss,
-                 float* rewards, float* dlogp, void* ws, hipStream_t s) {
+int launch_pairs(const gbdt_pairs& p, const gbdt_scores& x, const int32_t* classes, double temperature,
+                 const float* stats, float* loss, float* rewards, float* dlogp, void* ws, hipStream_t s) {
   PairArgs a = {};
+  a.x = x.data;
+  a.n = x.n_rows;
+  a.ld = x.row_stride;
+  a.cls = classes;
+  a.inv_T = 1.0 / temperature;
   a.offsets = p.offsets;
   a.ref_logp = p.ref_logp;
   a.weight = p.weight;
   a.beta = p.beta;
   a.smoothing = p.smoothing;
-  a.n = n_rows;
   a.n_pairs = p.n_pairs;
   a.average = p.average;
-  a.logp = logp;
   a.stats = stats;
   a.loss = loss;
   a.rewards = rewards;
   a.dlogp = dlogp;
   a.err = &static_cast<WsCtrl*>(ws)->err;
+  const dim3 grid((unsigned)p.n_pairs), block(kPairThreads);
   diag_begin(kDiagPairs, s);
-  hipLaunchKernelGGL(k_pairs, dim3((unsigned)p.n_pairs), dim3(kPairThreads), 0, s, a);
+  switch (x.dtype) {
+    case GBDT_DTYPE_F32: hipLaunchKernelGGL(k_pairs<GBDT_DTYPE_F32>, grid, block, 0, s, a); break;
+    case GBDT_DTYPE_BF16: hipLaunchKernelGGL(k_pairs<GBDT_DTYPE_BF16>, grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL(k_pairs<GBDT_DTYPE_F16>, grid, block, 0, s, a);
+  }
   diag_end(s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_pairs");
+}
+
+// Both passes: the rows' statistics (and logp, if asked for), the pairs, and the
+// gradient where there is one.
+int preference(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_pairs* p, float* loss,
+               float* rewards, float* logp, float* dlogp, float* stats, void* grad, int64_t grad_stride, bool step,
+               void* ws, size_t ws_bytes, hipStream_t s) {
+  int rc = check_logp(x, temperature);
+  if (!rc) rc = check_pairs(p);
+  if (rc) return rc;
+  if (p->n_pairs == 0) return GBDT_OK;
+  if (!p->offsets || !loss) return fail(GBDT_E_ARG, "offsets or loss is null");
+  if (x->n_rows > 0) {
+    if (!classes) return fail(GBDT_E_ARG, "classes is null");
+    if (!step && (!logp || !dlogp || !stats)) return fail(GBDT_E_ARG, "logp, dlogp or stats is null");
+    if (step) rc = check_grad(*x, grad, grad_stride);
+    if (rc) return rc;
+  }
+  rc = check_scores_ws(*x, ws, ws_bytes);
+  if (rc) return rc;
+  if (step) {
+    if (ws_bytes < gbdt_preference_workspace_bytes(x->n_rows, x->n_classes))
+      return fail(GBDT_E_ARG, "workspace smaller than gbdt_preference_workspace_bytes()");
+    stats = reinterpret_cast<float*>(static_cast<char*>(ws) + preference_rows_at());
+    dlogp = stats + 2 * x->n_rows;
+  }
+  LogpArgs a = logp_args(*x, classes, temperature, ws);
+  a.range = p->offsets;
+  a.last = 2 * p->n_pairs;
+  a.logp = logp;
+  a.stats = stats;
+  if (x->n_rows > 0) rc = launch_logp<kSums>(x->dtype, a, s);
+  if (!rc) rc = launch_pairs(*p, *x, classes, temperature, stats, loss, rewards, dlogp, ws, s);
+  if (rc || !step || x->n_rows == 0) return rc;
+  a.logp = nullptr;
+  a.dlogp = dlogp;
+  a.grad = grad;
+  a.ldg = grad_stride;
+  return launch_logp<kStats>(x->dtype, a, s);
 }
 
 }  // namespace
@@ -789,62 +851,21 @@ int gbdt_policy_step(const gbdt_scores* x, const int32_t* classes, double temper
 }
 
 size_t gbdt_preference_workspace_bytes(int64_t n_rows, int32_t n_classes) {
-  const size_t rows = gbdt_scores_workspace_bytes(n_rows, n_classes);
-  // a row's logp, slope and statistics
-  return rows == 0 ? 0 : (rows + 255) / 256 * 256 + size_t(n_rows) * 16;
+  return gbdt_scores_workspace_bytes(n_rows, n_classes) == 0 ? 0 : preference_rows_at() + size_t(n_rows) * 12;
 }
 
 int gbdt_preference_loss(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_pairs* p,
                          float* loss, float* rewards, float* logp, float* dlogp, float* stats, void* ws,
                          size_t ws_bytes, void* stream) {
-  int rc = check_logp(x, temperature);
-  if (!rc) rc = check_pairs(p);
-  if (rc) return rc;
-  if (p->n_pairs == 0) return GBDT_OK;
-  if (!p->offsets || !loss) return fail(GBDT_E_ARG, "offsets or loss is null");
-  if (x->n_rows > 0) {
-    if (!classes) return fail(GBDT_E_ARG, "classes is null");
-    if (!logp || !dlogp || !stats) return fail(GBDT_E_ARG, "logp, dlogp or stats is null");
-  }
-  rc = check_scores_ws(*x, ws, ws_bytes);
-  if (rc) return rc;
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (x->n_rows > 0) {
-    LogpArgs a = logp_args(*x, classes, temperature, ws);
-    a.range = p->offsets;
-    a.last = 2 * p->n_pairs;
-    a.logp = logp;
-    a.stats = stats;
-    rc = launch_logp<kSums>(x->dtype, a, s);
-    if (rc) return rc;
-  }
-  return launch_pairs(*p, x->n_rows, logp, stats, loss, rewards, dlogp, ws, s);
+  return preference(x, classes, temperature, p, loss, rewards, logp, dlogp, stats, nullptr, 0, false, ws, ws_bytes,
+                    reinterpret_cast<hipStream_t>(stream));
 }
 
 int gbdt_preference_step(const gbdt_scores* x, const int32_t* classes, double temperature, const gbdt_pairs* p,
                          float* loss, float* rewards, void* grad, int64_t grad_stride, void* ws, size_t ws_bytes,
                          void* stream) {
-  int rc = check_logp(x, temperature);
-  if (!rc) rc = check_pairs(p);
-  if (rc) return rc;
-  if (p->n_pairs == 0) return GBDT_OK;
-  if (x->n_rows > 0) rc = check_grad(*x, grad, grad_stride);
-  if (rc) return rc;
-  if (ws_bytes < gbdt_preference_workspace_bytes(x->n_rows, x->n_classes))
-    return fail(GBDT_E_ARG, "workspace smaller than gbdt_preference_workspace_bytes()");
-  const size_t rows = (gbdt_scores_workspace_bytes(x->n_rows, x->n_classes) + 255) / 256 * 256;
-  float* logp = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
-  float *dlogp = logp + x->n_rows, *stats = dlogp + x->n_rows;
-  rc = gbdt_preference_loss(x, classes, temperature, p, loss, rewards, logp, dlogp, stats, ws, ws_bytes, stream);
-  if (rc || x->n_rows == 0) return rc;
-  LogpArgs a = logp_args(*x, classes, temperature, ws);
-  a.range = p->offsets;
-  a.last = 2 * p->n_pairs;
-  a.stats = stats;
-  a.dlogp = dlogp;
-  a.grad = grad;
-  a.ldg = grad_stride;
-  return launch_logp<kStats>(x->dtype, a, reinterpret_cast<hipStream_t>(stream));
+  return preference(x, classes, temperature, p, loss, rewards, nullptr, nullptr, nullptr, grad, grad_stride, true, ws,
+                    ws_bytes, reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

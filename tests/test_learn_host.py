@@ -129,9 +129,9 @@ def test_workspace_rules():
         assert set(all_calls(x, **kw)) == {-1}
         assert lists(**kw) == -1
     more = g.gbdt_preference_workspace_bytes(4, 10)
-    assert more >= need + 4 * 16 and pref_step(x, q, nb=more - 1) == -1
+    assert more >= need + 4 * 12 and pref_step(x, q, nb=more - 1) == -1
     assert g.gbdt_preference_workspace_bytes(-1, 5) == 0 and g.gbdt_preference_workspace_bytes(5, 0) == 0
-    assert g.gbdt_preference_workspace_bytes(1 << 31, 7) >= 16 << 31
+    assert g.gbdt_preference_workspace_bytes(1 << 31, 7) >= 12 << 31
 
 
 @pytest.mark.parametrize("kw", [dict(clip_low=-0.1), dict(clip_low=1.1), dict(clip_low=float("nan")),
