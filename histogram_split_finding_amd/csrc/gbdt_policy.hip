@@ -43,6 +43,7 @@ struct LogpArgs {
   int64_t n, ld;
   const int32_t* cls;
   int32_t C, n_parts, part_len, last;  // last: of range
+  int32_t reverse;                     // from the last row to the first
   const int64_t* range;                // rows [range[0], range[last]) only, or NULL: all
   double c, inv_T;                     // log2(e) / T, 1 / T
   const float *old_logp, *ref_logp, *adv, *weight;
@@ -85,21 +86,23 @@ __device__ __forceinline__ double exp_64(double y) {
 // log(1 + e) for 0 <= e <= 1.
 __device__ __forceinline__ double log1p_64(double e) { return e < 0x1p-20 ? e - 0.5 * e * e : log_64(1.0 + e); }
 
-// A row's end: what its sums say about its class.
+// A row's end: what its sums say about its class.  t = e^L, the odds against it, is
+// o e^d with d = (m - x_a) / T: one exponential and one logarithm.  d is cut where t
+// would overflow; there log(1 + t) is log o + d to the last digit.
 struct RowEnd {
-  bool live;     // the row counts
+  bool live;             // the row counts
   double logp, against;  // log p_a, 1 - p_a
 };
 __device__ __forceinline__ RowEnd row_end(double inv_T, bool named, double m, double o, double xa) {
+  constexpr double kMostD = 690.0;
   RowEnd r;
   r.live = named && !(o == 0.0 && xa == -__builtin_inf());
-  double L = (m - xa) * inv_T + log_64(o);
-  if (o == 0.0) L = -__builtin_inf();
-  if (xa == __builtin_inf() || xa != xa) L = __builtin_nan("");
-  const double e = exp2_64(-__builtin_fabs(L) * kLog2e);
-  const double inv = rcp_64(1.0 + e);
-  r.logp = L != L ? L : (L < 0.0 ? -log1p_64(e) : -(L + log1p_64(e)));
-  r.against = L != L ? L : (L < 0.0 ? e * inv : inv);
+  const double d = (m - xa) * inv_T;
+  const double over = d > kMostD ? d - kMostD : 0.0;
+  double t = o * exp2_64((d > kMostD ? kMostD : d) * kLog2e);
+  if (!(xa < __builtin_inf())) t = __builtin_nan("");
+  r.against = t * rcp_64(1.0 + t);
+  r.logp = -((t < 0x1p-20 ? t - 0.5 * t * t : log_64(1.0 + t)) + over);
   return r;
 }
 
@@ -205,29 +208,26 @@ __device__ __forceinline__ void set_class(float (&f)[VE], int32_t cls, int32_t c
 }
 
 // One thread per row of at most CMAX classes, R rows a workgroup; rows and
-// gradients pass through LDS in rows of C | 1 words, so that memory sees whole
-// lines.  The exponentials are in FP64: a row's few terms do not average rounding
-// errors away, and a ratio next to the clip's border decides about the row.
+// gradients pass through LDS, so that memory sees whole lines: packed rows of an odd
+// length as they lie there, 16 bytes at a time, others in rows of C | 1 words.  The
+// exponentials are in FP64 (a row's few terms do not average rounding errors away,
+// and a ratio next to the clip's border decides about the row), four classes at a
+// time, -inf behind the row's end.
+constexpr int kShortStep = 4;
 template <int DT, int R, int CMAX, int FROM>
-__global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_logp_short(const LogpArgs a) {
+__global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
-  extern __shared__ float lds[];
+  constexpr int VE = Score<DT>::kVec, V = (CMAX + VE - 1) / VE;
+  extern __shared__ __align__(16) float lds[];
   const Span span = row_span(a);
   const int tid = threadIdx.x;
   const int64_t i0 = span.lo + int64_t(blockIdx.x) * R, i = i0 + tid;
   if (i0 >= span.hi) return;
   const int32_t rows = (int32_t)(span.hi - i0 < R ? span.hi - i0 : R);
-  const int32_t C = a.C, P = C | 1;
+  const int32_t C = a.C, P = C | 1, all = rows * C;
   const RowDiv by_c(C);
   const Elem* __restrict__ xg = static_cast<const Elem*>(a.x) + i0 * a.ld;
   const bool mine = tid < rows;
-  {
-    Staged<R, CMAX, float> xs;
-    xs.load(
-        rows, C, a.ld == C, by_c, [&](int32_t e) { return Score<DT>::to_f32(xg[(uint32_t)e]); },
-        [&](int32_t row, int32_t c) { return Score<DT>::to_f32(xg[row * a.ld + c]); });
-    xs.put(rows, C, by_c, lds);
-  }
   int32_t cls = -1;
   RowIn in = {};
   float m = -kInf;
@@ -240,43 +240,84 @@ __global__ void __launch_bounds__(R, CMAX == 8 ? 1 : 4) k_logp_short(const LogpA
       o = a.stats[2 * i + 1];
     }
   }
+  if ((C & 1) && a.ld == C) {
+    Vec16<DT> raw[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) raw[j] = load_tail<DT>(xg, (tid + j * R) * VE, all);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int32_t e = (tid + j * R) * VE;
+      float f[VE];
+      unpack<DT>(raw[j], f);
+      if (e < all) __builtin_memcpy(__builtin_assume_aligned(lds + e, 16), f, sizeof(f));
+    }
+  } else {
+    Staged<R, CMAX, float> xs;
+    xs.load(
+        rows, C, a.ld == C, by_c, [&](int32_t e) { return Score<DT>::to_f32(xg[(uint32_t)e]); },
+        [&](int32_t row, int32_t c) { return Score<DT>::to_f32(xg[row * a.ld + c]); });
+    xs.put(rows, C, by_c, lds);
+  }
   __syncthreads();
   float* __restrict__ x = lds + tid * P;
   if (mine) {
     const bool named = cls >= 0;
     const float xa = named ? x[cls] : 0.0f;
-    if (FROM != kStats) {
+    float v[CMAX];
 #pragma unroll
-      for (int c = 0; c < CMAX; ++c)
-        if (c < C) m = c == cls ? m : __builtin_fmaxf(m, x[c]);
-      const double base = m == -kInf ? 0.0 : (double)m;
+    for (int c0 = 0; c0 < CMAX; c0 += kShortStep) {
+      if (c0 < C) {
 #pragma unroll
-      for (int c = 0; c < CMAX; ++c) {
-        if (c < C) {
-          const double v = exp2_64(((double)x[c] - base) * a.c);
-          o += c == cls ? 0.0 : v;
-          x[c] = (float)v;
+        for (int q = 0; q < kShortStep; ++q) {
+          const int c = c0 + q;
+          v[c] = c < C ? x[c] : -kInf;  // (the read stays inside the LDS of the launch)
+          if (FROM != kStats) m = c == cls ? m : __builtin_fmaxf(m, v[c]);
+        }
+      }
+    }
+    const double base = m == -kInf ? 0.0 : (double)m;
+    const float cf = exponent_scale(a.c), mf = (float)base;
+#pragma unroll
+    for (int c0 = 0; c0 < CMAX; c0 += kShortStep) {
+      if (c0 < C) {
+#pragma unroll
+        for (int q = 0; q < kShortStep; ++q) {
+          const int c = c0 + q;
+          if (FROM != kStats) {
+            const double w = exp2_64(((double)v[c] - base) * a.c);
+            o += c == cls ? 0.0 : w;
+            v[c] = (float)w;
+          } else {
+            v[c] = exp2_32((v[c] - mf) * cf);
+          }
         }
       }
     }
     const RowGrad g = row_out<FROM>(a, i, true, named, in, m, o, xa);
     if (a.grad != nullptr) {
-      const float cf = exponent_scale(a.c), mf = m == -kInf ? 0.0f : m;
 #pragma unroll
-      for (int c = 0; c < CMAX; ++c) {
-        if (c < C) {
-          const float v = FROM != kStats ? x[c] : exp2_32((x[c] - mf) * cf);
-          x[c] = !g.any ? 0.0f : (c == cls ? g.mine : v * g.scale);
-        }
-      }
+      for (int c = 0; c < CMAX; ++c)
+        if (c < C) x[c] = !g.any ? 0.0f : (c == cls ? g.mine : v[c] * g.scale);
     }
   }
   if (a.grad != nullptr) {
     __syncthreads();
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i0 * a.ldg;
-    unstage<R, CMAX>(
-        rows, C, a.ldg == C, by_c, lds, [&](int32_t e, float v) { gr[(uint32_t)e] = Score<DT>::from_f32(v); },
-        [&](int32_t row, int32_t c, float v) { gr[row * a.ldg + c] = Score<DT>::from_f32(v); });
+    if ((C & 1) && a.ldg == C) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int32_t e = (tid + j * R) * VE;
+        if (e < all) {
+          float f[VE];
+          __builtin_memcpy(f, __builtin_assume_aligned(lds + e, 16), sizeof(f));
+          store_tail<DT>(gr, e, all, pack<DT>(f));
+        }
+      }
+    } else {
+      unstage<R, CMAX>(
+          rows, C, a.ldg == C, by_c, lds, [&](int32_t e, float f) { gr[(uint32_t)e] = Score<DT>::from_f32(f); },
+          [&](int32_t row, int32_t c, float f) { gr[row * a.ldg + c] = Score<DT>::from_f32(f); });
+    }
   }
 }
 
@@ -364,8 +405,8 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   const float cf = exponent_scale(a.c);
   const uint32_t in_launch = a.n_parts > 1 ? blockIdx.x / (uint32_t)a.n_parts : blockIdx.x;
   const int32_t part = (int32_t)(blockIdx.x - in_launch * (uint32_t)a.n_parts);
-  const int64_t row = a.row0 + in_launch, i = span.lo + row;
-  if (i >= span.hi) return;
+  const int64_t row = a.row0 + in_launch, i = a.reverse ? span.hi - 1 - row : span.lo + row;
+  if (row >= span.hi - span.lo) return;
   const int32_t lo = part * a.part_len;
   const int32_t hi = a.C - lo < a.part_len ? a.C : lo + a.part_len;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
@@ -376,8 +417,12 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   if ((FROM == kSums || FROM == kParts) && named) {
     float ref = -kInf;
     const int32_t c0 = tid * VE;
-    for (int32_t base = lo; base < hi; base += NT * BLK) {
-      const RawBlock<DT> raw = load_block<DT, NT>(xr, base, hi);
+    RawBlock<DT> raw = load_block<DT, NT>(xr, lo, hi);
+    for (int32_t base = lo;;) {
+      RawBlock<DT> next;
+      const bool more = base + NT * BLK < hi;
+      if (more) next = load_block<DT, NT>(xr, base + NT * BLK, hi);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         float f[VE];
@@ -395,6 +440,9 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
         o += (double)sum_of(f);
         __builtin_amdgcn_sched_barrier(0);  // (vector by vector: fewer registers)
       }
+      if (!more) break;
+      base += NT * BLK;
+      raw = next;
     }
     const float mine = m;
     m = block_max<NT>(m, sh_m);
@@ -477,10 +525,9 @@ struct PairArgs {
 // count (statistics other than (0, 0)), in FP64 in a fixed order, then the slope of
 // each row.  logp is taken from the statistics again: its FP32 value is off by up to
 // 2^-24 |logp|, some 10 times what o is, and the sums are small differences of many.
-constexpr int kPairThreads = 256;
-template <int DT>
-__global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
-  __shared__ double sh[2][2][kPairThreads / 64];
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT) k_pairs(const PairArgs a) {
+  __shared__ double sh[4][NT / 64];
   const int tid = threadIdx.x, wid = tid >> 6;
   const int64_t p = blockIdx.x;
   int64_t cut[3];
@@ -493,35 +540,41 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
     bad = bad || cut[u] != v;
   }
   if (bad && tid == 0) dev_error(a.err, GBDT_E_RANGE);
-  auto counts = [&](int64_t i) { return !(a.stats[2 * i] == 0.0f && a.stats[2 * i + 1] == 0.0f); };
-  auto score = [&](int64_t i) {  // (of a row that counts: its class is in range)
-    return Score<DT>::to_f32(static_cast<const typename Score<DT>::Elem*>(a.x)[i * a.ld + a.cls[i]]);
+  // a row's class and score, if it counts; sum: logp - ref and rows of both sequences
+  uint32_t moves = 0u;  // the thread's first 32 rows: whether they have a gradient
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  auto score = [&](int64_t i, bool& counts) {
+    const float m = a.stats[2 * i], o = a.stats[2 * i + 1];
+    const int32_t cls = a.cls[i];
+    counts = !(m == 0.0f && o == 0.0f);
+    return counts ? Score<DT>::to_f32(static_cast<const typename Score<DT>::Elem*>(a.x)[i * a.ld + cls]) : -kInf;
   };
-  double sum[2], count[2];
+  int32_t turn = 0;
+  for (int64_t i = cut[0] + tid; i < cut[2]; i += NT, ++turn) {
+    const double ref = a.ref_logp == nullptr ? 0.0 : (double)a.ref_logp[i];
+    bool counts;
+    const float xa = score(i, counts);
+    if (!counts) continue;
+    const double lead = row_end(a.inv_T, true, a.stats[2 * i], a.stats[2 * i + 1], xa).logp - ref;
+    const bool second = i >= cut[1];
+    sum[0] += second ? 0.0 : lead;
+    sum[1] += second ? lead : 0.0;
+    sum[2] += second ? 0.0 : 1.0;
+    sum[3] += second ? 1.0 : 0.0;
+    if (turn < 32) moves |= xa == -kInf ? 0u : 1u << turn;
+  }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    sum[s] = 0.0;
-    int64_t rows = 0;
-    for (int64_t i = cut[s] + tid; i < cut[s + 1]; i += kPairThreads) {
-      if (!counts(i)) continue;
-      const RowEnd e = row_end(a.inv_T, true, a.stats[2 * i], a.stats[2 * i + 1], score(i));
-      sum[s] += e.logp - (a.ref_logp == nullptr ? 0.0 : (double)a.ref_logp[i]);
-      ++rows;
-    }
+  for (int s = 0; s < 4; ++s) {
     sum[s] = wave_sum(sum[s]);
-    count[s] = wave_sum((double)rows);
-    if ((tid & 63) == 0) {
-      sh[s][0][wid] = sum[s];
-      sh[s][1][wid] = count[s];
-    }
+    if ((tid & 63) == 0) sh[s][wid] = sum[s];
   }
   __syncthreads();
+#pragma unroll
+  for (int s = 0; s < 4; ++s) sum[s] = across_waves<NT / 64>(sh[s], [](double u, double v) { return u + v; });
   double per[2], reward[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    sum[s] = across_waves<kPairThreads / 64>(sh[s][0], [](double u, double v) { return u + v; });
-    count[s] = across_waves<kPairThreads / 64>(sh[s][1], [](double u, double v) { return u + v; });
-    per[s] = a.average && count[s] > 1.0 ? 1.0 / count[s] : 1.0;
+    per[s] = a.average && sum[2 + s] > 1.0 ? 1.0 / sum[2 + s] : 1.0;
     reward[s] = a.beta * sum[s] * per[s];
   }
   // (1 - e) log(1 + e^-z) + e log(1 + e^z), and its slope
@@ -541,12 +594,12 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
   }
   const float wt = a.weight == nullptr ? 1.0f : a.weight[p];
   slope = wt == 0.0f ? 0.0 : slope * (double)wt * a.beta;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const float d = (float)((s == 0 ? slope : -slope) * per[s]);
-    for (int64_t i = cut[s] + tid; i < cut[s + 1]; i += kPairThreads) {
-      a.dlogp[i] = counts(i) && score(i) != -kInf ? d : 0.0f;
-    }
+  const float d[2] = {(float)(slope * per[0]), (float)(-slope * per[1])};
+  turn = 0;
+  for (int64_t i = cut[0] + tid; i < cut[2]; i += NT, ++turn) {
+    bool counts, moving = moves >> (turn & 31) & 1u;
+    if (turn >= 32) moving = score(i, counts) != -kInf;
+    a.dlogp[i] = moving ? d[i >= cut[1]] : 0.0f;
   }
 }
 
@@ -554,7 +607,8 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs a) {
 
 template <int DT, int R, int CMAX, int FROM>
 void launch_short(const LogpArgs& a, hipStream_t s) {
-  const size_t lds = size_t(R) * 4 * (a.C | 1);
+  // (a row's last step of classes, and the last vector, may end behind the rows)
+  const size_t lds = size_t(R) * 4 * (a.C | 1) + 32;
   diag_begin(kDiagClassLogp, s);
   hipLaunchKernelGGL((k_logp_short<DT, R, CMAX, FROM>), dim3((unsigned)((a.n + R - 1) / R)), dim3(R), lds, s, a);
   diag_end(s);
@@ -625,7 +679,7 @@ int launch_logp(LogpArgs a, hipStream_t s) {
     } else {
       launch_block<DT, 256, FROM>(a, s);
     }
-  } else if (a.C <= 40000) {
+  } else if (a.C <= 40000 || a.grad == nullptr) {
     launch_block<DT, 256, FROM>(a, s);
   } else {
     launch_block<DT, 1024, FROM>(a, s);
@@ -717,6 +771,18 @@ int check_pairs(const gbdt_pairs* p) {
   return GBDT_OK;
 }
 
+// 1,024 threads where a pair has more rows than that in the mean: each of a thread's
+// rows costs two latencies.
+template <int DT>
+void launch_pairs_of(const PairArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.n_pairs);
+  if (a.n / a.n_pairs > 512) {
+    hipLaunchKernelGGL((k_pairs<DT, 1024>), grid, dim3(1024), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_pairs<DT, 256>), grid, dim3(256), 0, s, a);
+  }
+}
+
 int launch_pairs(const gbdt_pairs& p, const gbdt_scores& x, const int32_t* classes, double temperature,
                  const float* stats, float* loss, float* rewards, float* dlogp, void* ws, hipStream_t s) {
   PairArgs a = {};
@@ -737,12 +803,11 @@ int launch_pairs(const gbdt_pairs& p, const gbdt_scores& x, const int32_t* class
   a.rewards = rewards;
   a.dlogp = dlogp;
   a.err = &static_cast<WsCtrl*>(ws)->err;
-  const dim3 grid((unsigned)p.n_pairs), block(kPairThreads);
   diag_begin(kDiagPairs, s);
   switch (x.dtype) {
-    case GBDT_DTYPE_F32: hipLaunchKernelGGL(k_pairs<GBDT_DTYPE_F32>, grid, block, 0, s, a); break;
-    case GBDT_DTYPE_BF16: hipLaunchKernelGGL(k_pairs<GBDT_DTYPE_BF16>, grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL(k_pairs<GBDT_DTYPE_F16>, grid, block, 0, s, a);
+    case GBDT_DTYPE_F32: launch_pairs_of<GBDT_DTYPE_F32>(a, s); break;
+    case GBDT_DTYPE_BF16: launch_pairs_of<GBDT_DTYPE_BF16>(a, s); break;
+    default: launch_pairs_of<GBDT_DTYPE_F16>(a, s);
   }
   diag_end(s);
   const hipError_t e = hipGetLastError();
@@ -783,6 +848,7 @@ int preference(const gbdt_scores* x, const int32_t* classes, double temperature,
   if (rc || !step || x->n_rows == 0) return rc;
   a.logp = nullptr;
   a.dlogp = dlogp;
+  a.reverse = 1;  // the rows read last are still in the last-level cache
   a.grad = grad;
   a.ldg = grad_stride;
   return launch_logp<kStats>(x->dtype, a, s);

@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
   int32_t e0 = group * a.group_size + within * a.per_lane, e1 = e0 + a.per_lane;
   e1 = e1 < group_end ? e1 : group_end;
   if (group >= a.groups || e0 >= e1) e0 = e1 = 0;
-  const int32_t count = e1 - e0;
   float x[V * VE];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -137,8 +136,12 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
   if (a.by_value) {
     if (a.bias != nullptr) {
 #pragma unroll
-      for (int e = 0; e < EPL; ++e)
-        if (e < count) v[e] += (double)a.bias[e0 + e];
+      for (int j = 0; j < EPL / 4; ++j) {
+        float f[4];
+        load_chunk<GBDT_DTYPE_F32>(a.bias, e0 + j * 4, e1, f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[j * 4 + q] += (double)f[q];
+      }
     }
 #pragma unroll
     for (int e = 0; e < EPL; ++e) v[e] = x[e] > -kInf && v[e] == v[e] ? v[e] : -__builtin_inf();
@@ -411,21 +414,43 @@ template <int NT>
 __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
   constexpr int W = NT / 64, EPT = (GBDT_MAX_EXPERTS + NT - 1) / NT;
   __shared__ uint32_t next[W][GBDT_MAX_EXPERTS];
+  __shared__ int32_t total_of[GBDT_MAX_EXPERTS], before_of[GBDT_MAX_EXPERTS];
   __shared__ int32_t sh[32];
   const int tid = threadIdx.x, wid = tid >> 6, lane = tid & 63;
   const int64_t lo = int64_t(blockIdx.x) * a.chunk, hi = a.n - lo < a.chunk ? a.n : lo + a.chunk;
   const int64_t share = (a.chunk + W * 64 - 1) / (W * 64) * 64;
   const int64_t from_all = lo + wid * share, from = from_all < hi ? from_all : hi;
   const int64_t to = hi - from < share ? hi : from + share;
-  for (int w = 0; w < W; ++w)
-    for (int e = tid; e < a.E; e += NT) next[w][e] = 0u;
+  for (int e = tid; e < a.E; e += NT) {
+    for (int w = 0; w < W; ++w) next[w][e] = 0u;
+    total_of[e] = before_of[e] = 0;
+  }
   __syncthreads();
   for (int64_t p = from + lane; p < to; p += 64) {
     const int32_t c = listed_class(a, p, true);
     if (c >= 0) atomicAdd(&next[wid][c], 1u);
   }
   __syncthreads();
-  // experts tid * EPT ..: all workgroups' counts, and those before this one
+  // All workgroups' counts, and those before this one: where experts are few, several
+  // threads share an expert's workgroups.
+  if (a.blocks > 1) {
+    int32_t width = 1;
+    while (width < a.E) width *= 2;
+    width = width < NT ? width : NT;
+    const int32_t first = tid / width, step = NT / width;
+    for (int32_t e = tid & (width - 1); e < a.E; e += width) {
+      int32_t all = 0, before = 0;
+#pragma unroll 16
+      for (int32_t b = first; b < a.blocks; b += step) {
+        const int32_t v = a.counts[b * a.E + e];
+        all += v;
+        before += b < (int32_t)blockIdx.x ? v : 0;
+      }
+      atomicAdd(&total_of[e], all);
+      atomicAdd(&before_of[e], before);
+    }
+    __syncthreads();
+  }
   int32_t all[EPT], before[EPT], sum = 0;
 #pragma unroll
   for (int u = 0; u < EPT; ++u) {
@@ -435,12 +460,8 @@ __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
       if (a.blocks == 1) {
         for (int w = 0; w < W; ++w) all[u] += next[w][e];
       } else {
-#pragma unroll 8
-        for (int b = 0; b < a.blocks; ++b) {
-          const int32_t v = a.counts[int64_t(b) * a.E + e];
-          all[u] += v;
-          before[u] += b < (int)blockIdx.x ? v : 0;
-        }
+        all[u] = total_of[e];
+        before[u] = before_of[e];
       }
     }
     sum += all[u];
