@@ -242,8 +242,7 @@ __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
   }
   if ((C & 1) && a.ld == C) {
     Vec16<DT> raw[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) raw[j] = load_tail<DT>(xg, (tid + j * R) * VE, all);
+    load_vecs<DT, V>(xg, tid * VE, R * VE, all, raw);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int32_t e = (tid + j * R) * VE;
@@ -336,13 +335,12 @@ __global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
   const int64_t i = mine ? i_all : span.hi - 1;
   const int32_t C = a.C, c0 = lane * VE;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-  Vec16<DT> raw[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) raw[j] = load_tail<DT>(xr, c0 + j * NT * VE, C);
   const int32_t cls = row_class(a, i, mine && lane == 0);
   const bool named = cls >= 0;
-  const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
   const RowIn in = row_in<FROM>(a, i);
+  Vec16<DT> raw[V];
+  load_vecs<DT, V>(xr, c0, NT * VE, C, raw);
+  const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
   float m = -kInf;
   double o = 0.0;
   if (FROM == kStats) {
@@ -387,6 +385,15 @@ __global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
   }
 }
 
+// The sums of a wave's lanes, each o against its own m, as one against the largest m.
+__device__ __forceinline__ void join_lanes(double c, float& m, double& o) {
+  const float top = wave_max(m);
+  // (o of 0 or NaN stays what it is; a maximum of -inf has o = 0 or NaN)
+  if (m != top && m != -kInf) o *= exp2_64(((double)m - (double)top) * c);
+  m = top;
+  o = wave_sum(o);
+}
+
 // One workgroup per row, or per part of one: part_len classes (a multiple of
 // NT * kBlk) of a row that n_parts workgroups share.  The sum is taken against a
 // reference that is the first maximum the thread meets and moves only when a
@@ -410,19 +417,16 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   const int32_t lo = part * a.part_len;
   const int32_t hi = a.C - lo < a.part_len ? a.C : lo + a.part_len;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  constexpr bool kFromScores = FROM == kSums || FROM == kParts;
   const int32_t cls = row_class(a, i, tid == 0 && part == 0);
   const bool named = cls >= 0;
   float m = -kInf;
   double o = 0.0;
-  if ((FROM == kSums || FROM == kParts) && named) {
+  if (kFromScores && named) {
     float ref = -kInf;
     const int32_t c0 = tid * VE;
     RawBlock<DT> raw = load_block<DT, NT>(xr, lo, hi);
     for (int32_t base = lo;;) {
-      RawBlock<DT> next;
-      const bool more = base + NT * BLK < hi;
-      if (more) next = load_block<DT, NT>(xr, base + NT * BLK, hi);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         float f[VE];
@@ -440,17 +444,23 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
         o += (double)sum_of(f);
         __builtin_amdgcn_sched_barrier(0);  // (vector by vector: fewer registers)
       }
-      if (!more) break;
       base += NT * BLK;
-      raw = next;
+      if (base >= hi) break;
+      raw = load_block<DT, NT>(xr, base, hi);
     }
-    const float mine = m;
-    m = block_max<NT>(m, sh_m);
-    if (ref != m && mine != -kInf) o *= exp2_64(((double)ref - (double)m) * a.c);
-    o = block_sum<NT>(o, sh_o);
+    if (ref != m && m != -kInf) o *= exp2_64(((double)ref - (double)m) * a.c);
+    join_lanes(a.c, m, o);
+    if ((tid & 63) == 0) {
+      sh_m[tid >> 6] = m;
+      sh_o[tid >> 6] = o;
+    }
+    __syncthreads();
+    m = sh_m[tid & (W - 1)];
+    o = (tid & 63) < W ? sh_o[tid & (W - 1)] : 0.0;
+    join_lanes(a.c, m, o);
   }
+  PartSum* __restrict__ parts = a.parts + row * a.n_parts;
   if constexpr (FROM == kParts) {
-    PartSum* __restrict__ parts = a.parts + row * a.n_parts;
     if (tid == 0) {
       __hip_atomic_store(&parts[part].o, o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(&parts[part].m, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -465,23 +475,23 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
     if (tid == 0) __hip_atomic_store(&a.tickets[row], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   if constexpr (FROM == kJoin || FROM == kParts) {
-    PartSum* __restrict__ parts = a.parts + row * a.n_parts;
-    float part_m = -kInf;
-    double part_o = 0.0;
-    if (tid < a.n_parts) {  // (at most 64 parts, as many as a row has steps of the split)
-      part_o = __hip_atomic_load(&parts[tid].o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      part_m = __hip_atomic_load(&parts[tid].m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    m = -kInf;
+    o = 0.0;
+    const int lane = tid & 63;
+    if (lane < a.n_parts) {  // (at most 64 parts, as many as a row has steps of the split)
+      o = __hip_atomic_load(&parts[lane].o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      m = __hip_atomic_load(&parts[lane].m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    m = block_max<NT>(part_m, sh_m);
-    if (part_m != m && part_m != -kInf) part_o *= exp2_64(((double)part_m - (double)m) * a.c);
-    o = block_sum<NT>(part_o, sh_o);
+    join_lanes(a.c, m, o);
   } else if constexpr (FROM == kStats) {
     m = a.stats[2 * i];
     o = a.stats[2 * i + 1];
   }
+  const RowIn in = row_in<FROM>(a, i);
   const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
+  if (a.grad == nullptr && tid >= 64) return;  // (what is left is one thread's)
   const bool write = tid == 0 && (FROM == kParts || part == 0);
-  const RowGrad g = row_out<FROM>(a, i, write, named, row_in<FROM>(a, i), m, o, xa);
+  const RowGrad g = row_out<FROM>(a, i, write, named, in, m, o, xa);
   if (FROM != kParts && a.grad != nullptr) {
     const float mf = m == -kInf ? 0.0f : m;
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;

@@ -33,7 +33,7 @@ struct RouteArgs {
   const void* x;
   int64_t n, ld;
   int32_t E, k;
-  int32_t sigmoid, renorm, by_value;
+  int32_t sigmoid, renorm;
   int32_t groups, kept, top, group_size;
   int32_t per_lane;   // experts of a lane, at most EPL
   int32_t log_lanes;  // lanes of a group of experts, as a power of two
@@ -50,22 +50,58 @@ struct RouteArgs {
 // A score as the softmax has it: NaN is out of service, +inf the largest number.
 __device__ __forceinline__ float in_service(float f) { return f == f ? __builtin_fminf(f, kMaxF32) : -kInf; }
 
-// A lane's value from another one of its row of 16 lanes.
-template <int CTRL>
-__device__ __forceinline__ double dpp_f64(double v) {
-  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true);
-  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
-  return __hiloint2double(hi, lo);
-}
-// The largest value of NT neighbouring lanes, in all of them; no NaN among them.
-template <int NT>
-__device__ __forceinline__ double lanes_max(double v) {
-  if constexpr (NT >= 2) v = __builtin_fmax(v, dpp_f64<0xB1>(v));   // quad_perm 1, 0, 3, 2
-  if constexpr (NT >= 4) v = __builtin_fmax(v, dpp_f64<0x4E>(v));   // quad_perm 2, 3, 0, 1
-  if constexpr (NT >= 8) v = __builtin_fmax(v, dpp_f64<0x141>(v));  // row_half_mirror
-  if constexpr (NT >= 16) v = __builtin_fmax(v, dpp_f64<0x140>(v)); // row_mirror
-  if constexpr (NT >= 32) v = __builtin_fmax(v, __shfl_xor(v, 16, 64));
-  if constexpr (NT >= 64) v = __builtin_fmax(v, __shfl_xor(v, 32, 64));
+// The choice's keys: the scores themselves, or choice values in FP64.  `taken` is
+// below all keys but -inf; an FP64 key is taken by its upper word alone, whatever the
+// lower one.  The larger of two keys: no NaN comes here, so FP64 has the bare
+// instruction (the compiler's own would quiet both operands first).
+template <bool BY_VALUE>
+struct RouteKey;
+template <>
+struct RouteKey<false> {
+  using T = float;
+  static __device__ __forceinline__ T taken() { return -kInf; }
+  static __device__ __forceinline__ T take(T v, bool it) { return it ? -kInf : v; }
+  static __device__ __forceinline__ T larger(T a, T b) { return __builtin_fmaxf(a, b); }
+  static __device__ __forceinline__ T smaller(T a, T b) { return __builtin_fminf(a, b); }
+  template <int CTRL>
+  static __device__ __forceinline__ T moved(T v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+  }
+};
+template <>
+struct RouteKey<true> {
+  using T = double;
+  static __device__ __forceinline__ T taken() { return -0x1p1022; }
+  static __device__ __forceinline__ T take(T v, bool it) {
+    return __hiloint2double(it ? __double2hiint(taken()) : __double2hiint(v), __double2loint(v));
+  }
+  static __device__ __forceinline__ T larger(T a, T b) {
+    T r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
+  static __device__ __forceinline__ T smaller(T a, T b) {
+    T r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
+  template <int CTRL>
+  static __device__ __forceinline__ T moved(T v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
+    return __hiloint2double(hi, lo);
+  }
+};
+
+// The largest key of NT neighbouring lanes, in all of them.
+template <typename K, int NT>
+__device__ __forceinline__ typename K::T lanes_max(typename K::T v) {
+  if constexpr (NT >= 2) v = K::larger(v, K::template moved<0xB1>(v));   // quad_perm 1, 0, 3, 2
+  if constexpr (NT >= 4) v = K::larger(v, K::template moved<0x4E>(v));   // quad_perm 2, 3, 0, 1
+  if constexpr (NT >= 8) v = K::larger(v, K::template moved<0x141>(v));  // row_half_mirror
+  if constexpr (NT >= 16) v = K::larger(v, K::template moved<0x140>(v)); // row_mirror
+  if constexpr (NT >= 32) v = K::larger(v, __shfl_xor(v, 16, 64));
+  if constexpr (NT >= 64) v = K::larger(v, __shfl_xor(v, 32, 64));
   return v;
 }
 
@@ -76,17 +112,22 @@ __device__ __forceinline__ double sigmoid_64(float x) {
 }
 
 // NT lanes a row, EPL experts a lane at most, neighbours, and no lane with experts of
-// two groups: of equal values the first is in the lowest lane that has one.  The
-// choice takes k rounds: the row's largest value by lane moves, the lane that has
-// it by a ballot.
-template <int DT, int NT, int EPL>
+// two groups: of equal keys the first is in the lowest lane that has one.  The
+// choice takes k rounds: the row's largest key by lane moves, the lane that has it by
+// a ballot, its first place there by comparisons.  Round j's score is kept by the lane
+// that works out weight j: the key itself, or read again where the key is a value.
+template <int DT, int NT, int EPL, bool BY_VALUE>
 __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
   using Elem = typename Score<DT>::Elem;
+  using K = RouteKey<BY_VALUE>;
+  using Key = typename K::T;
   constexpr int VE = Score<DT>::kVec, V = (EPL + VE - 1) / VE;
   constexpr int kRows = kRouteThreads / NT;
+  constexpr int kMost = (GBDT_MAX_ROUTED + NT - 1) / NT;
   __shared__ int32_t all_chosen[kRows][GBDT_MAX_ROUTED];
   const int lane = threadIdx.x & (NT - 1), sub = threadIdx.x / NT;
   const int first_lane = (threadIdx.x & 63) & ~(NT - 1);  // of the row, in the wave
+  const uint64_t below = ((uint64_t(1) << lane) - 1) << first_lane;  // the row's lanes below this one
   const int64_t row = int64_t(blockIdx.x) * kRows + sub;
   const bool mine = row < a.n;
   const int64_t i = mine ? row : a.n - 1;
@@ -97,130 +138,153 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
   int32_t e0 = group * a.group_size + within * a.per_lane, e1 = e0 + a.per_lane;
   e1 = e1 < group_end ? e1 : group_end;
   if (group >= a.groups || e0 >= e1) e0 = e1 = 0;
-  float x[V * VE];
+  const int32_t count = e1 - e0;
+  float x[V * VE], bias[EPL];
+  {
+    Vec16<DT> raw[V];
+    Vec16<GBDT_DTYPE_F32> raw_bias[EPL / 4];
+    load_vecs<DT, V>(xr, e0, VE, a.E, raw);
+    if (BY_VALUE && a.bias != nullptr) load_vecs<GBDT_DTYPE_F32, EPL / 4>(a.bias, e0, 4, a.E, raw_bias);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    float f[VE];
-    load_chunk<DT>(xr, e0 + j * VE, e1, f);
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      unpack<DT>(raw[j], f);
 #pragma unroll
-    for (int q = 0; q < VE; ++q) x[j * VE + q] = f[q] == f[q] ? f[q] : -kInf;
+      for (int q = 0; q < VE; ++q) x[j * VE + q] = __builtin_fmaxf(f[q], -kInf);  // (NaN: -inf)
+    }
+    if (BY_VALUE && a.bias != nullptr) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) bias[e] = __uint_as_float(raw_bias[e / 4].w[e % 4]);
+    }
+  }
+  if (__any(count < EPL)) {  // what is another lane's
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) x[e] = e < count ? x[e] : -kInf;
   }
   // the softmax's maximum and sum
-  double top_x = 0.0, total = 1.0;
-  if (!a.sigmoid && (a.by_value || !a.renorm)) {
+  const bool softmax = !a.sigmoid && (BY_VALUE || !a.renorm);
+  double top_x = 0.0, inv_total = 1.0;
+  Key v[EPL];
+  if (softmax) {
     float m = -kInf;
 #pragma unroll
     for (int e = 0; e < EPL; ++e) m = __builtin_fmaxf(m, x[e]);
     m = __builtin_fminf(group_max<NT>(m), kMaxF32);
     top_x = m == -kInf ? 0.0 : (double)m;
-  }
-  double v[EPL];
-  if (a.sigmoid) {
-    if (a.by_value) {
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) v[e] = sigmoid_64(x[e]);
-    }
-  } else if (a.by_value || !a.renorm) {
-    total = 0.0;
+    double total = 0.0;
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
-      v[e] = exp2_64(((double)__builtin_fminf(x[e], kMaxF32) - top_x) * kLog2e);
-      total += v[e];
+      const double w = exp2_64(((double)__builtin_fminf(x[e], kMaxF32) - top_x) * kLog2e);
+      total += w;
+      if constexpr (BY_VALUE) v[e] = w;
     }
     total = group_sum<NT>(total);
-    const double inv = total > 0.0 ? 1.0 / total : 0.0;
+    inv_total = total > 0.0 ? 1.0 / total : 0.0;
+    if constexpr (BY_VALUE) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) v[e] *= inv;
-    total = inv;
+      for (int e = 0; e < EPL; ++e) v[e] *= inv_total;
+    }
+  } else if constexpr (BY_VALUE) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) v[e] = sigmoid_64(x[e]);
   }
-  if (a.by_value) {
+  if constexpr (BY_VALUE) {
     if (a.bias != nullptr) {
 #pragma unroll
-      for (int j = 0; j < EPL / 4; ++j) {
-        float f[4];
-        load_chunk<GBDT_DTYPE_F32>(a.bias, e0 + j * 4, e1, f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[j * 4 + q] += (double)f[q];
+      for (int e = 0; e < EPL; ++e) {
+        v[e] += (double)bias[e];
+        v[e] = v[e] == v[e] ? v[e] : -__builtin_inf();
       }
     }
+    float least = x[0];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) v[e] = x[e] > -kInf && v[e] == v[e] ? v[e] : -__builtin_inf();
+    for (int e = 1; e < EPL; ++e) least = __builtin_fminf(least, x[e]);
+    if (__any(least == -kInf)) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[e] = x[e] > -kInf ? v[e] : -__builtin_inf();
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) v[e] = (double)x[e];
+    for (int e = 0; e < EPL; ++e) v[e] = x[e];
   }
   if (a.groups > 1) {
     // a group's two largest: of a lane's, then of its lanes'
-    double t1 = -__builtin_inf(), t2 = t1;
+    Key t1 = -__builtin_inf(), t2 = t1;
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
-      t2 = __builtin_fmax(t2, __builtin_fmin(t1, v[e]));
-      t1 = __builtin_fmax(t1, v[e]);
+      if (BY_VALUE) t2 = K::larger(t2, K::smaller(t1, v[e]));
+      t1 = K::larger(t1, v[e]);
     }
     for (int off = 1; off < 1 << a.log_lanes; off <<= 1) {
-      const double o1 = __shfl_xor(t1, off, 64), o2 = __shfl_xor(t2, off, 64);
-      t2 = __builtin_fmax(__builtin_fmax(t2, o2), __builtin_fmin(t1, o1));
-      t1 = __builtin_fmax(t1, o1);
+      const Key o1 = __shfl_xor(t1, off, 64);
+      if (BY_VALUE) t2 = K::larger(K::larger(t2, __shfl_xor(t2, off, 64)), K::smaller(t1, o1));
+      t1 = K::larger(t1, o1);
     }
-    double rank = t1;
-    if (a.top == 2 && t2 > -__builtin_inf()) rank = t1 + t2;
-    rank = rank == rank ? rank : -__builtin_inf();
+    Key rank = t1;
+    if (BY_VALUE && a.top == 2 && t2 > -__builtin_inf()) rank = t1 + t2;
     int32_t before = 0;  // groups ahead of this one
     for (int32_t g = 0; g < a.groups; ++g) {
-      const double other = __shfl(rank, first_lane + (g << a.log_lanes), 64);
+      const Key other = __shfl(rank, first_lane + (g << a.log_lanes), 64);
       before += other > rank || (other == rank && g < group);
     }
-    if (before >= a.kept) {
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) v[e] = -__builtin_inf();
-    }
+    for (int e = 0; e < EPL; ++e) v[e] = K::take(v[e], before >= a.kept);
   }
-  // (classes -1 where nothing is left)
-  for (int32_t j = lane; j < a.k; j += NT) chosen[j] = -1;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
+  float xc[kMost], m = -kInf;
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) xc[u] = -kInf;
   for (int32_t j = 0; j < a.k; ++j) {
-    double best = v[0];
+    Key part[EPL];
 #pragma unroll
-    for (int e = 1; e < EPL; ++e) best = __builtin_fmax(best, v[e]);
-    const double top = lanes_max<NT>(best);
-    const bool has = best == top && top > -__builtin_inf();
-    const uint64_t who = __ballot(has) >> first_lane & (~uint64_t(0) >> (64 - NT));
-    if (has && lane == __ffsll((unsigned long long)who) - 1) {
-      int32_t at = EPL;
+    for (int e = 0; e < EPL; ++e) part[e] = v[e];
 #pragma unroll
-      for (int e = EPL - 1; e >= 0; --e) at = v[e] == top ? e : at;
+    for (int w = EPL / 2; w > 0; w /= 2) {
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) v[e] = e == at ? -__builtin_inf() : v[e];
-      chosen[j] = e0 + at;
+      for (int e = 0; e < w; ++e) part[e] = K::larger(part[e], part[e + w]);
+    }
+    const Key top = lanes_max<K, NT>(part[0]);
+    const bool left = top > K::taken(), has = part[0] == top && left;
+    bool open = has && (__ballot(has) & below) == 0;  // this lane's, and not yet found
+    const bool wins = open;
+    int32_t at = 0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      const bool it = open && v[e] == top;
+      v[e] = K::take(v[e], it);
+      at = it ? e : at;
+      open = open && !it;
+    }
+    // (class -1 where nothing is left)
+    if (left ? wins : lane == 0) chosen[j] = left ? e0 + at : -1;
+    if constexpr (!BY_VALUE) {
+#pragma unroll
+      for (int u = 0; u < kMost; ++u) xc[u] = j == lane + u * NT ? __builtin_fminf(top, kMaxF32) : xc[u];
     }
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
   // the weights of places lane, lane + NT, ...
-  constexpr int kMost = (GBDT_MAX_ROUTED + NT - 1) / NT;
   double s[kMost], sum = 0.0;
   int32_t cls[kMost];
-  float xc[kMost], m = -kInf;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int u = 0; u < kMost; ++u) {
     const int32_t j = lane + u * NT;
     cls[u] = j < a.k ? chosen[j] : -1;
-    xc[u] = -kInf;
-    if (cls[u] >= 0) xc[u] = __builtin_fminf(Score<DT>::to_f32(xr[cls[u]]), kMaxF32);
-    m = __builtin_fmaxf(m, xc[u]);
+    if (BY_VALUE && cls[u] >= 0) xc[u] = __builtin_fminf(Score<DT>::to_f32(xr[cls[u]]), kMaxF32);
   }
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) m = __builtin_fmaxf(m, xc[u]);
   if (!a.sigmoid && a.renorm) {
     // of the chosen alone: against the largest of them
     m = group_max<NT>(m);
     top_x = m == -kInf ? 0.0 : (double)m;
-    total = 1.0;
+    inv_total = 1.0;
   }
 #pragma unroll
   for (int u = 0; u < kMost; ++u) {
     s[u] = 0.0;
-    if (cls[u] >= 0)
-      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - top_x) * kLog2e) * total;
+    if (u * NT < a.k && xc[u] > -kInf)
+      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - top_x) * kLog2e) * inv_total;
     sum += s[u];
   }
   double by = a.scale;
@@ -274,10 +338,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
   }
   Vec16<DT> raw[V];
   float m = -kInf;
-  if (whole) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) raw[j] = load_tail<DT>(xr, c0 + j * NT * VE, E);
-  }
+  if (whole) load_vecs<DT, V>(xr, c0, NT * VE, E, raw);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
 #pragma unroll
@@ -512,12 +573,12 @@ __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
 
 // -------------------------------------------------------------------- host --
 
-template <int DT, int NT, int EPL>
+template <int DT, int NT, int EPL, bool BY_VALUE>
 void launch_route(const RouteArgs& a, hipStream_t s) {
   constexpr int64_t kRows = kRouteThreads / NT;
   diag_begin(kDiagRoute, s);
-  hipLaunchKernelGGL((k_route<DT, NT, EPL>), dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kRouteThreads), 0, s,
-                     a);
+  hipLaunchKernelGGL((k_route<DT, NT, EPL, BY_VALUE>), dim3((unsigned)((a.n + kRows - 1) / kRows)),
+                     dim3(kRouteThreads), 0, s, a);
   diag_end(s);
 }
 
@@ -529,6 +590,9 @@ void launch_route_grad(const RouteArgs& a, hipStream_t s) {
                      a);
   diag_end(s);
 }
+
+// Rows that all run at once get a wave each: fewer experts a lane, shorter rounds.
+constexpr int64_t kRouteFewRows = 1024;
 
 // The lanes of a row: as many as its experts need at EPL each, and at least one a
 // group; a group has a power of two of them.
@@ -545,24 +609,27 @@ bool route_fits(RouteArgs& a) {
   return true;
 }
 
-template <int DT>
+template <int DT, bool BY_VALUE>
 int route_rows(RouteArgs a, hipStream_t s) {
-  if (route_fits<4, 8>(a)) {
-    launch_route<DT, 4, 8>(a, s);
-  } else if (route_fits<8, 8>(a)) {
-    launch_route<DT, 8, 8>(a, s);
-  } else if (route_fits<16, 8>(a)) {
-    launch_route<DT, 16, 8>(a, s);
-  } else if (route_fits<16, 16>(a)) {
-    launch_route<DT, 16, 16>(a, s);
-  } else if (route_fits<32, 16>(a)) {
-    launch_route<DT, 32, 16>(a, s);
+  const bool few = a.n <= kRouteFewRows;
+  if (few && route_fits<64, 4>(a)) {
+    launch_route<DT, 64, 4, BY_VALUE>(a, s);
+  } else if (!few && route_fits<4, 8>(a)) {
+    launch_route<DT, 4, 8, BY_VALUE>(a, s);
+  } else if (!few && route_fits<8, 8>(a)) {
+    launch_route<DT, 8, 8, BY_VALUE>(a, s);
+  } else if (!few && route_fits<16, 8>(a)) {
+    launch_route<DT, 16, 8, BY_VALUE>(a, s);
+  } else if (!few && route_fits<16, 16>(a)) {
+    launch_route<DT, 16, 16, BY_VALUE>(a, s);
+  } else if (!few && route_fits<32, 16>(a)) {
+    launch_route<DT, 32, 16, BY_VALUE>(a, s);
   } else if (route_fits<64, 16>(a)) {
-    launch_route<DT, 64, 16>(a, s);
+    launch_route<DT, 64, 16, BY_VALUE>(a, s);
   } else {
     // (3, 5, 9, 17, 33 and a few more groups leave lanes over; a lane then has up to 31 experts)
     route_fits<64, 32>(a);
-    launch_route<DT, 64, 32>(a, s);
+    launch_route<DT, 64, 32, BY_VALUE>(a, s);
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_route");
@@ -645,12 +712,14 @@ int gbdt_route_classes(const gbdt_scores* x, const gbdt_routing* r, const float*
   a.bias = bias;
   a.classes = classes;
   a.weights = weights;
-  a.by_value = bias != nullptr || (r->n_groups > 1 && r->group_top == 2);
+  const bool by_value = bias != nullptr || (r->n_groups > 1 && r->group_top == 2);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (x->dtype) {
-    case GBDT_DTYPE_F32: return route_rows<GBDT_DTYPE_F32>(a, s);
-    case GBDT_DTYPE_BF16: return route_rows<GBDT_DTYPE_BF16>(a, s);
-    default: return route_rows<GBDT_DTYPE_F16>(a, s);
+    case GBDT_DTYPE_F32:
+      return by_value ? route_rows<GBDT_DTYPE_F32, true>(a, s) : route_rows<GBDT_DTYPE_F32, false>(a, s);
+    case GBDT_DTYPE_BF16:
+      return by_value ? route_rows<GBDT_DTYPE_BF16, true>(a, s) : route_rows<GBDT_DTYPE_BF16, false>(a, s);
+    default: return by_value ? route_rows<GBDT_DTYPE_F16, true>(a, s) : route_rows<GBDT_DTYPE_F16, false>(a, s);
   }
 }
 

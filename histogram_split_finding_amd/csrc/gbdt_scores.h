@@ -145,6 +145,43 @@ __device__ __forceinline__ void store_tail(typename Score<DT>::Elem* __restrict_
   }
 }
 
+// Vectors [c0 + j step, ...) of a row of C, -inf past the row's end, all loads in
+// flight at once: those that the end cuts, or that lie behind it, are the row's last
+// one, and moved down when all are there.
+template <int DT, int V>
+__device__ __forceinline__ void load_vecs(const typename Score<DT>::Elem* __restrict__ row, int32_t c0, int32_t step,
+                                          int32_t C, Vec16<DT> (&v)[V]) {
+  constexpr int VE = Score<DT>::kVec;
+  constexpr uint32_t inf = DT == GBDT_DTYPE_F32 ? 0xff800000u : DT == GBDT_DTYPE_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+  if (C < VE) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = load_tail<DT>(row, c0 + j * step, C);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int32_t c = c0 + j * step, last = C - VE;
+    v[j] = load_vec<DT>(row + (c < last ? c : last));
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    int32_t down = c0 + j * step - (C - VE);
+    if (down > 0) {
+      Vec16<DT> w = v[j];
+      if constexpr (DT != GBDT_DTYPE_F32) {
+        if (down & 1)
+          w = {{w.w[0] >> 16 | w.w[1] << 16, w.w[1] >> 16 | w.w[2] << 16, w.w[2] >> 16 | w.w[3] << 16,
+                w.w[3] >> 16 | (inf & 0xffff0000u)}};
+        down >>= 1;
+      }
+      if (down & 1) w = {{w.w[1], w.w[2], w.w[3], inf}};
+      if (down & 2) w = {{w.w[2], w.w[3], inf, inf}};
+      if (down > 3) w = {{inf, inf, inf, inf}};
+      v[j] = w;
+    }
+  }
+}
+
 // Classes [c0, c0 + kVec) of a row of C, as FP32; -inf past the row's end.
 template <int DT>
 __device__ __forceinline__ void load_chunk(const typename Score<DT>::Elem* __restrict__ row, int32_t c0,
