@@ -46,8 +46,12 @@ struct LogpArgs {
   int32_t reverse;                     // from the last row to the first
   const int64_t* range;                // rows [range[0], range[last]) only, or NULL: all
   double c, inv_T;                     // log2(e) / T, 1 / T
+  // c as c_hi + c_lo, both positive: rounding c alone would move all terms of a sum the
+  // same way, by D 2^-25 (and c_lo > 0 leaves -inf what it is)
+  float c_hi, c_lo;
   const float *old_logp, *ref_logp, *adv, *weight;
   double low, high, kl;  // borders of the ratio
+  double log_low, log_high;
   float *loss, *logp, *dlogp;
   float* stats;
   void* grad;
@@ -57,6 +61,12 @@ struct LogpArgs {
   uint32_t* tickets;  // [n], zero between calls
   int64_t row0;       // of this launch
 };
+
+// exp(d / T) as a term of a sum, and as a factor of a gradient.
+__device__ __forceinline__ float sum_term(const LogpArgs& a, float d) {
+  return exp2_32(__builtin_fmaf(d, a.c_hi, d * a.c_lo));
+}
+__device__ __forceinline__ float grad_term(const LogpArgs& a, float d) { return exp2_32(d * a.c_hi); }
 
 // The rows of the call, and one of them.
 struct Span {
@@ -160,17 +170,25 @@ __device__ __forceinline__ RowIn row_in(const LogpArgs& a, int64_t i) {
   return r;
 }
 
+// Whether a row's ratio is so near to a border of the clip that FP32 exponentials
+// (off by at most (3 D + 6) 2^-24 in logp, D = |x - m| / T at most 40 where it matters:
+// 7.5e-6) could take it to the other side: such a row's sum is taken again in FP64.
+__device__ __forceinline__ bool next_to_border(const LogpArgs& a, const RowEnd& e, const RowIn& in) {
+  const double y = e.logp - (double)in.old_logp;
+  return a.adv != nullptr && e.live && in.adv != 0.0f &&
+         (__builtin_fabs(y - a.log_low) < 0x1p-16 || __builtin_fabs(y - a.log_high) < 0x1p-16);
+}
+
 // Writes what a row has to say (`write`: by this thread) and returns what its
 // gradient is made of: mine at the class, scale v at the others; both 0 for a row
-// that leaves the scores alone.
+// that leaves the scores alone, whatever they are.
 struct RowGrad {
-  bool any;
   float mine, scale;
+  __device__ __forceinline__ bool any() const { return !(mine == 0.0f && scale == 0.0f); }
 };
 template <int FROM>
-__device__ __forceinline__ RowGrad row_out(const LogpArgs& a, int64_t i, bool write, bool named, const RowIn& in,
+__device__ __forceinline__ RowGrad row_out(const LogpArgs& a, int64_t i, bool write, const RowEnd& e, const RowIn& in,
                                            float m, double o, float xa) {
-  const RowEnd e = row_end(a.inv_T, named, m, o, xa);
   double slope = in.dlogp;
   if (FROM != kStats) {
     PolicyRow p = {0.0, 0.0};
@@ -189,11 +207,12 @@ __device__ __forceinline__ RowGrad row_out(const LogpArgs& a, int64_t i, bool wr
       }
     }
   }
-  RowGrad g;
-  g.any = e.live && xa != -kInf && slope != 0.0;
-  const double k = slope * a.inv_T * e.against;
-  g.mine = (float)k;
-  g.scale = o == 0.0 ? 0.0f : (float)(-k * rcp_64(o));
+  RowGrad g = {0.0f, 0.0f};
+  if (e.live && xa != -kInf && slope != 0.0) {
+    const double k = slope * a.inv_T * e.against;
+    g.mine = (float)k;
+    g.scale = o == 0.0 ? 0.0f : (float)(-k * rcp_64(o));
+  }
   return g;
 }
 
@@ -209,10 +228,9 @@ __device__ __forceinline__ void set_class(float (&f)[VE], int32_t cls, int32_t c
 
 // One thread per row of at most CMAX classes, R rows a workgroup; rows and
 // gradients pass through LDS, so that memory sees whole lines: packed rows of an odd
-// length as they lie there, 16 bytes at a time, others in rows of C | 1 words.  The
-// exponentials are in FP64 (a row's few terms do not average rounding errors away,
-// and a ratio next to the clip's border decides about the row), four classes at a
-// time, -inf behind the row's end.
+// length as they lie there, 16 bytes at a time, others (up to 8 classes; longer ones
+// do not come here) in rows of C | 1 words.  Four classes at a time, -inf behind the
+// row's end.
 constexpr int kShortStep = 4;
 template <int DT, int R, int CMAX, int FROM>
 __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
@@ -240,7 +258,7 @@ __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
       o = a.stats[2 * i + 1];
     }
   }
-  if ((C & 1) && a.ld == C) {
+  if (CMAX > 8 || ((C & 1) && a.ld == C)) {
     Vec16<DT> raw[V];
     load_vecs<DT, V>(xg, tid * VE, R * VE, all, raw);
 #pragma unroll
@@ -274,35 +292,37 @@ __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
         }
       }
     }
-    const double base = m == -kInf ? 0.0 : (double)m;
-    const float cf = exponent_scale(a.c), mf = (float)base;
+    const float mf = m == -kInf ? 0.0f : m;
 #pragma unroll
     for (int c0 = 0; c0 < CMAX; c0 += kShortStep) {
       if (c0 < C) {
+        float w[kShortStep];
 #pragma unroll
         for (int q = 0; q < kShortStep; ++q) {
-          const int c = c0 + q;
-          if (FROM != kStats) {
-            const double w = exp2_64(((double)v[c] - base) * a.c);
-            o += c == cls ? 0.0 : w;
-            v[c] = (float)w;
-          } else {
-            v[c] = exp2_32((v[c] - mf) * cf);
-          }
+          v[c0 + q] = FROM == kStats ? grad_term(a, v[c0 + q] - mf) : sum_term(a, v[c0 + q] - mf);
+          w[q] = c0 + q == cls ? 0.0f : v[c0 + q];
         }
+        if (FROM != kStats) o += (double)sum_of(w);
       }
     }
-    const RowGrad g = row_out<FROM>(a, i, true, named, in, m, o, xa);
+    RowEnd e = row_end(a.inv_T, named, m, o, xa);
+    if (FROM != kStats && next_to_border(a, e, in)) {
+      o = 0.0;
+      for (int c = 0; c < C; ++c)
+        if (c != cls) o += exp2_64(((double)x[c] - (double)mf) * a.c);
+      e = row_end(a.inv_T, named, m, o, xa);
+    }
+    const RowGrad g = row_out<FROM>(a, i, true, e, in, m, o, xa);
     if (a.grad != nullptr) {
 #pragma unroll
       for (int c = 0; c < CMAX; ++c)
-        if (c < C) x[c] = !g.any ? 0.0f : (c == cls ? g.mine : v[c] * g.scale);
+        if (c < C) x[c] = !g.any() ? 0.0f : (c == cls ? g.mine : v[c] * g.scale);
     }
   }
   if (a.grad != nullptr) {
     __syncthreads();
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i0 * a.ldg;
-    if ((C & 1) && a.ldg == C) {
+    if (CMAX > 8 || ((C & 1) && a.ldg == C)) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int32_t e = (tid + j * R) * VE;
@@ -320,67 +340,123 @@ __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
   }
 }
 
-// NT lanes for a row that their V vectors of 16 bytes each hold whole: one read,
-// and the maximum before the exponentials (in FP64, as above).
-template <int DT, int NT, int V, int FROM>
+// NT lanes for a row that their V vectors of 16 bytes each hold whole, B rows one
+// after the other in registers.  What is FP64 about a row (some 250 instructions where
+// there is a policy) is done for B rows at once: lane b of the NT has row b.
+template <int DT, int NT, int V, int B, int FROM>
 __global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
-  constexpr int VE = Score<DT>::kVec;
+  constexpr int VE = Score<DT>::kVec, R = 64 / NT;
   const Span span = row_span(a);
-  const int lane = threadIdx.x & (NT - 1);
-  const int64_t wave0 = span.lo + a.row0 + (int64_t(blockIdx.x) * 256 + (threadIdx.x & ~63)) / NT;
-  if (wave0 >= span.hi) return;
-  const int64_t i_all = wave0 + (threadIdx.x & 63) / NT;
-  const bool mine = i_all < span.hi;
-  const int64_t i = mine ? i_all : span.hi - 1;
+  const int lane = threadIdx.x & (NT - 1), sub = (threadIdx.x & 63) / NT;
+  const int64_t first = span.lo + a.row0 + (int64_t(blockIdx.x) * 4 + threadIdx.x / 64) * (R * B) + sub;
+  if (first - sub >= span.hi) return;
   const int32_t C = a.C, c0 = lane * VE;
-  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
-  const int32_t cls = row_class(a, i, mine && lane == 0);
+  const Elem* __restrict__ x = static_cast<const Elem*>(a.x);
+  auto row = [&](int b) { return first + b * R < span.hi ? first + b * R : span.hi - 1; };
+  Vec16<DT> raw[B][V];
+  int32_t cls_of[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) cls_of[b] = a.cls[row(b)];
+#pragma unroll
+  for (int b = 0; b < B; ++b) load_vecs<DT, V>(x + row(b) * a.ld, c0, NT * VE, C, raw[b]);
+  const int mine = lane < B ? lane : B - 1;
+  const int64_t i = row(mine);
+  const bool own = lane < B && first + mine * R < span.hi;
+  const int32_t cls = row_class(a, i, own);
   const bool named = cls >= 0;
+  const float xa = named ? Score<DT>::to_f32(x[i * a.ld + cls]) : 0.0f;
   const RowIn in = row_in<FROM>(a, i);
-  Vec16<DT> raw[V];
-  load_vecs<DT, V>(xr, c0, NT * VE, C, raw);
-  const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
-  float m = -kInf;
+  float m_of[B], m = -kInf;
   double o = 0.0;
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    if (FROM == kStats) {
+      m_of[b] = a.stats[2 * row(b)];
+      continue;
+    }
+    float top = -kInf;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      forget<DT>(raw[b][j]);
+      unpack<DT>(raw[b][j], f);
+      set_class<VE>(f, cls_of[b], c0 + j * NT * VE, -kInf);
+      top = __builtin_fmaxf(top, max_of(f));
+      settle(top);  // (vector by vector: fewer registers)
+    }
+    top = lanes_reduce<NT>(top, [](float p, float q) { return __builtin_fmaxf(p, q); });
+    const float base = top == -kInf ? 0.0f : top;
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j > 0 && j * NT * VE >= C) break;
+      float f[VE];
+      forget<DT>(raw[b][j]);
+      unpack<DT>(raw[b][j], f);
+      set_class<VE>(f, cls_of[b], c0 + j * NT * VE, -kInf);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = sum_term(a, f[q] - base);
+      sum += (double)sum_of(f);
+      settle(sum);
+    }
+    sum = lanes_reduce<NT>(sum, [](double p, double q) { return p + q; });
+    m_of[b] = top;
+    if (mine == b) {
+      m = top;
+      o = sum;
+    }
+  }
   if (FROM == kStats) {
     m = a.stats[2 * i];
     o = a.stats[2 * i + 1];
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float f[VE];
-      unpack<DT>(raw[j], f);
-      set_class<VE>(f, cls, c0 + j * NT * VE, -kInf);
-      m = __builtin_fmaxf(m, max_of(f));
-    }
-    m = group_max<NT>(m);
-    const double base = m == -kInf ? 0.0 : (double)m;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (j > 0 && j * NT * VE >= C) break;
-      float f[VE];
-      unpack<DT>(raw[j], f);
-      set_class<VE>(f, cls, c0 + j * NT * VE, -kInf);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) o += exp2_64(((double)f[q] - base) * a.c);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    o = group_sum<NT>(o);
   }
-  const RowGrad g = row_out<FROM>(a, i, mine && lane == 0, named, in, m, o, xa);
-  if (a.grad != nullptr && mine) {
-    Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
-    const float cf = exponent_scale(a.c), mf = m == -kInf ? 0.0f : m;
+  RowEnd e = row_end(a.inv_T, named, m, o, xa);
+  if (FROM != kStats) {
+    const bool near = own && next_to_border(a, e, in);
+    if (__any(near)) {
+#pragma unroll 1
+      for (int b = 0; b < B; ++b) {
+        const Elem* __restrict__ xr = x + row(b) * a.ld;
+        const int32_t skip = a.cls[row(b)];
+        const float top = __shfl(m, (threadIdx.x & 63 & ~(NT - 1)) + b, 64);
+        const double base = top == -kInf ? 0.0 : (double)top;
+        double sum = 0.0;
+#pragma unroll 1
+        for (int32_t k = lane; k < C; k += 4 * NT) {
+          float f[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) f[q] = k + q * NT < C ? Score<DT>::to_f32(xr[k + q * NT]) : -kInf;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sum += k + q * NT == skip ? 0.0 : exp2_64(((double)f[q] - base) * a.c);
+        }
+        sum = lanes_reduce<NT>(sum, [](double p, double q) { return p + q; });
+        if (near && mine == b) o = sum;
+      }
+      e = row_end(a.inv_T, named, m, o, xa);
+    }
+  }
+  const RowGrad all = row_out<FROM>(a, i, own, e, in, m, o, xa);
+  if (a.grad == nullptr) return;
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int from = (threadIdx.x & 63 & ~(NT - 1)) + b;
+    const RowGrad g = {__shfl(all.mine, from, 64), __shfl(all.scale, from, 64)};
+    if (first + b * R >= span.hi) continue;
+    Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + (first + b * R) * a.ldg;
+    const float base = m_of[b] == -kInf ? 0.0f : m_of[b];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (j > 0 && j * NT * VE >= C) break;
       float f[VE];
-      unpack<DT>(raw[j], f);
+      forget<DT>(raw[b][j]);
+      unpack<DT>(raw[b][j], f);
 #pragma unroll
-      for (int q = 0; q < VE; ++q) f[q] = g.any ? exp2_32((f[q] - mf) * cf) * g.scale : 0.0f;
-      if (g.any) set_class<VE>(f, cls, c0 + j * NT * VE, g.mine);
+      for (int q = 0; q < VE; ++q) f[q] = g.any() ? grad_term(a, f[q] - base) * g.scale : 0.0f;
+      set_class<VE>(f, cls_of[b], c0 + j * NT * VE, g.mine);
       store_tail<DT>(gr, c0 + j * NT * VE, C, pack<DT>(f));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -392,6 +468,135 @@ __device__ __forceinline__ void join_lanes(double c, float& m, double& o) {
   if (m != top && m != -kInf) o *= exp2_64(((double)m - (double)top) * c);
   m = top;
   o = wave_sum(o);
+}
+
+// The sum over a row's other classes in FP64, by a workgroup (which all of it calls).
+template <int DT, int NT>
+__device__ __forceinline__ double exact_sum(const typename Score<DT>::Elem* __restrict__ xr, int32_t C, int32_t cls,
+                                            float m, double c, double* sh) {
+  constexpr int VE = Score<DT>::kVec;
+  const double base = m == -kInf ? 0.0 : (double)m;
+  double o = 0.0;
+#pragma unroll 1
+  for (int32_t c0 = threadIdx.x * VE; c0 < C; c0 += NT * VE) {
+    float f[VE];
+    load_chunk<DT>(xr, c0, C, f);
+    set_class<VE>(f, cls, c0, -kInf);
+#pragma unroll
+    for (int q = 0; q < VE; ++q) o += exp2_64(((double)f[q] - base) * c);
+  }
+  return block_sum<NT>(o, sh);
+}
+
+// The end of a workgroup's row, in all its threads: the first wave does what is FP64
+// about it.  A row next to a border has its sum taken again; what the caller has of it
+// in registers need not be kept for that, it has it read again.
+struct RowShared {
+  float mine, scale;
+  int again;
+};
+template <int DT, int NT, int FROM, typename Reload>
+__device__ __forceinline__ RowGrad finish_row(const LogpArgs& a, int64_t i, bool write,
+                                              const typename Score<DT>::Elem* __restrict__ xr, int32_t cls, float m,
+                                              double o, double* sh, RowShared& out, Reload reload) {
+  const bool first = threadIdx.x < 64, writes = write && threadIdx.x == 0;
+  if (first) {
+    const RowIn in = row_in<FROM>(a, i);
+    const float xa = cls >= 0 ? Score<DT>::to_f32(xr[cls]) : 0.0f;
+    const RowEnd e = row_end(a.inv_T, cls >= 0, m, o, xa);
+    const RowGrad g = row_out<FROM>(a, i, writes, e, in, m, o, xa);
+    if (threadIdx.x == 0) out = RowShared{g.mine, g.scale, FROM != kStats && next_to_border(a, e, in)};
+  }
+  if (a.grad == nullptr && a.adv == nullptr) return RowGrad{0.0f, 0.0f};  // (nothing follows)
+  __syncthreads();
+  if (FROM != kStats && out.again) {
+    o = exact_sum<DT, NT>(xr, a.C, cls, m, a.c, sh);
+    if (first) {
+      const RowIn in = row_in<FROM>(a, i);
+      const float xa = Score<DT>::to_f32(xr[cls]);
+      const RowGrad g = row_out<FROM>(a, i, writes, row_end(a.inv_T, true, m, o, xa), in, m, o, xa);
+      if (threadIdx.x == 0) out = RowShared{g.mine, g.scale, 0};
+    }
+    __syncthreads();
+    reload();
+  }
+  return RowGrad{out.mine, out.scale};
+}
+
+// A workgroup of NT threads for a row that their V vectors each hold whole: one read
+// where the gradient follows.  The first wave does what is FP64 about the row.
+template <int DT, int NT, int V>
+__global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
+  using Elem = typename Score<DT>::Elem;
+  constexpr int VE = Score<DT>::kVec, W = NT / 64;
+  __shared__ float sh_m[W];
+  __shared__ double sh_o[W];
+  __shared__ RowShared sh_end;
+  const Span span = row_span(a);
+  const int tid = threadIdx.x;
+  const int64_t i = span.lo + a.row0 + blockIdx.x;
+  if (i >= span.hi) return;
+  const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
+  const int32_t C = a.C, c0 = tid * VE;
+  const int32_t cls = row_class(a, i, tid == 0);
+  const bool named = cls >= 0;
+  Vec16<DT> raw[V];
+  float m = -kInf;
+  double o = 0.0;
+  if (named) {
+    load_vecs<DT, V>(xr, c0, NT * VE, C, raw);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      forget<DT>(raw[j]);
+      unpack<DT>(raw[j], f);
+      set_class<VE>(f, cls, c0 + j * NT * VE, -kInf);
+      m = __builtin_fmaxf(m, max_of(f));
+      settle(m);  // (vector by vector: fewer registers)
+    }
+    const float base = m == -kInf ? 0.0f : m;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j > 0 && j * NT * VE >= C) break;
+      float f[VE];
+      forget<DT>(raw[j]);
+      unpack<DT>(raw[j], f);
+      set_class<VE>(f, cls, c0 + j * NT * VE, -kInf);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = sum_term(a, f[q] - base);
+      o += (double)sum_of(f);
+      settle(o);
+    }
+    join_lanes(a.c, m, o);
+    if ((tid & 63) == 0) {
+      sh_m[tid >> 6] = m;
+      sh_o[tid >> 6] = o;
+    }
+  }
+  __syncthreads();
+  if (named) {
+    m = sh_m[tid & (W - 1)];
+    o = (tid & 63) < W ? sh_o[tid & (W - 1)] : 0.0;
+    join_lanes(a.c, m, o);
+  }
+  const RowGrad g = finish_row<DT, NT, kSums>(a, i, true, xr, cls, m, o, sh_o, sh_end,
+                                                  [&] { load_vecs<DT, V>(xr, c0, NT * VE, C, raw); });
+  const float base = m == -kInf ? 0.0f : m;
+  Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (j > 0 && j * NT * VE >= C) break;
+    float f[VE] = {};
+    if (g.any()) {
+      forget<DT>(raw[j]);
+      unpack<DT>(raw[j], f);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = grad_term(a, f[q] - base) * g.scale;
+      set_class<VE>(f, cls, c0 + j * NT * VE, g.mine);
+    }
+    store_stream<DT>(gr, c0 + j * NT * VE, C, pack<DT>(f));
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // One workgroup per row, or per part of one: part_len classes (a multiple of
@@ -406,10 +611,10 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   constexpr int VE = Score<DT>::kVec, BLK = kBlk<DT>, W = NT / 64;
   __shared__ float sh_m[W];
   __shared__ double sh_o[W];
+  __shared__ RowShared sh_end;
   __shared__ int sh_last;
   const Span span = row_span(a);
   const int tid = threadIdx.x;
-  const float cf = exponent_scale(a.c);
   const uint32_t in_launch = a.n_parts > 1 ? blockIdx.x / (uint32_t)a.n_parts : blockIdx.x;
   const int32_t part = (int32_t)(blockIdx.x - in_launch * (uint32_t)a.n_parts);
   const int64_t row = a.row0 + in_launch, i = a.reverse ? span.hi - 1 - row : span.lo + row;
@@ -429,18 +634,19 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
     for (int32_t base = lo;;) {
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
+        if (j > 0 && base + j * NT * VE >= hi) break;
         float f[VE];
         unpack<DT>(raw.v[j], f);
         set_class<VE>(f, cls, base + c0 + j * NT * VE, -kInf);
         const float vm = max_of(f);
         m = __builtin_fmaxf(m, vm);
-        if ((vm - ref) * cf > 20.0f) {  // (the first finite score among them)
+        if ((vm - ref) * a.c_hi > 20.0f) {  // (the first finite score among them)
           o *= exp2_64(((double)ref - (double)vm) * a.c);
           ref = vm;
         }
         const float rf = ref == -kInf ? 0.0f : ref;
 #pragma unroll
-        for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - rf) * cf);
+        for (int q = 0; q < VE; ++q) f[q] = sum_term(a, f[q] - rf);
         o += (double)sum_of(f);
         __builtin_amdgcn_sched_barrier(0);  // (vector by vector: fewer registers)
       }
@@ -487,24 +693,22 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
     m = a.stats[2 * i];
     o = a.stats[2 * i + 1];
   }
-  const RowIn in = row_in<FROM>(a, i);
-  const float xa = named ? Score<DT>::to_f32(xr[cls]) : 0.0f;
-  if (a.grad == nullptr && tid >= 64) return;  // (what is left is one thread's)
-  const bool write = tid == 0 && (FROM == kParts || part == 0);
-  const RowGrad g = row_out<FROM>(a, i, write, named, in, m, o, xa);
+  const RowGrad g =
+      finish_row<DT, NT, FROM>(a, i, FROM == kParts || part == 0, xr, cls, m, o, sh_o, sh_end, [] {});
   if (FROM != kParts && a.grad != nullptr) {
     const float mf = m == -kInf ? 0.0f : m;
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
     for (int32_t base = lo; base < hi; base += NT * BLK) {
       RawBlock<DT> out = {};
-      if (g.any) {
+      if (g.any()) {
         const RawBlock<DT> raw = load_block<DT, NT>(xr, base, hi);
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
+          if (j > 0 && base + j * NT * VE >= hi) break;
           float f[VE];
           unpack<DT>(raw.v[j], f);
 #pragma unroll
-          for (int q = 0; q < VE; ++q) f[q] = exp2_32((f[q] - mf) * cf) * g.scale;
+          for (int q = 0; q < VE; ++q) f[q] = grad_term(a, f[q] - mf) * g.scale;
           set_class<VE>(f, cls, base + tid * VE + j * NT * VE, g.mine);
           out.v[j] = pack<DT>(f);
           __builtin_amdgcn_sched_barrier(0);
@@ -624,14 +828,25 @@ void launch_short(const LogpArgs& a, hipStream_t s) {
   diag_end(s);
 }
 
-template <int DT, int NT, int V, int FROM>
+template <int DT, int NT, int V, int B, int FROM>
 void launch_wave(LogpArgs a, hipStream_t s) {
-  constexpr int64_t kRows = 256 / NT;
+  constexpr int64_t kRows = 256 / NT * B;
   for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid * kRows) {
     const int64_t left = (a.n - a.row0 + kRows - 1) / kRows;
     diag_begin(kDiagClassLogp, s);
-    hipLaunchKernelGGL((k_logp_wave<DT, NT, V, FROM>), dim3((unsigned)(left < kMaxRowGrid ? left : kMaxRowGrid)),
+    hipLaunchKernelGGL((k_logp_wave<DT, NT, V, B, FROM>), dim3((unsigned)(left < kMaxRowGrid ? left : kMaxRowGrid)),
                        dim3(256), 0, s, a);
+    diag_end(s);
+  }
+}
+
+template <int DT, int NT, int V>
+void launch_wide(LogpArgs a, hipStream_t s) {
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
+    const int64_t left = a.n - a.row0;
+    diag_begin(kDiagClassLogp, s);
+    hipLaunchKernelGGL((k_logp_wide<DT, NT, V>), dim3((unsigned)(left < kMaxRowGrid ? left : kMaxRowGrid)), dim3(NT), 0,
+                       s, a);
     diag_end(s);
   }
 }
@@ -648,9 +863,17 @@ void launch_block(LogpArgs a, hipStream_t s) {
   }
 }
 
-// Threads for a row as the distillation has them: one up to 32 classes, up to a
-// wave while its registers hold the row, then a workgroup, 1,024 threads where
-// rows are long enough to be read twice from memory; few long rows are split.
+// Threads for a row.  Up to 8 classes one, and up to 32 where rows are packed and of
+// odd length, whose LDS rows need no padding (600,000 steps of 31 f32: 30 us, 36 with
+// lanes; of 16, with padding: 28, and 22 with lanes).  Then as many lanes as hold the
+// row in at most 8 vectors each, up to a wave (33,554 steps of 2,000 bf16: 50 us, 80
+// when the row was read twice).  A step of a longer row keeps it in a workgroup's
+// registers while they take it: 512 threads rather than 1,024 up to 4,096 vectors, so
+// that four rows a CU are at different stages (3,355 x 20,000 bf16: 49 us, 65 with
+// 1,024).  Longer rows are read twice, 1,024 threads each, so that the second read
+// finds more of them in the last-level cache.  Where no gradient follows, 256
+// threads: more rows side by side (4,096 x 65,537 bf16: 97 us, 130 with 1,024).  Few
+// long rows are split.
 template <int DT, int FROM>
 int launch_logp(LogpArgs a, hipStream_t s) {
   constexpr int VE = Score<DT>::kVec;
@@ -658,26 +881,30 @@ int launch_logp(LogpArgs a, hipStream_t s) {
   a.n_parts = 1;
   a.part_len = 0;
   const int32_t vecs = (a.C + VE - 1) / VE, steps = (a.C + kPartStep - 1) / kPartStep;
+  const bool step = FROM == kSums && a.grad != nullptr;
+  const bool packed = (a.C & 1) && a.ld == a.C && (a.grad == nullptr || a.ldg == a.C);
   if (a.C <= 8) {
     launch_short<DT, 64, 8, FROM>(a, s);
-  } else if (a.C <= 16) {
+  } else if (packed && a.C <= 16) {
     launch_short<DT, 128, 16, FROM>(a, s);
-  } else if (a.C <= kRowsMaxClasses) {
+  } else if (packed && a.C <= kRowsMaxClasses) {
     launch_short<DT, 64, 32, FROM>(a, s);
+  } else if (vecs <= 4) {
+    launch_wave<DT, 4, 1, 4, FROM>(a, s);
   } else if (vecs <= 8) {
-    launch_wave<DT, 8, 1, FROM>(a, s);
+    launch_wave<DT, 8, 1, 8, FROM>(a, s);
   } else if (vecs <= 16) {
-    launch_wave<DT, 8, 2, FROM>(a, s);
+    launch_wave<DT, 8, 2, 4, FROM>(a, s);
   } else if (vecs <= 32) {
-    launch_wave<DT, 8, 4, FROM>(a, s);
+    launch_wave<DT, 8, 4, 2, FROM>(a, s);
   } else if (vecs <= 64) {
-    launch_wave<DT, 16, 4, FROM>(a, s);
+    launch_wave<DT, 16, 4, 2, FROM>(a, s);
   } else if (vecs <= 128) {
-    launch_wave<DT, 32, 4, FROM>(a, s);
+    launch_wave<DT, 32, 4, 1, FROM>(a, s);
   } else if (vecs <= 256) {
-    launch_wave<DT, 64, 4, FROM>(a, s);
-  } else if (DT == GBDT_DTYPE_F32 && vecs <= 512) {
-    launch_wave<DT, 64, 8, FROM>(a, s);
+    launch_wave<DT, 64, 4, 1, FROM>(a, s);
+  } else if (vecs <= 512) {
+    launch_wave<DT, 64, 8, 1, FROM>(a, s);
   } else if (a.n <= kSplitRows && steps >= 4) {
     const int32_t want = (int32_t)(kSplitGrid / a.n);
     const int32_t per = (steps + want - 1) / want;
@@ -689,6 +916,14 @@ int launch_logp(LogpArgs a, hipStream_t s) {
     } else {
       launch_block<DT, 256, FROM>(a, s);
     }
+  } else if (step && vecs <= 1024) {
+    launch_wide<DT, 256, 4>(a, s);
+  } else if (step && vecs <= 2048) {
+    launch_wide<DT, 256, 8>(a, s);
+  } else if (step && vecs <= 4096) {
+    launch_wide<DT, 512, 8>(a, s);
+  } else if (step && vecs <= 8192) {
+    launch_wide<DT, 1024, 8>(a, s);
   } else if (a.C <= 40000 || a.grad == nullptr) {
     launch_block<DT, 256, FROM>(a, s);
   } else {
@@ -723,6 +958,9 @@ LogpArgs logp_args(const gbdt_scores& x, const int32_t* classes, double temperat
   a.cls = classes;
   a.c = kLog2e / temperature;
   a.inv_T = 1.0 / temperature;
+  a.c_hi = (float)a.c;
+  if ((double)a.c_hi >= a.c) a.c_hi = std::nextafterf(a.c_hi, 0.0f);
+  a.c_lo = (float)(a.c - (double)a.c_hi);
   a.err = &static_cast<WsCtrl*>(ws)->err;
   a.parts = reinterpret_cast<PartSum*>(static_cast<char*>(ws) + sizeof(WsCtrl));
   a.tickets = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + sizeof(WsCtrl) + kScoresPartBytes);
@@ -757,6 +995,8 @@ int policy(const gbdt_scores* x, const int32_t* classes, double temperature, con
   a.weight = p->weight;
   a.low = 1.0 - p->clip_low;
   a.high = 1.0 + p->clip_high;
+  a.log_low = std::log(a.low);
+  a.log_high = std::log(a.high);
   a.kl = p->kl;
   a.loss = loss;
   a.logp = logp;
@@ -781,13 +1021,15 @@ int check_pairs(const gbdt_pairs* p) {
   return GBDT_OK;
 }
 
-// 1,024 threads where a pair has more rows than that in the mean: each of a thread's
-// rows costs two latencies.
+// Threads for a pair by its rows in the mean: each of a thread's rows costs latencies,
+// each wave of a pair the pair's own arithmetic.
 template <int DT>
 void launch_pairs_of(const PairArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.n_pairs);
   if (a.n / a.n_pairs > 512) {
     hipLaunchKernelGGL((k_pairs<DT, 1024>), grid, dim3(1024), 0, s, a);
+  } else if (a.n / a.n_pairs <= 128) {
+    hipLaunchKernelGGL((k_pairs<DT, 64>), grid, dim3(64), 0, s, a);
   } else {
     hipLaunchKernelGGL((k_pairs<DT, 256>), grid, dim3(256), 0, s, a);
   }

@@ -63,10 +63,6 @@ struct RouteKey<false> {
   static __device__ __forceinline__ T take(T v, bool it) { return it ? -kInf : v; }
   static __device__ __forceinline__ T larger(T a, T b) { return __builtin_fmaxf(a, b); }
   static __device__ __forceinline__ T smaller(T a, T b) { return __builtin_fminf(a, b); }
-  template <int CTRL>
-  static __device__ __forceinline__ T moved(T v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
-  }
 };
 template <>
 struct RouteKey<true> {
@@ -85,25 +81,7 @@ struct RouteKey<true> {
     asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
   }
-  template <int CTRL>
-  static __device__ __forceinline__ T moved(T v) {
-    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true);
-    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
-    return __hiloint2double(hi, lo);
-  }
 };
-
-// The largest key of NT neighbouring lanes, in all of them.
-template <typename K, int NT>
-__device__ __forceinline__ typename K::T lanes_max(typename K::T v) {
-  if constexpr (NT >= 2) v = K::larger(v, K::template moved<0xB1>(v));   // quad_perm 1, 0, 3, 2
-  if constexpr (NT >= 4) v = K::larger(v, K::template moved<0x4E>(v));   // quad_perm 2, 3, 0, 1
-  if constexpr (NT >= 8) v = K::larger(v, K::template moved<0x141>(v));  // row_half_mirror
-  if constexpr (NT >= 16) v = K::larger(v, K::template moved<0x140>(v)); // row_mirror
-  if constexpr (NT >= 32) v = K::larger(v, __shfl_xor(v, 16, 64));
-  if constexpr (NT >= 64) v = K::larger(v, __shfl_xor(v, 32, 64));
-  return v;
-}
 
 __device__ __forceinline__ double sigmoid_64(float x) {
   const double e = exp2_64(-(double)__builtin_fabsf(x) * kLog2e);
@@ -242,7 +220,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
 #pragma unroll
       for (int e = 0; e < w; ++e) part[e] = K::larger(part[e], part[e + w]);
     }
-    const Key top = lanes_max<K, NT>(part[0]);
+    const Key top = lanes_reduce<NT>(part[0], [](Key p, Key q) { return K::larger(p, q); });
     const bool left = top > K::taken(), has = part[0] == top && left;
     bool open = has && (__ballot(has) & below) == 0;  // this lane's, and not yet found
     const bool wins = open;

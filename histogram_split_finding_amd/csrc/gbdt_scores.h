@@ -58,6 +58,20 @@ __device__ __forceinline__ Vec16<DT> load_vec(const typename Score<DT>::Elem* p)
   return v;
 }
 
+// The same vector, but nothing that was worked out from it before is kept for later
+// (in FP32 it takes up to twice its registers).
+template <int DT>
+__device__ __forceinline__ void forget(Vec16<DT>& v) {
+  asm("" : "+v"(v.w[0]), "+v"(v.w[1]), "+v"(v.w[2]), "+v"(v.w[3]));
+}
+
+// A value that is worked out here, and not where it is used: what it comes from need
+// not be kept until then.
+template <typename T>
+__device__ __forceinline__ void settle(T& v) {
+  asm volatile("" : "+v"(v));
+}
+
 template <int DT>
 __device__ __forceinline__ void unpack(const Vec16<DT>& v, float (&f)[Score<DT>::kVec]) {
 #pragma unroll
@@ -268,6 +282,29 @@ __device__ __forceinline__ double group_sum(double v) {
   return v;
 }
 
+// A value from another lane of the row of 16, by lane moves (no LDS round trip).
+template <int CTRL>
+__device__ __forceinline__ float dpp_moved(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_moved(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
+  return __hiloint2double(hi, lo);
+}
+// NT neighbouring lanes' values combined by a commutative f, the same in all of them.
+template <int NT, typename T, typename F>
+__device__ __forceinline__ T lanes_reduce(T v, F f) {
+  if constexpr (NT >= 2) v = f(v, dpp_moved<0xB1>(v));   // quad_perm 1, 0, 3, 2
+  if constexpr (NT >= 4) v = f(v, dpp_moved<0x4E>(v));   // quad_perm 2, 3, 0, 1
+  if constexpr (NT >= 8) v = f(v, dpp_moved<0x141>(v));  // row_half_mirror
+  if constexpr (NT >= 16) v = f(v, dpp_moved<0x140>(v)); // row_mirror
+  if constexpr (NT >= 32) v = f(v, __shfl_xor(v, 16, 64));
+  if constexpr (NT >= 64) v = f(v, __shfl_xor(v, 32, 64));
+  return v;
+}
+
 // The waves' values sh[W] combined, in every lane (behind a barrier).
 template <int W, typename T, typename F>
 __device__ __forceinline__ T across_waves(const T* sh, F f) {
@@ -361,6 +398,19 @@ __device__ __forceinline__ void store_block(typename Score<DT>::Elem* __restrict
   } else {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) store_tail<DT>(row, c0 + j * NT * VE, C, r.v[j]);
+  }
+}
+
+// One vector of such a store, where a row's vectors may be behind its end.
+template <int DT>
+__device__ __forceinline__ void store_stream(typename Score<DT>::Elem* __restrict__ row, int32_t c, int32_t C,
+                                             Vec16<DT> v) {
+  using Words = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
+  if (c + Score<DT>::kVec <= C) {
+    const Words o = {v.w[0], v.w[1], v.w[2], v.w[3]};
+    __builtin_nontemporal_store(o, reinterpret_cast<Words*>(row + c));
+  } else {
+    store_tail<DT>(row, c, C, v);
   }
 }
 

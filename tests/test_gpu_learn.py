@@ -1,9 +1,7 @@
 """Log-probabilities, policy and preference losses and their gradients on the GPU
 against the FP64 reference in learn_ref.py.
 
-Tolerances.  Rows of up to 2,048 classes have FP64 exponentials; what is left is
-the result's rounding, 2^-24 relative (`fine`: with 2^-40 for the FP64 functions).
-In longer rows a score's FP32 exponential exp2((x - m) c): the difference, c and
+Tolerances.  A score's FP32 exponential exp2((x - m) c): the difference, c and
 the product are each off by half a step (2^-24 relative), which moves the exponent
 by 3 2^-24 D with D = |x - m| / T, and the exponential itself by a step (2^-23): a sum
 of them, with D at most 40 where it matters, is off by e = (3 D + 6) 2^-24 with the
@@ -11,7 +9,8 @@ sums' own roundings.  The logarithm of the odds is then off by e, logp by
 (1 - p_a) e, the gradient at the class by e relative (and one more half step each
 for o as FP32 statistics, the product and the result); elsewhere its own FP32
 exponential adds (3 D_c + 2) 2^-24.  A slope's error follows logp's: |r A| + kl e^y
-times it.  Results below FP32's normal numbers, 2^-126 times the slope, may be 0.
+times it; which side of the clip a ratio is on is decided in FP64.  Results below
+FP32's normal numbers, 2^-126 times the slope, may be 0.
 """
 import numpy as np
 import pytest
@@ -43,7 +42,7 @@ def spread(x, T):
     """e, and D_c of each class against the largest other."""
     fin = x[np.isfinite(x)]
     D = min(40.0, (fin.max() - fin.min()) / T) if len(fin) else 0.0
-    e = 2.0 ** -40 if len(x) <= 2048 else (3 * D + 6) * STEP
+    e = (3 * D + 6) * STEP
     with np.errstate(all="ignore"):
         Dc = np.where(np.isfinite(x), np.abs(x - (fin.max() if len(fin) else 0.0)) / T, 0.0)
     return e, Dc
@@ -415,6 +414,33 @@ def test_clip_borders():
     assert np.allclose(loss.cpu().numpy(), [-1.0, 1.0, -np.exp(-1e-6), -1.0, 1.0, np.exp(1e-6), -2.0, 0.0],
                        rtol=2.0 ** -23, atol=0.0)
     assert bool((stats[:, 0] == float("-inf")).all()) and bool((stats[:, 1] == 0).all())
+
+
+@pytest.mark.parametrize("C,n", [(2, 64), (7, 300), (20, 64), (40, 200), (60, 64), (100, 64), (200, 40), (700, 64),
+                                 (1500, 20), (3000, 20), (6000, 20), (9001, 130), (20011, 20), (70001, 20), (70001, 140)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_ratios_next_to_the_borders(C, n, dtype):
+    """Ratios within a few parts in ten million of 0.8 and 1.28, on both sides, as old
+    log-probabilities in FP32 come to lie: FP32 exponentials could not tell the side."""
+    say("learn, next to the borders: %d x %d %s" % (n, C, dtype))
+    T = 1.3
+    x, xh = ref.rows(n, C, dtype, C + n, pad=C % 3)
+    cls = draw_classes(xh, C, 0.0)
+    r = np.random.default_rng(C)
+    lp = np.array([lref.row(xh[i], int(cls[i]), T)[1] for i in range(n)])
+    border = np.where(r.random(n) < 0.5, 0.8, 1.28)
+    old = (lp - np.log(border)).astype(np.float32)
+    for _ in range(2):
+        old = np.where(r.random(n) < 0.3, np.nextafter(old, np.float32(r.choice([-99, 99]))), old)
+    A = np.where(border < 1, -1.0, 1.0).astype(np.float32) * r.uniform(0.5, 2.0, n).astype(np.float32)
+    ratio = np.exp(lp - old.astype(np.float64))
+    # (the FP64 functions of either side are off by a few 2^-52; old is a rounding and at most
+    # two steps, of 2^-23 |old| each, away)
+    off = np.abs(ratio / border - 1)
+    assert np.all(off > 1e-13) and np.all(off <= 3 * 2.0 ** -23 * np.abs(old) + 1e-9)
+    kept = np.where(border < 1, ratio >= border, ratio <= border)
+    assert 0 < kept.sum() < n
+    check_policy(x, xh, cls, T, dtype, with_ref=False, rows=(old, None, A, np.ones(n, dtype=np.float32)))
 
 
 @pytest.mark.parametrize("C", [5, 300, 3001])
