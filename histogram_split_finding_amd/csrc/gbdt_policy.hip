@@ -461,13 +461,29 @@ __global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
   }
 }
 
-// The sums of a wave's lanes, each o against its own m, as one against the largest m.
+// The sums of N neighbouring lanes, each o against its own m, as one against the
+// largest m.
+template <int N>
 __device__ __forceinline__ void join_lanes(double c, float& m, double& o) {
-  const float top = wave_max(m);
+  const float top = lanes_reduce<N>(m, [](float p, float q) { return __builtin_fmaxf(p, q); });
   // (o of 0 or NaN stays what it is; a maximum of -inf has o = 0 or NaN)
   if (m != top && m != -kInf) o *= exp2_64(((double)m - (double)top) * c);
   m = top;
-  o = wave_sum(o);
+  o = lanes_reduce<N>(o, [](double p, double q) { return p + q; });
+}
+// The same of a workgroup's W waves; sh_m, sh_o: [W].
+template <int W>
+__device__ __forceinline__ void join_waves(double c, float& m, double& o, float* sh_m, double* sh_o) {
+  const int tid = threadIdx.x;
+  join_lanes<64>(c, m, o);
+  if ((tid & 63) == 0) {
+    sh_m[tid >> 6] = m;
+    sh_o[tid >> 6] = o;
+  }
+  __syncthreads();
+  m = sh_m[tid & (W - 1)];
+  o = sh_o[tid & (W - 1)];
+  join_lanes<W>(c, m, o);
 }
 
 // The sum over a row's other classes in FP64, by a workgroup (which all of it calls).
@@ -495,7 +511,7 @@ struct RowShared {
   float mine, scale;
   int again;
 };
-template <int DT, int NT, int FROM, typename Reload>
+template <int DT, int NT, int FROM, bool GRAD, typename Reload>
 __device__ __forceinline__ RowGrad finish_row(const LogpArgs& a, int64_t i, bool write,
                                               const typename Score<DT>::Elem* __restrict__ xr, int32_t cls, float m,
                                               double o, double* sh, RowShared& out, Reload reload) {
@@ -507,7 +523,7 @@ __device__ __forceinline__ RowGrad finish_row(const LogpArgs& a, int64_t i, bool
     const RowGrad g = row_out<FROM>(a, i, writes, e, in, m, o, xa);
     if (threadIdx.x == 0) out = RowShared{g.mine, g.scale, FROM != kStats && next_to_border(a, e, in)};
   }
-  if (a.grad == nullptr && a.adv == nullptr) return RowGrad{0.0f, 0.0f};  // (nothing follows)
+  if (!GRAD && a.adv == nullptr) return RowGrad{0.0f, 0.0f};  // (nothing follows)
   __syncthreads();
   if (FROM != kStats && out.again) {
     o = exact_sum<DT, NT>(xr, a.C, cls, m, a.c, sh);
@@ -567,19 +583,9 @@ __global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
       o += (double)sum_of(f);
       settle(o);
     }
-    join_lanes(a.c, m, o);
-    if ((tid & 63) == 0) {
-      sh_m[tid >> 6] = m;
-      sh_o[tid >> 6] = o;
-    }
+    join_waves<W>(a.c, m, o, sh_m, sh_o);
   }
-  __syncthreads();
-  if (named) {
-    m = sh_m[tid & (W - 1)];
-    o = (tid & 63) < W ? sh_o[tid & (W - 1)] : 0.0;
-    join_lanes(a.c, m, o);
-  }
-  const RowGrad g = finish_row<DT, NT, kSums>(a, i, true, xr, cls, m, o, sh_o, sh_end,
+  const RowGrad g = finish_row<DT, NT, kSums, true>(a, i, true, xr, cls, m, o, sh_o, sh_end,
                                                   [&] { load_vecs<DT, V>(xr, c0, NT * VE, C, raw); });
   const float base = m == -kInf ? 0.0f : m;
   Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
@@ -605,7 +611,7 @@ __global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
 // score is above it by 2^20 in the exponential; a second read writes the gradient.
 // Parts leave their sums behind; where no gradient follows, the last workgroup of
 // a row to arrive adds them up, else a second launch does.
-template <int DT, int NT, int FROM>
+template <int DT, int NT, int FROM, bool GRAD>
 __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
   constexpr int VE = Score<DT>::kVec, BLK = kBlk<DT>, W = NT / 64;
@@ -655,15 +661,7 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
       raw = load_block<DT, NT>(xr, base, hi);
     }
     if (ref != m && m != -kInf) o *= exp2_64(((double)ref - (double)m) * a.c);
-    join_lanes(a.c, m, o);
-    if ((tid & 63) == 0) {
-      sh_m[tid >> 6] = m;
-      sh_o[tid >> 6] = o;
-    }
-    __syncthreads();
-    m = sh_m[tid & (W - 1)];
-    o = (tid & 63) < W ? sh_o[tid & (W - 1)] : 0.0;
-    join_lanes(a.c, m, o);
+    join_waves<W>(a.c, m, o, sh_m, sh_o);
   }
   PartSum* __restrict__ parts = a.parts + row * a.n_parts;
   if constexpr (FROM == kParts) {
@@ -671,7 +669,7 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
       __hip_atomic_store(&parts[part].o, o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(&parts[part].m, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (a.grad != nullptr) return;
+    if constexpr (GRAD) return;
     if (tid == 0) {
       const uint32_t before = __hip_atomic_fetch_add(&a.tickets[row], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
       sh_last = before == (uint32_t)a.n_parts - 1u;
@@ -688,14 +686,14 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
       o = __hip_atomic_load(&parts[lane].o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       m = __hip_atomic_load(&parts[lane].m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    join_lanes(a.c, m, o);
+    join_lanes<64>(a.c, m, o);
   } else if constexpr (FROM == kStats) {
     m = a.stats[2 * i];
     o = a.stats[2 * i + 1];
   }
   const RowGrad g =
-      finish_row<DT, NT, FROM>(a, i, FROM == kParts || part == 0, xr, cls, m, o, sh_o, sh_end, [] {});
-  if (FROM != kParts && a.grad != nullptr) {
+      finish_row<DT, NT, FROM, GRAD>(a, i, FROM == kParts || part == 0, xr, cls, m, o, sh_o, sh_end, [] {});
+  if constexpr (GRAD && FROM != kParts) {
     const float mf = m == -kInf ? 0.0f : m;
     Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
     for (int32_t base = lo; base < hi; base += NT * BLK) {
@@ -851,14 +849,14 @@ void launch_wide(LogpArgs a, hipStream_t s) {
   }
 }
 
-template <int DT, int NT, int FROM>
+template <int DT, int NT, int FROM, bool GRAD>
 void launch_block(LogpArgs a, hipStream_t s) {
   constexpr int32_t kStep = NT * kBlk<DT>;
   if (a.n_parts == 1) a.part_len = (a.C + kStep - 1) / kStep * kStep;
   for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid) {
     const int64_t n = a.n - a.row0 < kMaxRowGrid ? a.n - a.row0 : kMaxRowGrid;
     diag_begin(kDiagClassLogp, s);
-    hipLaunchKernelGGL((k_logp_block<DT, NT, FROM>), dim3((unsigned)(n * a.n_parts)), dim3(NT), 0, s, a);
+    hipLaunchKernelGGL((k_logp_block<DT, NT, FROM, GRAD>), dim3((unsigned)(n * a.n_parts)), dim3(NT), 0, s, a);
     diag_end(s);
   }
 }
@@ -910,11 +908,13 @@ int launch_logp(LogpArgs a, hipStream_t s) {
     const int32_t per = (steps + want - 1) / want;
     a.part_len = per * kPartStep;
     a.n_parts = (steps + per - 1) / per;
-    if constexpr (FROM == kSums) {
-      launch_block<DT, 256, kParts>(a, s);
-      if (a.grad != nullptr) launch_block<DT, 256, kJoin>(a, s);
+    if constexpr (FROM == kStats) {
+      launch_block<DT, 256, kStats, true>(a, s);
+    } else if (step) {
+      launch_block<DT, 256, kParts, true>(a, s);
+      launch_block<DT, 256, kJoin, true>(a, s);
     } else {
-      launch_block<DT, 256, FROM>(a, s);
+      launch_block<DT, 256, kParts, false>(a, s);
     }
   } else if (step && vecs <= 1024) {
     launch_wide<DT, 256, 4>(a, s);
@@ -924,10 +924,12 @@ int launch_logp(LogpArgs a, hipStream_t s) {
     launch_wide<DT, 512, 8>(a, s);
   } else if (step && vecs <= 8192) {
     launch_wide<DT, 1024, 8>(a, s);
-  } else if (a.C <= 40000 || a.grad == nullptr) {
-    launch_block<DT, 256, FROM>(a, s);
+  } else if (FROM == kSums && !step) {
+    launch_block<DT, 256, kSums, false>(a, s);
+  } else if (FROM == kStats && a.C <= 40000) {
+    launch_block<DT, 256, kStats, true>(a, s);
   } else {
-    launch_block<DT, 1024, FROM>(a, s);
+    launch_block<DT, 1024, FROM, true>(a, s);
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? GBDT_OK : hip_fail(e, "k_logp");

@@ -293,6 +293,34 @@ __device__ __forceinline__ double dpp_moved(double v) {
   const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
   return __hiloint2double(hi, lo);
 }
+// f of the value and the one of the other row of 16 lanes (N 16), or of the other half
+// of the wave (N 32): the swap of a register with its own copy leaves one row's value
+// in both rows of the first, and the other's in both of the second.
+template <int N>
+__device__ __forceinline__ void swapped(uint32_t v, uint32_t& a, uint32_t& b) {
+  if constexpr (N == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+  }
+}
+template <int N, typename F>
+__device__ __forceinline__ float across_rows(float v, F f) {
+  uint32_t a, b;
+  swapped<N>(__float_as_uint(v), a, b);
+  return f(__uint_as_float(a), __uint_as_float(b));
+}
+template <int N, typename F>
+__device__ __forceinline__ double across_rows(double v, F f) {
+  uint32_t a[2], b[2];
+  swapped<N>((uint32_t)__double2loint(v), a[0], b[0]);
+  swapped<N>((uint32_t)__double2hiint(v), a[1], b[1]);
+  return f(__hiloint2double((int)a[1], (int)a[0]), __hiloint2double((int)b[1], (int)b[0]));
+}
 // NT neighbouring lanes' values combined by a commutative f, the same in all of them.
 template <int NT, typename T, typename F>
 __device__ __forceinline__ T lanes_reduce(T v, F f) {
@@ -300,8 +328,8 @@ __device__ __forceinline__ T lanes_reduce(T v, F f) {
   if constexpr (NT >= 4) v = f(v, dpp_moved<0x4E>(v));   // quad_perm 2, 3, 0, 1
   if constexpr (NT >= 8) v = f(v, dpp_moved<0x141>(v));  // row_half_mirror
   if constexpr (NT >= 16) v = f(v, dpp_moved<0x140>(v)); // row_mirror
-  if constexpr (NT >= 32) v = f(v, __shfl_xor(v, 16, 64));
-  if constexpr (NT >= 64) v = f(v, __shfl_xor(v, 32, 64));
+  if constexpr (NT >= 32) v = across_rows<16>(v, f);
+  if constexpr (NT >= 64) v = across_rows<32>(v, f);
   return v;
 }
 
