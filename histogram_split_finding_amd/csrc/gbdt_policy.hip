@@ -47,8 +47,8 @@ struct LogpArgs {
   const int64_t* range;                // rows [range[0], range[last]) only, or NULL: all
   double c, inv_T;                     // log2(e) / T, 1 / T
   // c as c_hi + c_lo, both positive: rounding c alone would move all terms of a sum the
-  // same way, by D 2^-25 (and c_lo > 0 leaves -inf what it is)
-  float c_hi, c_lo;
+  // same way, by D 2^-25 (and c_lo > 0 leaves -inf what it is); and c rounded
+  float c_hi, c_lo, c_near;
   const float *old_logp, *ref_logp, *adv, *weight;
   double low, high, kl;  // borders of the ratio
   double log_low, log_high;
@@ -66,7 +66,7 @@ struct LogpArgs {
 __device__ __forceinline__ float sum_term(const LogpArgs& a, float d) {
   return exp2_32(__builtin_fmaf(d, a.c_hi, d * a.c_lo));
 }
-__device__ __forceinline__ float grad_term(const LogpArgs& a, float d) { return exp2_32(d * a.c_hi); }
+__device__ __forceinline__ float grad_term(const LogpArgs& a, float d) { return exp2_32(d * a.c_near); }
 
 // The rows of the call, and one of them.
 struct Span {
@@ -219,7 +219,7 @@ __device__ __forceinline__ RowGrad row_out(const LogpArgs& a, int64_t i, bool wr
 // The class's element of a vector of classes c0, c0 + 1, ...
 template <int VE>
 __device__ __forceinline__ void set_class(float (&f)[VE], int32_t cls, int32_t c0, float v) {
-  const uint32_t at = (uint32_t)(cls - c0);
+  const uint32_t at = (uint32_t)cls - (uint32_t)c0;  // (cls may be any number)
   if (at < (uint32_t)VE) {
 #pragma unroll
     for (int q = 0; q < VE; ++q) f[q] = at == (uint32_t)q ? v : f[q];
@@ -230,7 +230,9 @@ __device__ __forceinline__ void set_class(float (&f)[VE], int32_t cls, int32_t c
 // gradients pass through LDS, so that memory sees whole lines: packed rows of an odd
 // length as they lie there, 16 bytes at a time, others (up to 8 classes; longer ones
 // do not come here) in rows of C | 1 words.  Four classes at a time, -inf behind the
-// row's end.
+// row's end.  Vector instructions bound it, 432 a wave, some 250 of them the row's FP64
+// (step of 581,012 x 7 f32: 12.8 us, floor 8.3; 19.1 when rows were staged word by word
+// and the exponentials were FP64).
 constexpr int kShortStep = 4;
 template <int DT, int R, int CMAX, int FROM>
 __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
@@ -342,7 +344,10 @@ __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
 
 // NT lanes for a row that their V vectors of 16 bytes each hold whole, B rows one
 // after the other in registers.  What is FP64 about a row (some 250 instructions where
-// there is a policy) is done for B rows at once: lane b of the NT has row b.
+// there is a policy) is done for B rows at once: lane b of the NT has row b.  From some
+// 200 classes on memory bounds it (steps of 67,108 x 1,000 bf16: 53 us, 5.1 TB/s; of
+// 33,537 x 2,001 f32: 100 us, 5.4 TB/s), below that vector instructions, the row's ends
+// and odd tails most (600,000 x 33 bf16: 48 us, floor 17).
 template <int DT, int NT, int V, int B, int FROM>
 __global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -540,7 +545,9 @@ __device__ __forceinline__ RowGrad finish_row(const LogpArgs& a, int64_t i, bool
 }
 
 // A workgroup of NT threads for a row that their V vectors each hold whole: one read
-// where the gradient follows.  The first wave does what is FP64 about the row.
+// where the gradient follows.  The first wave does what is FP64 about the row.  Memory
+// bounds it: steps of 22,369 x 3,000 bf16 50 us (5.4 TB/s; 122 when each row was read
+// twice by 256 threads), of 8,388 x 8,000 bf16 47 us.
 template <int DT, int NT, int V>
 __global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -611,6 +618,14 @@ __global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
 // score is above it by 2^20 in the exponential; a second read writes the gradient.
 // Parts leave their sums behind; where no gradient follows, the last workgroup of
 // a row to arrive adds them up, else a second launch does.
+//
+// Memory bounds it where rows are many: step of 4,096 x 131,072 bf16 419 us (4.9 TB/s of
+// what has to move, the rate of a copy; the second read comes from the last-level
+// cache), gradient of 2,048 x 50,001 f32 148 us (5.2 TB/s), sums of 4,096 x 65,537 bf16
+// 96 us (5.0 TB/s).  Loading the next block before this one is worked on made it
+// slower (policy loss of 1,000 x 32,003 f16: 19.4 us, 17.6 without): four to eight
+// workgroups a CU cover for each other.  What is left there is the chain of a row of
+// its own: class, scores, joined sums, FP64 (4 us of 17).
 template <int DT, int NT, int FROM, bool GRAD>
 __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -737,6 +752,7 @@ struct PairArgs {
 // count (statistics other than (0, 0)), in FP64 in a fixed order, then the slope of
 // each row.  logp is taken from the statistics again: its FP32 value is off by up to
 // 2^-24 |logp|, some 10 times what o is, and the sums are small differences of many.
+// Latencies bound it: offsets, statistics, score, FP64 (4 pairs of 25 rows: 4.4 us).
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT) k_pairs(const PairArgs a) {
   __shared__ double sh[4][NT / 64];
@@ -960,9 +976,9 @@ LogpArgs logp_args(const gbdt_scores& x, const int32_t* classes, double temperat
   a.cls = classes;
   a.c = kLog2e / temperature;
   a.inv_T = 1.0 / temperature;
-  a.c_hi = (float)a.c;
+  a.c_near = a.c_hi = (float)a.c;
   if ((double)a.c_hi >= a.c) a.c_hi = std::nextafterf(a.c_hi, 0.0f);
-  a.c_lo = (float)(a.c - (double)a.c_hi);
+  a.c_lo = std::fmax((float)(a.c - (double)a.c_hi), 0x1p-126f);
   a.err = &static_cast<WsCtrl*>(ws)->err;
   a.parts = reinterpret_cast<PartSum*>(static_cast<char*>(ws) + sizeof(WsCtrl));
   a.tickets = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + sizeof(WsCtrl) + kScoresPartBytes);
@@ -1023,14 +1039,16 @@ int check_pairs(const gbdt_pairs* p) {
   return GBDT_OK;
 }
 
-// Threads for a pair by its rows in the mean: each of a thread's rows costs latencies,
-// each wave of a pair the pair's own arithmetic.
+// Threads for a pair by its rows in the mean: each of a thread's rows costs latencies
+// (32 pairs of 128: 6 us with 256 threads, 10 with 64), each wave of a pair the pair's own
+// arithmetic, which counts where pairs are many (a step of 9,375 pairs of 64 rows of 3
+// classes: 28 us with 64 threads, 50 with 256).
 template <int DT>
 void launch_pairs_of(const PairArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.n_pairs);
   if (a.n / a.n_pairs > 512) {
     hipLaunchKernelGGL((k_pairs<DT, 1024>), grid, dim3(1024), 0, s, a);
-  } else if (a.n / a.n_pairs <= 128) {
+  } else if (a.n / a.n_pairs <= 128 && a.n_pairs >= 2048) {
     hipLaunchKernelGGL((k_pairs<DT, 64>), grid, dim3(64), 0, s, a);
   } else {
     hipLaunchKernelGGL((k_pairs<DT, 256>), grid, dim3(256), 0, s, a);
