@@ -538,14 +538,21 @@ def _rows_2d(t, name, n=None, c=None):
     return r, w, stride
 
 
-_dtype_codes = None
+_dtype_codes = _torch = None
+
+
+def _load_torch():
+    """torch as a module's name: an import statement in each call takes its time too."""
+    global _dtype_codes, _torch
+    if _torch is None:
+        import torch
+        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        _torch = torch
 
 
 def _scores(x, name="scores") -> Scores:
-    global _dtype_codes
-    if _dtype_codes is None:
-        import torch
-        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if _torch is None:
+        _load_torch()
     code = _dtype_codes.get(x.dtype)
     if code is None:
         raise ValueError("%s must be float32, bfloat16 or float16" % name)
@@ -671,29 +678,37 @@ def gbdt_sample_classes(scores, u, temperature, top_k, top_p, min_p, out, logp, 
 # --------------------------------------------- learning from drawn classes --
 
 def _here(x):
-    """Refuses tensors of a device that is not the current one: its stream would not be theirs."""
-    import torch
-    if x.is_cuda and x.get_device() != torch._C._cuda_getDevice():
-        raise ValueError("tensors on %s, but the current device is cuda:%d" % (x.device, torch.cuda.current_device()))
+    """Index of a tensor's device, which has to be the current one: its stream is taken."""
+    dev = x.get_device()
+    if dev != _torch._C._cuda_getDevice():
+        raise ValueError("tensors on %s, but the current device is cuda:%d" % (x.device, _torch.cuda.current_device()))
+    return dev
+
+
+def _at(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of the given type and shape on device dev (_vector
+    in half its time)."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on the scores' device"
+                     % (name, dtype, tuple(shape)))
 
 
 def _rows_of(scores, classes, ws):
-    """(Scores, rows, address of classes, workspace address, workspace bytes)"""
-    import torch
+    """(Scores, device, rows, address of classes, workspace address, workspace bytes)"""
     s = _scores(scores)
-    _here(scores)
-    return (s, (s.n_rows,), _vector(classes, "classes", torch.int32, (s.n_rows,), scores)) + _workspace(ws, scores)
+    dev, n = _here(scores), (s.n_rows,)
+    return (s, dev, n, _at(classes, "classes", _torch.int32, n, dev)) + _workspace(ws, scores)
 
 
 def gbdt_class_logp(scores, classes, temperature, logp, stats, ws, stream=None):
     """logp float32 [n]: log softmax(scores / temperature) of one class a row
     (classes int32 [n], below 0: padding), and stats float32 [n, 2] (or None) for
     gbdt_class_logp_grad."""
-    import torch
-    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
     rc = load().gbdt_class_logp(ctypes.byref(s), cp, float(temperature),
-                                _vector(logp, "logp", torch.float32, n, scores),
-                                _vector(stats, "stats", torch.float32, n + (2,), scores, optional=True),
+                                _at(logp, "logp", _torch.float32, n, dev),
+                                None if stats is None else _at(stats, "stats", _torch.float32, n + (2,), dev),
                                 wp, wb, _stream(stream))
     _check(rc, "gbdt_class_logp")
 
@@ -701,20 +716,20 @@ def gbdt_class_logp(scores, classes, temperature, logp, stats, ws, stream=None):
 def gbdt_class_logp_grad(scores, classes, temperature, stats, dlogp, grad, ws, stream=None):
     """Backward pass of the log-probabilities, and of the losses below: grad (the
     scores' type and shape) from dlogp float32 [n] and the forward pass's stats."""
-    import torch
-    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
     rc = load().gbdt_class_logp_grad(ctypes.byref(s), cp, float(temperature),
-                                     _vector(stats, "stats", torch.float32, n + (2,), scores),
-                                     _vector(dlogp, "dlogp", torch.float32, n, scores), grad.data_ptr(),
+                                     _at(stats, "stats", _torch.float32, n + (2,), dev),
+                                     _at(dlogp, "dlogp", _torch.float32, n, dev), grad.data_ptr(),
                                      _grad_rows(scores, grad), wp, wb, _stream(stream))
     _check(rc, "gbdt_class_logp_grad")
 
 
-def _policy(x, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl) -> Policy:
-    import torch
-    f32 = torch.float32
-    return Policy(_vector(old_logp, "old_logp", f32, n, x), _vector(ref_logp, "ref_logp", f32, n, x, optional=True),
-                  _vector(advantage, "advantage", f32, n, x), _vector(weight, "weight", f32, n, x, optional=True),
+def _policy(dev, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl) -> Policy:
+    f32 = _torch.float32
+    return Policy(_at(old_logp, "old_logp", f32, n, dev),
+                  None if ref_logp is None else _at(ref_logp, "ref_logp", f32, n, dev),
+                  _at(advantage, "advantage", f32, n, dev),
+                  None if weight is None else _at(weight, "weight", f32, n, dev),
                   float(clip_low), float(clip_high), float(kl))
 
 
@@ -723,15 +738,14 @@ def gbdt_policy_loss(scores, classes, temperature, old_logp, ref_logp, advantage
     """Forward pass of the clipped policy loss with a KL term.  Per row, float32
     [n]: old_logp, ref_logp (or None: no KL term), advantage, weight (or None);
     out: loss, logp (or None), dlogp = weight times dloss/dlogp, stats [n, 2]."""
-    import torch
-    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
-    p = _policy(scores, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
-    f32 = torch.float32
+    s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p = _policy(dev, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
+    f32 = _torch.float32
     rc = load().gbdt_policy_loss(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
-                                 _vector(loss, "loss", f32, n, scores),
-                                 _vector(logp, "logp", f32, n, scores, optional=True),
-                                 _vector(dlogp, "dlogp", f32, n, scores),
-                                 _vector(stats, "stats", f32, n + (2,), scores), wp, wb, _stream(stream))
+                                 _at(loss, "loss", f32, n, dev),
+                                 None if logp is None else _at(logp, "logp", f32, n, dev),
+                                 _at(dlogp, "dlogp", f32, n, dev),
+                                 _at(stats, "stats", f32, n + (2,), dev), wp, wb, _stream(stream))
     _check(rc, "gbdt_policy_loss")
 
 
@@ -739,12 +753,11 @@ def gbdt_policy_step(scores, classes, temperature, old_logp, ref_logp, advantage
                      loss, logp, grad, ws, stream=None):
     """Loss and gradient in one call: what gbdt_policy_loss and
     gbdt_class_logp_grad give."""
-    import torch
-    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
-    p = _policy(scores, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
+    s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p = _policy(dev, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
     rc = load().gbdt_policy_step(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
-                                 _vector(loss, "loss", torch.float32, n, scores),
-                                 _vector(logp, "logp", torch.float32, n, scores, optional=True), grad.data_ptr(),
+                                 _at(loss, "loss", _torch.float32, n, dev),
+                                 None if logp is None else _at(logp, "logp", _torch.float32, n, dev), grad.data_ptr(),
                                  _grad_rows(scores, grad), wp, wb, _stream(stream))
     _check(rc, "gbdt_policy_step")
 
@@ -753,16 +766,15 @@ def gbdt_preference_workspace_bytes(n_rows: int, n_classes: int) -> int:
     return int(load().gbdt_preference_workspace_bytes(int(n_rows), int(n_classes)))
 
 
-def _pairs(x, n, offsets, ref_logp, weight, beta, smoothing, average):
+def _pairs(dev, n, offsets, ref_logp, weight, beta, smoothing, average):
     """(Pairs, pairs)"""
-    import torch
     cuts = offsets.numel()
     if cuts % 2 != 1:
         raise ValueError("offsets must have 2 pairs + 1 elements")
-    f32, pairs = torch.float32, cuts // 2
-    return Pairs(_vector(offsets, "offsets", torch.int64, (cuts,), x),
-                 _vector(ref_logp, "ref_logp", f32, n, x, optional=True),
-                 _vector(weight, "weight", f32, (pairs,), x, optional=True), pairs, int(bool(average)),
+    f32, pairs = _torch.float32, cuts // 2
+    return Pairs(_at(offsets, "offsets", _torch.int64, (cuts,), dev),
+                 None if ref_logp is None else _at(ref_logp, "ref_logp", f32, n, dev),
+                 None if weight is None else _at(weight, "weight", f32, (pairs,), dev), pairs, int(bool(average)),
                  float(beta), float(smoothing)), pairs
 
 
@@ -772,15 +784,14 @@ def gbdt_preference_loss(scores, classes, temperature, offsets, ref_logp, weight
     [2 pairs + 1]; ref_logp float32 [n] or None, weight float32 [pairs] or None):
     loss float32 [pairs], rewards float32 [pairs, 2] (or None), and of the rows in
     sequences logp, dlogp float32 [n], stats float32 [n, 2]."""
-    import torch
-    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
-    p, pairs = _pairs(scores, n, offsets, ref_logp, weight, beta, smoothing, average)
-    f32 = torch.float32
+    s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p, pairs = _pairs(dev, n, offsets, ref_logp, weight, beta, smoothing, average)
+    f32 = _torch.float32
     rc = load().gbdt_preference_loss(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
-                                     _vector(loss, "loss", f32, (pairs,), scores),
-                                     _vector(rewards, "rewards", f32, (pairs, 2), scores, optional=True),
-                                     _vector(logp, "logp", f32, n, scores), _vector(dlogp, "dlogp", f32, n, scores),
-                                     _vector(stats, "stats", f32, n + (2,), scores), wp, wb, _stream(stream))
+                                     _at(loss, "loss", f32, (pairs,), dev),
+                                     None if rewards is None else _at(rewards, "rewards", f32, (pairs, 2), dev),
+                                     _at(logp, "logp", f32, n, dev), _at(dlogp, "dlogp", f32, n, dev),
+                                     _at(stats, "stats", f32, n + (2,), dev), wp, wb, _stream(stream))
     _check(rc, "gbdt_preference_loss")
 
 
@@ -788,12 +799,12 @@ def gbdt_preference_step(scores, classes, temperature, offsets, ref_logp, weight
                          rewards, grad, ws, stream=None):
     """Loss and gradient in one call; the gradient of rows in no sequence stays as
     it is.  ws: of gbdt_preference_workspace_bytes()."""
-    import torch
-    s, n, cp, wp, wb = _rows_of(scores, classes, ws)
-    p, pairs = _pairs(scores, n, offsets, ref_logp, weight, beta, smoothing, average)
+    s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
+    p, pairs = _pairs(dev, n, offsets, ref_logp, weight, beta, smoothing, average)
     rc = load().gbdt_preference_step(ctypes.byref(s), cp, float(temperature), ctypes.byref(p),
-                                     _vector(loss, "loss", torch.float32, (pairs,), scores),
-                                     _vector(rewards, "rewards", torch.float32, (pairs, 2), scores, optional=True),
+                                     _at(loss, "loss", _torch.float32, (pairs,), dev),
+                                     None if rewards is None else
+                                     _at(rewards, "rewards", _torch.float32, (pairs, 2), dev),
                                      grad.data_ptr(), _grad_rows(scores, grad), wp, wb, _stream(stream))
     _check(rc, "gbdt_preference_step")
 
@@ -814,15 +825,13 @@ def gbdt_route_classes(scores, routing, bias, classes, weights, ws, stream=None)
     make_routing): classes int32 [n, k], ended by -1 where experts are out of
     service, weights float32 [n, k]; bias float32 [experts] (or None) is added for
     the choice alone."""
-    import torch
     s = _scores(scores)
-    _here(scores)
-    shape = (s.n_rows, routing.k)
+    dev, shape = _here(scores), (s.n_rows, routing.k)
     wp, wb = _workspace(ws, scores)
     rc = load().gbdt_route_classes(ctypes.byref(s), ctypes.byref(routing),
-                                   _vector(bias, "bias", torch.float32, (s.n_classes,), scores, optional=True),
-                                   _vector(classes, "classes", torch.int32, shape, scores),
-                                   _vector(weights, "weights", torch.float32, shape, scores), wp, wb,
+                                   None if bias is None else _at(bias, "bias", _torch.float32, (s.n_classes,), dev),
+                                   _at(classes, "classes", _torch.int32, shape, dev),
+                                   _at(weights, "weights", _torch.float32, shape, dev), wp, wb,
                                    _stream(stream))
     _check(rc, "gbdt_route_classes")
 
@@ -830,14 +839,12 @@ def gbdt_route_classes(scores, routing, bias, classes, weights, ws, stream=None)
 def gbdt_route_grad(scores, routing, classes, dweights, grad, ws, stream=None):
     """Backward pass of the routing weights: grad (the scores' type and shape) from
     dweights float32 [n, k], the choice held fixed."""
-    import torch
     s = _scores(scores)
-    _here(scores)
-    shape = (s.n_rows, routing.k)
+    dev, shape = _here(scores), (s.n_rows, routing.k)
     wp, wb = _workspace(ws, scores)
     rc = load().gbdt_route_grad(ctypes.byref(s), ctypes.byref(routing),
-                                _vector(classes, "classes", torch.int32, shape, scores),
-                                _vector(dweights, "dweights", torch.float32, shape, scores), grad.data_ptr(),
+                                _at(classes, "classes", _torch.int32, shape, dev),
+                                _at(dweights, "dweights", _torch.float32, shape, dev), grad.data_ptr(),
                                 _grad_rows(scores, grad), wp, wb, _stream(stream))
     _check(rc, "gbdt_route_grad")
 
@@ -847,16 +854,15 @@ def gbdt_route_lists(classes, n_experts, offsets, order, place, ws, stream=None)
     expert e's are order[offsets[e]:offsets[e + 1]], ascending; offsets int32
     [n_experts + 1], order int32 [places], place int32 (classes' shape, or None),
     where each place stands in order, or -1."""
-    import torch
-    i32t, places = torch.int32, classes.numel()
     if not classes.is_cuda:
         raise ValueError("classes must be a device tensor")
-    _here(classes)
+    _load_torch()
+    dev, i32t, places = _here(classes), _torch.int32, classes.numel()
     wp, wb = _workspace(ws, classes)
-    rc = load().gbdt_route_lists(_vector(classes, "classes", i32t, classes.shape, classes), places, int(n_experts),
-                                 _vector(offsets, "offsets", i32t, (int(n_experts) + 1,), classes),
-                                 _vector(order, "order", i32t, (places,), classes),
-                                 _vector(place, "place", i32t, classes.shape, classes, optional=True), wp, wb,
+    rc = load().gbdt_route_lists(_at(classes, "classes", i32t, classes.shape, dev), places, int(n_experts),
+                                 _at(offsets, "offsets", i32t, (int(n_experts) + 1,), dev),
+                                 _at(order, "order", i32t, (places,), dev),
+                                 None if place is None else _at(place, "place", i32t, classes.shape, dev), wp, wb,
                                  _stream(stream))
     _check(rc, "gbdt_route_lists")
 

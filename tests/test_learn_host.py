@@ -200,10 +200,24 @@ def test_python_calls_refuse_tensors():
 
 
 def test_pair_offsets_shape():
-    x, f = torch.zeros(4, 10), torch.zeros(4)
+    g._load_torch()
+    f, cpu = torch.zeros(4), -1
     with pytest.raises(ValueError, match="2 pairs"):
-        g._pairs(x, (4,), torch.zeros(4, dtype=torch.int64), f, None, 0.1, 0.0, False)
+        g._pairs(cpu, (4,), torch.zeros(4, dtype=torch.int64), f, None, 0.1, 0.0, False)
     with pytest.raises(ValueError, match="offsets"):
-        g._pairs(x, (4,), torch.zeros(3, dtype=torch.int32), f, None, 0.1, 0.0, False)
+        g._pairs(cpu, (4,), torch.zeros(3, dtype=torch.int32), f, None, 0.1, 0.0, False)
     with pytest.raises(ValueError, match="weight"):
-        g._pairs(x, (4,), torch.zeros(3, dtype=torch.int64), f, f, 0.1, 0.0, False)
+        g._pairs(cpu, (4,), torch.zeros(3, dtype=torch.int64), f, f, 0.1, 0.0, False)
+    with pytest.raises(ValueError, match="ref_logp"):
+        g._pairs(cpu, (4,), torch.zeros(3, dtype=torch.int64), f[::2], None, 0.1, 0.0, False)
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(4).double(), torch.zeros(8)[::2], torch.zeros(3), torch.zeros(4, 1)])
+def test_vectors(bad):
+    g._load_torch()
+    with pytest.raises(ValueError, match="loss"):
+        g._at(bad, "loss", torch.float32, (4,), -1)
+    with pytest.raises(ValueError, match="loss"):
+        g._at(torch.zeros(4), "loss", torch.float32, (4,), 0)  # another device
+    with pytest.raises(ValueError, match="loss"):
+        g._at(None, "loss", torch.float32, (4,), -1)
