@@ -1033,7 +1033,7 @@ constexpr size_t preference_rows_at() {
 
 int check_pairs(const gbdt_pairs* p) {
   if (!p) return fail(GBDT_E_ARG, "pairs is null");
-  if (p->n_pairs < 0 || p->n_pairs > 1 << 29) return fail(GBDT_E_ARG, "n_pairs out of [0, 2^29]");
+  if (p->n_pairs < 0 || p->n_pairs > 1 << 21) return fail(GBDT_E_ARG, "n_pairs out of [0, 2^21]");
   if (!std::isfinite(p->beta)) return fail(GBDT_E_ARG, "beta must be finite");
   if (!(p->smoothing >= 0.0) || !(p->smoothing < 0.5)) return fail(GBDT_E_ARG, "smoothing out of [0, 1/2)");
   return GBDT_OK;

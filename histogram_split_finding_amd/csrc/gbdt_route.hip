@@ -45,6 +45,7 @@ struct RouteArgs {
   void* grad;
   int64_t ldg;
   int32_t* err;
+  int64_t row0;  // of this launch
 };
 
 // A score as the softmax has it: NaN is out of service, +inf the largest number.
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
   const int lane = threadIdx.x & (NT - 1), sub = threadIdx.x / NT;
   const int first_lane = (threadIdx.x & 63) & ~(NT - 1);  // of the row, in the wave
   const uint64_t below = ((uint64_t(1) << lane) - 1) << first_lane;  // the row's lanes below this one
-  const int64_t row = int64_t(blockIdx.x) * kRows + sub;
+  const int64_t row = a.row0 + int64_t(blockIdx.x) * kRows + sub;
   const bool mine = row < a.n;
   const int64_t i = mine ? row : a.n - 1;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
   __shared__ uint32_t all_place[kRows][W / 4];  // a byte per expert
   __shared__ float all_value[kRows][GBDT_MAX_ROUTED];
   const int lane = threadIdx.x & (NT - 1), sub = threadIdx.x / NT;
-  const int64_t row = int64_t(blockIdx.x) * kRows + sub;
+  const int64_t row = a.row0 + int64_t(blockIdx.x) * kRows + sub;
   const bool mine = row < a.n;
   const int64_t i = mine ? row : a.n - 1;
   const Elem* __restrict__ xr = static_cast<const Elem*>(a.x) + i * a.ld;
@@ -468,36 +469,55 @@ __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
   const int64_t share = (a.chunk + W * 64 - 1) / (W * 64) * 64;
   const int64_t from_all = lo + wid * share, from = from_all < hi ? from_all : hi;
   const int64_t to = hi - from < share ? hi : from + share;
+  // A wave's first places stay in registers; they and the counts are on their way
+  // together.  Of the counts a thread adds up some workgroups' of an expert or two (where
+  // experts are few, several threads share an expert's workgroups).
+  constexpr int kHeld = 2;
+  int32_t held[kHeld];
+#pragma unroll
+  for (int t = 0; t < kHeld; ++t) {
+    const int64_t p = from + t * 64 + lane;
+    held[t] = p < to ? listed_class(a, p, true) : -1;
+  }
+  int32_t width = 1;
+  while (width < a.E) width *= 2;
+  width = width < NT ? width : NT;
+  int32_t seen[EPT], ahead_of[EPT];
+#pragma unroll
+  for (int u = 0; u < EPT; ++u) {
+    const int32_t e = (tid & (width - 1)) + u * width;
+    seen[u] = ahead_of[u] = 0;
+    if (a.blocks > 1 && e < a.E) {
+      const int32_t step = NT / width;
+#pragma unroll 16
+      for (int32_t b = tid / width; b < a.blocks; b += step) {
+        const int32_t v = a.counts[b * a.E + e];
+        seen[u] += v;
+        ahead_of[u] += b < (int32_t)blockIdx.x ? v : 0;
+      }
+    }
+  }
   for (int e = tid; e < a.E; e += NT) {
     for (int w = 0; w < W; ++w) next[w][e] = 0u;
     total_of[e] = before_of[e] = 0;
   }
   __syncthreads();
-  for (int64_t p = from + lane; p < to; p += 64) {
+#pragma unroll
+  for (int t = 0; t < kHeld; ++t)
+    if (held[t] >= 0) atomicAdd(&next[wid][held[t]], 1u);
+  for (int64_t p = from + kHeld * 64 + lane; p < to; p += 64) {
     const int32_t c = listed_class(a, p, true);
     if (c >= 0) atomicAdd(&next[wid][c], 1u);
   }
-  __syncthreads();
-  // All workgroups' counts, and those before this one: where experts are few, several
-  // threads share an expert's workgroups.
-  if (a.blocks > 1) {
-    int32_t width = 1;
-    while (width < a.E) width *= 2;
-    width = width < NT ? width : NT;
-    const int32_t first = tid / width, step = NT / width;
-    for (int32_t e = tid & (width - 1); e < a.E; e += width) {
-      int32_t all = 0, before = 0;
-#pragma unroll 16
-      for (int32_t b = first; b < a.blocks; b += step) {
-        const int32_t v = a.counts[b * a.E + e];
-        all += v;
-        before += b < (int32_t)blockIdx.x ? v : 0;
-      }
-      atomicAdd(&total_of[e], all);
-      atomicAdd(&before_of[e], before);
+#pragma unroll
+  for (int u = 0; u < EPT; ++u) {
+    const int32_t e = (tid & (width - 1)) + u * width;
+    if (a.blocks > 1 && e < a.E) {
+      atomicAdd(&total_of[e], seen[u]);
+      atomicAdd(&before_of[e], ahead_of[u]);
     }
-    __syncthreads();
   }
+  __syncthreads();
   int32_t all[EPT], before[EPT], sum = 0;
 #pragma unroll
   for (int u = 0; u < EPT; ++u) {
@@ -533,9 +553,7 @@ __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
   __syncthreads();
   int bits = 0;
   while (1 << bits < a.E) ++bits;
-  for (int64_t p0 = from; p0 < to; p0 += 64) {
-    const int64_t p = p0 + lane;
-    const int32_t c = p < to ? listed_class(a, p, false) : -1;
+  auto put = [&](int64_t p, int32_t c) {  // 64 places, by a wave
     uint64_t same = __ballot(c >= 0);
     for (int b = 0; b < bits; ++b) {
       const uint64_t set = __ballot(c >> b & 1);
@@ -554,27 +572,39 @@ __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (a.place != nullptr && p < to) a.place[p] = pos;
-  }
+  };
+#pragma unroll
+  for (int t = 0; t < kHeld; ++t)
+    if (from + t * 64 < to) put(from + t * 64 + lane, held[t]);
+  for (int64_t p0 = from + kHeld * 64; p0 < to; p0 += 64)
+    put(p0 + lane, p0 + lane < to ? listed_class(a, p0 + lane, false) : -1);
 }
 
 // -------------------------------------------------------------------- host --
 
+// `launch` for all rows, kRows a workgroup.
+template <int64_t kRows, typename Launch>
+void each_grid(RouteArgs a, hipStream_t s, Launch launch) {
+  for (a.row0 = 0; a.row0 < a.n; a.row0 += kMaxRowGrid * kRows) {
+    const int64_t left = (a.n - a.row0 + kRows - 1) / kRows;
+    diag_begin(kDiagRoute, s);
+    launch(dim3((unsigned)(left < kMaxRowGrid ? left : kMaxRowGrid)), a);
+    diag_end(s);
+  }
+}
+
 template <int DT, int NT, int EPL, bool BY_VALUE>
-void launch_route(const RouteArgs& a, hipStream_t s) {
-  constexpr int64_t kRows = kRouteThreads / NT;
-  diag_begin(kDiagRoute, s);
-  hipLaunchKernelGGL((k_route<DT, NT, EPL, BY_VALUE>), dim3((unsigned)((a.n + kRows - 1) / kRows)),
-                     dim3(kRouteThreads), 0, s, a);
-  diag_end(s);
+void launch_route(const RouteArgs& args, hipStream_t s) {
+  each_grid<kRouteThreads / NT>(args, s, [s](dim3 grid, const RouteArgs& a) {
+    hipLaunchKernelGGL((k_route<DT, NT, EPL, BY_VALUE>), grid, dim3(kRouteThreads), 0, s, a);
+  });
 }
 
 template <int DT, int NT, int V>
-void launch_route_grad(const RouteArgs& a, hipStream_t s) {
-  constexpr int64_t kRows = kRouteThreads / NT;
-  diag_begin(kDiagRoute, s);
-  hipLaunchKernelGGL((k_route_grad<DT, NT, V>), dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kRouteThreads), 0, s,
-                     a);
-  diag_end(s);
+void launch_route_grad(const RouteArgs& args, hipStream_t s) {
+  each_grid<kRouteThreads / NT>(args, s, [s](dim3 grid, const RouteArgs& a) {
+    hipLaunchKernelGGL((k_route_grad<DT, NT, V>), grid, dim3(kRouteThreads), 0, s, a);
+  });
 }
 
 // Rows that all run at once get a wave each: fewer experts a lane, shorter rounds.

@@ -875,7 +875,7 @@ typedef struct gbdt_pairs {
   const int64_t* offsets;
   const float* ref_logp;
   const float* weight;
-  int32_t n_pairs; /* 0 .. 2^29 */
+  int32_t n_pairs; /* 0 .. 2^21 */
   int32_t average;
   double beta, smoothing;
 } gbdt_pairs;

@@ -271,6 +271,51 @@ def test_many_rows(C, n):
     check_pairs(x, xh, cls, 1.0, "f32", cuts, 0.1, 0.0, True)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [7, 60, 1000, 2049])
+def test_few_rows_as_many(C, dtype):
+    """The rows of a few pairs alone, and as the first of many rows: the same losses,
+    rewards, statistics and gradients, and those of loss and step."""
+    say("learn, few rows as many: C=%d %s" % (C, dtype))
+    n, more = 300, 700
+    x, xh = ref.rows(n + more, C, dtype, C)
+    cls = draw_classes(xh, 4)
+    cuts = np.array([0, 90, 100, 100, 290], dtype=np.int64)
+    got = []
+    for rows in (n, n + more):
+        f = lambda *s: torch.zeros(*s, device=DEV)  # noqa: E731
+        part = x[:rows]
+        ws = workspace(part, True)
+        loss, rewards, logp, dlogp, stats, grad = f(2), f(2, 2), f(rows), f(rows), f(rows, 2), torch.zeros_like(part)
+        args = (to_dev(cls[:rows]), 1.0, to_dev(cuts), None, None, 0.1, 0.1, False)
+        g.gbdt_preference_loss(part, *args, loss, rewards, logp, dlogp, stats, ws)
+        loss2 = f(2)
+        g.gbdt_preference_step(part, *args, loss2, None, grad, ws)
+        assert torch.equal(loss, loss2) and g.gbdt_read_error(ws) == 0
+        got.append([t.double().cpu().numpy()[:290] for t in (loss, rewards, stats[:, 0], stats[:, 1], logp, dlogp, grad)])
+    # sums in another order: FP32 terms in FP64 sums, then what follows from one rounding of o
+    for a, b in zip(*got):
+        assert np.allclose(a, b, rtol=8 * STEP, atol=8 * STEP * np.abs(b).max())
+
+
+@pytest.mark.parametrize("C,n", [(4100, (1 << 20) + 5)])
+def test_more_rows_than_a_grid(C, n):
+    """A second launch takes up where the first grid ends."""
+    say("learn, rows of two grids: %d x %d" % (n, C))
+    few, xh = ref.rows(64, C, "bf16", 9)
+    x = few.repeat((n + 63) // 64, 1)[:n]
+    cls = to_dev(draw_classes(xh, 1, 0.0)).repeat((n + 63) // 64)[:n].contiguous()
+    ws = workspace(x)
+    logp, stats = torch.zeros(n, device=DEV), torch.zeros(n, 2, device=DEV)
+    g.gbdt_class_logp(x, cls, 1.0, logp, stats, ws)
+    want = logp[:64].repeat((n + 63) // 64)[:n]
+    assert torch.equal(logp, want) and bool((want < 0).all())
+    grad = torch.empty_like(x)
+    g.gbdt_class_logp_grad(x, cls, 1.0, stats, torch.ones(n, device=DEV), grad, ws)
+    assert torch.equal(grad[-69:], grad[:n][(n - 69) % 64:][:69])
+    assert g.gbdt_read_error(ws) == 0
+
+
 def test_long_sequences():
     """More rows of a sequence than a workgroup has threads, and pairs of one row."""
     say("learn: long sequences")

@@ -302,6 +302,24 @@ def test_streams_graphs_and_repeats(n):
     assert g.gbdt_read_error(ws) == 0 and g.gbdt_read_error(ws2) == 0
 
 
+def test_more_rows_than_a_grid():
+    """A second launch takes up where the first grid ends."""
+    E, n, k = 520, (1 << 22) + 5, 3
+    say("route, rows of two grids: %d x %d" % (n, E))
+    few, xh = scores(64, E, "bf16", 3)
+    x = few.repeat((n + 63) // 64, 1)[:n]
+    r = g.make_routing(k, renormalise=False)
+    ws = workspace(n, E)
+    classes, weights = torch.full((n, k), -7, dtype=torch.int32, device=DEV), torch.zeros(n, k, device=DEV)
+    g.gbdt_route_classes(x, r, None, classes, weights, ws)
+    assert np.array_equal(classes[:64].cpu().numpy(), np.stack([lref.route(xh[i], r, None)[0] for i in range(64)]))
+    assert torch.equal(classes, classes[:64].repeat((n + 63) // 64, 1)[:n])
+    grad = torch.full_like(x, 7.0)
+    g.gbdt_route_grad(x, r, classes, weights, grad, ws)
+    assert torch.equal(grad[64:], grad[:64].repeat((n + 63) // 64, 1)[64:n])
+    assert g.gbdt_read_error(ws) == 0
+
+
 def test_no_rows():
     x = torch.zeros(0, 12, device=DEV)
     ws = workspace(0, 12)

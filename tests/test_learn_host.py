@@ -141,7 +141,7 @@ def test_policy_rules(kw):
     assert policy_loss(scores(), policy(**kw)) == policy_step(scores(), policy(**kw)) == -1
 
 
-@pytest.mark.parametrize("kw", [dict(n_pairs=-1), dict(n_pairs=(1 << 29) + 1), dict(beta=float("nan")),
+@pytest.mark.parametrize("kw", [dict(n_pairs=-1), dict(n_pairs=(1 << 21) + 1), dict(beta=float("nan")),
                                 dict(beta=float("inf")), dict(smoothing=-0.1), dict(smoothing=0.5),
                                 dict(smoothing=float("nan"))])
 def test_pair_rules(kw):
