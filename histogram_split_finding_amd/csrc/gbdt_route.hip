@@ -342,7 +342,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     for (int j = 0; j < V; ++j) {
       float f[VE];
       unpack<DT>(raw[j], f);
-      m = __builtin_fmaxf(m, __builtin_fminf(max_of(f), kMaxF32));  // (NaN stays out)
+#pragma unroll
+      for (int q = 0; q < VE; ++q) f[q] = in_service(f[q]);  // (a maximum of NaN alone would be NaN)
+      m = __builtin_fmaxf(m, max_of(f));
     }
   }
   m = group_max<NT>(m);
