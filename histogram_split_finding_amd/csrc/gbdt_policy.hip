@@ -72,12 +72,15 @@ __device__ __forceinline__ float grad_term(const LogpArgs& a, float d) { return 
 struct Span {
   int64_t lo, hi;
 };
+__device__ __forceinline__ Span span_of(const int64_t* __restrict__ offsets, int32_t last, int64_t n) {
+  int64_t lo = offsets[0], hi = offsets[last];
+  lo = lo < 0 ? 0 : lo > n ? n : lo;
+  hi = hi < lo ? lo : hi > n ? n : hi;
+  return {lo, hi};
+}
 __device__ __forceinline__ Span row_span(const LogpArgs& a) {
   if (a.range == nullptr) return {0, a.n};
-  int64_t lo = a.range[0], hi = a.range[a.last];
-  lo = lo < 0 ? 0 : lo > a.n ? a.n : lo;
-  hi = hi < lo ? lo : hi > a.n ? a.n : hi;
-  return {lo, hi};
+  return span_of(a.range, a.last, a.n);
 }
 
 __device__ __forceinline__ int32_t row_class(const LogpArgs& a, int64_t i, bool report) {
@@ -742,7 +745,7 @@ struct PairArgs {
   const int64_t* offsets;
   const float *ref_logp, *weight;
   double beta, smoothing;
-  int32_t n_pairs, average;
+  int32_t C, n_pairs, average;
   const float* stats;
   float *loss, *rewards, *dlogp;
   int32_t* err;
@@ -758,13 +761,15 @@ __global__ void __launch_bounds__(NT) k_pairs(const PairArgs a) {
   __shared__ double sh[4][NT / 64];
   const int tid = threadIdx.x, wid = tid >> 6;
   const int64_t p = blockIdx.x;
+  // (no rows but those that the launch before had: of others there are no statistics)
+  const Span span = span_of(a.offsets, 2 * a.n_pairs, a.n);
   int64_t cut[3];
   bool bad = false;
 #pragma unroll
   for (int u = 0; u < 3; ++u) {
     const int64_t v = a.offsets[2 * p + u];
-    const int64_t from = u == 0 ? 0 : cut[u - 1];
-    cut[u] = v < from ? from : v > a.n ? a.n : v;
+    const int64_t from = u == 0 ? span.lo : cut[u - 1];
+    cut[u] = v < from ? from : v > span.hi ? span.hi : v;
     bad = bad || cut[u] != v;
   }
   if (bad && tid == 0) dev_error(a.err, GBDT_E_RANGE);
@@ -774,7 +779,7 @@ __global__ void __launch_bounds__(NT) k_pairs(const PairArgs a) {
   auto score = [&](int64_t i, bool& counts) {
     const float m = a.stats[2 * i], o = a.stats[2 * i + 1];
     const int32_t cls = a.cls[i];
-    counts = !(m == 0.0f && o == 0.0f);
+    counts = !(m == 0.0f && o == 0.0f) && (uint32_t)cls < (uint32_t)a.C;
     return counts ? Score<DT>::to_f32(static_cast<const typename Score<DT>::Elem*>(a.x)[i * a.ld + cls]) : -kInf;
   };
   int32_t turn = 0;
@@ -1061,6 +1066,7 @@ int launch_pairs(const gbdt_pairs& p, const gbdt_scores& x, const int32_t* class
   a.x = x.data;
   a.n = x.n_rows;
   a.ld = x.row_stride;
+  a.C = x.n_classes;
   a.cls = classes;
   a.inv_T = 1.0 / temperature;
   a.offsets = p.offsets;

@@ -861,8 +861,9 @@ int gbdt_policy_step(const gbdt_scores* x /* host */, const int32_t* classes, do
  * (ones); a pair of weight 0 has slopes 0.  A logp of -inf makes its reward -inf
  * and leaves the other rows' slopes finite; two rewards of the same infinity, as a
  * NaN, make the pair NaN.  beta finite, smoothing in [0, 1/2).  Offsets that
- * descend or leave [0, n_rows] are recorded as GBDT_E_RANGE, and the outputs are
- * then unspecified.  Host struct holding device pointers.
+ * descend or leave [0, n_rows] are recorded as GBDT_E_RANGE, and the outputs of the
+ * pairs, and of the rows from the first offset to the last, are then unspecified.
+ * Host struct holding device pointers.
  *
  * gbdt_preference_loss writes loss[n_pairs], rewards[n_pairs][2] (may be NULL),
  * and logp, dlogp, stats of the rows in sequences; rows before the first and
