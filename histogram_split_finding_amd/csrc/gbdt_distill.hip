@@ -708,7 +708,7 @@ extern "C" {
 
 size_t gbdt_scores_workspace_bytes(int64_t n_rows, int32_t n_classes) {
   if (n_rows < 0 || n_rows > (int64_t(1) << 31) || n_classes < 1 || n_classes > GBDT_MAX_CLASSES) return 0;
-  return sizeof(WsCtrl) + kScoresPartBytes + kScoresTicketBytes;
+  return sizeof(WsCtrl) + kScoresPartBytes;
 }
 
 int gbdt_distill_loss(const gbdt_scores* x, const gbdt_teacher* t, float temperature, float* loss,

@@ -34,7 +34,9 @@ struct WsCtrl {
   int32_t err_detail;   // call-specific detail (e.g. offending node)
   uint32_t unused0;
   int32_t plan_total;   // tiles planned by the last planner launch
-  int32_t pad[60];
+  uint32_t arrived[32]; // a byte for each row of scores that workgroups share:
+                        // how many of them are done, 0 between calls
+  int32_t pad[28];
 };
 static_assert(sizeof(WsCtrl) == 256, "control block is 256 bytes");
 

@@ -58,7 +58,7 @@ struct LogpArgs {
   int64_t ldg;
   int32_t* err;
   PartSum* parts;     // [n][n_parts]
-  uint32_t* tickets;  // [n], zero between calls
+  uint32_t* arrived;  // a byte a row: its parts that are done, zero between calls
   int64_t row0;       // of this launch
 };
 
@@ -688,13 +688,17 @@ __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
       __hip_atomic_store(&parts[part].m, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     if constexpr (GRAD) return;
+    // (at most 64 parts: no byte carries into its neighbour)
+    uint32_t* word = a.arrived + row / 4;
+    const int shift = (int)(row % 4) * 8;
     if (tid == 0) {
-      const uint32_t before = __hip_atomic_fetch_add(&a.tickets[row], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      sh_last = before == (uint32_t)a.n_parts - 1u;
+      const uint32_t before = __hip_atomic_fetch_add(word, 1u << shift, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      sh_last = (before >> shift & 0xffu) == (uint32_t)a.n_parts - 1u;
     }
     __syncthreads();
     if (!sh_last) return;
-    if (tid == 0) __hip_atomic_store(&a.tickets[row], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (tid == 0)
+      __hip_atomic_fetch_sub(word, (uint32_t)a.n_parts << shift, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   if constexpr (FROM == kJoin || FROM == kParts) {
     m = -kInf;
@@ -986,7 +990,7 @@ LogpArgs logp_args(const gbdt_scores& x, const int32_t* classes, double temperat
   a.c_lo = std::fmax((float)(a.c - (double)a.c_hi), 0x1p-126f);
   a.err = &static_cast<WsCtrl*>(ws)->err;
   a.parts = reinterpret_cast<PartSum*>(static_cast<char*>(ws) + sizeof(WsCtrl));
-  a.tickets = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + sizeof(WsCtrl) + kScoresPartBytes);
+  a.arrived = static_cast<WsCtrl*>(ws)->arrived;
   return a;
 }
 
@@ -1033,7 +1037,7 @@ int policy(const gbdt_scores* x, const int32_t* classes, double temperature, con
 // The preference step's workspace: that of the rows, then each row's statistics and
 // slope.
 constexpr size_t preference_rows_at() {
-  return (sizeof(WsCtrl) + kScoresPartBytes + kScoresTicketBytes + 255) / 256 * 256;
+  return sizeof(WsCtrl) + kScoresPartBytes;
 }
 
 int check_pairs(const gbdt_pairs* p) {

@@ -530,10 +530,11 @@ __device__ __forceinline__ void unstage(int32_t rows, int32_t width, bool flat, 
 }
 
 // Workspace of the row calls: the control block, then partial results of rows
-// that several workgroups share, then a counter for each such row, zero between
-// calls (the last workgroup of a row to arrive sets it back).
+// that several workgroups share.  What has to stay from call to call, a counter
+// for each such row, is in the control block: behind it every call of the library
+// writes what it likes.
 constexpr size_t kScoresPartBytes = size_t(1) << 20;
-constexpr size_t kScoresTicketBytes = kSplitRows * 4;
+static_assert(sizeof(WsCtrl::arrived) == kSplitRows, "a byte for each row that is split");
 
 // Host checks shared by the entry points.
 int check_scores(const gbdt_scores* x);

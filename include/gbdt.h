@@ -43,7 +43,8 @@
  *  - Every call that takes a workspace needs at least gbdt_workspace_bytes()
  *    bytes, 256-byte aligned.  Calls that share a workspace must be ordered
  *    (same stream).  The workspace must be zero-filled once before first use
- *    (its error word); after that the library keeps it consistent.
+ *    (its first 256 bytes: the error word, and counters that are zero between
+ *    calls); after that the library keeps it consistent.
  */
 #ifndef GBDT_H_
 #define GBDT_H_
@@ -709,7 +710,8 @@ typedef struct gbdt_teacher {
 
 /* Workspace bytes of every call of this section for n_rows x n_classes scores
  * (0 if a size is out of range).  Zero-filled before its first use; it serves
- * one call at a time (calls on one stream may share it). */
+ * one call at a time (calls on one stream may share it, calls of other sections
+ * among them). */
 size_t gbdt_scores_workspace_bytes(int64_t n_rows, int32_t n_classes);
 
 /*
