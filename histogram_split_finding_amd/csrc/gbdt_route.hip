@@ -5,7 +5,7 @@
 // d_j = dweight_j:
 //   weight_j = scale s_j / N,  N = sum_J s or 1,
 //   ds_j = scale (d_j - [renormalised] sum_J d s / N) / N,
-//   sigmoid:  dx_j = ds_j s_j (1 - s_j),
+//   sigmoid:  dx_j = ds_j s_j (1 - s_j), with 1 - s(x) as s(-x),
 //   softmax:  dx_c = s_c ([c in J] ds_c - sum_J ds s), whose second sum is 0 where
 // the weights are renormalised: then, as with sigmoid values, the gradient is 0
 // outside J.
@@ -362,12 +362,14 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     total = group_sum<NT>((double)sum);
     total = total > 0.0 ? 1.0 / total : 0.0;
   }
-  double s[kMost], part[2] = {0.0, 0.0};
+  double s[kMost], away[kMost], part[2] = {0.0, 0.0};
 #pragma unroll
   for (int u = 0; u < kMost; ++u) {
     s[u] = 0.0;
+    away[u] = 1.0;
     if (cls[u] >= 0 && !(xc[u] == -kInf)) {
       s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - (double)base) * kLog2e) * total;
+      if (a.sigmoid) away[u] = sigmoid_64(-xc[u]);
       part[0] += s[u];
       part[1] += s[u] * (double)d[u];
     }
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     const int32_t j = lane + u * NT;
     if (cls[u] >= 0) {
       const double ds = by * ((double)d[u] - mean) - pull;
-      value[j] = (float)(s[u] == 0.0 ? 0.0 : s[u] * (a.sigmoid ? 1.0 - s[u] : 1.0) * ds);
+      value[j] = (float)(s[u] == 0.0 ? 0.0 : s[u] * away[u] * ds);
       uint32_t* word = place + cls[u] / 4;
       const int shift = cls[u] % 4 * 8;
       if (atomicOr(word, (uint32_t)(j + 1) << shift) >> shift & 0xffu && mine) dev_error(a.err, GBDT_E_ARG);

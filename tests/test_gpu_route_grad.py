@@ -83,3 +83,25 @@ def test_vectors_of_nan(E, dtype):
             tol = (ref.EPS[dtype] / 2 + 2 * STEP) * np.abs(want) + size * (6 * D + 10) * STEP + TINY[dtype]
             assert np.all(np.abs(got[i] - want) <= tol), (form, i, got[i], want)
             assert np.all(got[i][~np.isfinite(xh[i])] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_saturated_sigmoids(renormalise, dtype):
+    """Scores from -80 to 80: the derivative s(x) s(-x) keeps its digits on both sides.
+    FP64, rounded once; 2^-45 for the functions and for what cancels in the mean."""
+    say("route gradient, saturated: %s %s" % (renormalise, dtype))
+    E, k = 40, 16
+    rng = np.random.default_rng(3)
+    b = np.stack([np.linspace(-80.0, 80.0, E), rng.uniform(-80.0, 80.0, E), rng.uniform(10.0, 60.0, E),
+                  rng.uniform(-60.0, -10.0, E), np.where(np.arange(E) % 2, 30.0, -30.0)])
+    t = torch.from_numpy(b).to(ref.TYPES[dtype])
+    x, xh = ref.place(t), t.double().numpy()
+    r = g.make_routing(k, sigmoid=True, renormalise=renormalise, scale=1.5)
+    c = np.stack([rng.permutation(E)[:k] for _ in b]).astype(np.int32)
+    dw = rng.normal(0.0, 1.0, (len(b), k)).astype(np.float32)
+    got = gradient(x, r, to_dev(c), dw)
+    for i in range(len(b)):
+        want, size = rref.grad(xh[i], r, c[i], dw[i])
+        tol = (ref.EPS[dtype] / 2 + STEP) * np.abs(want) + 2.0 ** -45 * size + TINY[dtype]
+        assert np.all(np.abs(got[i] - want) <= tol), (i, got[i], want)
