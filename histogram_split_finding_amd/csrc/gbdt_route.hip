@@ -3,12 +3,17 @@
 //
 // With s the softmax or sigmoid values of a row's scores, J the chosen experts and
 // d_j = dweight_j:
-//   weight_j = scale s_j / N,  N = sum_J s or 1,
-//   ds_j = scale (d_j - [renormalised] sum_J d s / N) / N,
-//   sigmoid:  dx_j = ds_j s_j (1 - s_j), with 1 - s(x) as s(-x),
-//   softmax:  dx_c = s_c ([c in J] ds_c - sum_J ds s), whose second sum is 0 where
-// the weights are renormalised: then, as with sigmoid values, the gradient is 0
-// outside J.
+//   weight_j = scale w_j,  w_j = s_j / sum_J s or s_j,
+//   sigmoid:                    dx_j = scale s_j s(-x_j) d_j,
+//   sigmoid, renormalised:      dx_j = scale w_j s(-x_j) (d_j - sum_J w d),
+//   softmax, renormalised:      dx_j = scale w_j (d_j - sum_J w d),
+//   softmax:                    dx_j = scale s_j (d_j - sum_J s d),
+//                               dx_c = -scale s_c sum_J s d outside J.
+// d_j - sum_J w d cancels where one expert has nearly all: with u the dweight of J's
+// largest score and R the softmax mass outside J (0 where renormalised) it is
+//   (d_j - u) - sum_J w (d - u) + u R,
+// whose terms are as small as the sum itself.  Where R is 1/2 or more nothing cancels,
+// and u = 0 keeps small d_j beside a large u.
 
 #include <hip/hip_runtime.h>
 
@@ -50,6 +55,12 @@ struct RouteArgs {
 
 // A score as the softmax has it: NaN is out of service, +inf the largest number.
 __device__ __forceinline__ float in_service(float f) { return f == f ? __builtin_fminf(f, kMaxF32) : -kInf; }
+
+// 2^y of a score against the largest, y <= 0.  A NaN score has 0; one of +inf, which
+// counts as the largest number and is then the largest score, 1.  (One instruction.)
+__device__ __forceinline__ float share_32(float y) {
+  return __builtin_fminf(__builtin_fmaxf(exp2_32(y), 0.0f), 1.0f);
+}
 
 // The choice's keys: the scores themselves, or choice values in FP64.  `taken` is
 // below all keys but -inf; an FP64 key is taken by its upper word alone, whatever the
@@ -290,8 +301,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
 }
 
 // NT lanes a row that their V vectors of 16 bytes each hold whole.  A byte per
-// expert in LDS says which place of the list has it.  65,536 x 128 f32 softmax: 15 us,
-// 4.7 TB/s; all rows are in flight at once, so reads and writes do not overlap.
+// expert in LDS says which place of the list has it: the mass outside the choice is
+// summed by itself (as 1 less the rest it would lose its digits).  65,536 x 128 f32
+// softmax: 14 us, 4.9 TB/s; all rows are in flight at once, so reads and writes do not
+// overlap.
 template <int DT, int NT, int V>
 __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -300,6 +313,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
   __shared__ uint32_t all_place[kRows][W / 4];  // a byte per expert
   __shared__ float all_value[kRows][GBDT_MAX_ROUTED];
   const int lane = threadIdx.x & (NT - 1), sub = threadIdx.x / NT;
+  const int first_lane = (threadIdx.x & 63) & ~(NT - 1);  // of the row, in the wave
   const int64_t row = a.row0 + int64_t(blockIdx.x) * kRows + sub;
   const bool mine = row < a.n;
   const int64_t i = mine ? row : a.n - 1;
@@ -336,67 +350,95 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     if (cls[u] >= 0) xc[u] = in_service(Score<DT>::to_f32(xr[cls[u]]));
     m = __builtin_fmaxf(m, xc[u]);
   }
-  double total = 1.0;
   if (whole) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float f[VE];
       unpack<DT>(raw[j], f);
 #pragma unroll
-      for (int q = 0; q < VE; ++q) f[q] = in_service(f[q]);  // (a maximum of NaN alone would be NaN)
-      m = __builtin_fmaxf(m, max_of(f));
+      for (int q = 0; q < VE; ++q) m = __builtin_fmaxf(m, f[q]);  // (m is no NaN, so no NaN gets in)
     }
+    m = __builtin_fminf(m, kMaxF32);
   }
-  m = group_max<NT>(m);
+  const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
+  const auto add = [](double p, double q) { return p + q; };
+  m = lanes_reduce<NT>(m, larger);
   const float base = m == -kInf ? 0.0f : m, c = (float)kLog2e;
-  if (whole) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float f[VE];
-      unpack<DT>(raw[j], f);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) f[q] = exp2_32((in_service(f[q]) - base) * c);
-      sum += sum_of(f);
-    }
-    total = group_sum<NT>((double)sum);
-    total = total > 0.0 ? 1.0 / total : 0.0;
-  }
-  double s[kMost], away[kMost], part[2] = {0.0, 0.0};
-#pragma unroll
-  for (int u = 0; u < kMost; ++u) {
-    s[u] = 0.0;
-    away[u] = 1.0;
-    if (cls[u] >= 0 && !(xc[u] == -kInf)) {
-      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - (double)base) * kLog2e) * total;
-      if (a.sigmoid) away[u] = sigmoid_64(-xc[u]);
-      part[0] += s[u];
-      part[1] += s[u] * (double)d[u];
-    }
-  }
-  part[0] = group_sum<NT>(part[0]);
-  part[1] = group_sum<NT>(part[1]);
-  const double by = a.renorm ? (part[0] > 0.0 ? a.scale / part[0] : (part[0] == 0.0 ? 0.0 : part[0])) : a.scale;
-  const double mean = a.renorm ? (part[0] > 0.0 ? part[1] / part[0] : 0.0) : 0.0;
-  const double pull = whole ? by * part[1] : 0.0;  // sum ds s
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int u = 0; u < kMost; ++u) {
     const int32_t j = lane + u * NT;
     if (cls[u] >= 0) {
-      const double ds = by * ((double)d[u] - mean) - pull;
-      value[j] = (float)(s[u] == 0.0 ? 0.0 : s[u] * away[u] * ds);
       uint32_t* word = place + cls[u] / 4;
       const int shift = cls[u] % 4 * 8;
       if (atomicOr(word, (uint32_t)(j + 1) << shift) >> shift & 0xffu && mine) dev_error(a.err, GBDT_E_ARG);
+    }
+  }
+  double rest = 0.0;  // the exponentials outside the choice
+  if (whole) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f[VE];
+      unpack<DT>(raw[j], f);
+#pragma unroll
+      for (int w = 0; w < VE / 4; ++w) {
+        const uint32_t at = place[(j * NT + lane) * (VE / 4) + w];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float e = share_32((f[w * 4 + q] - base) * c);
+          f[w * 4 + q] = at >> (8 * q) & 0xffu ? 0.0f : e;
+        }
+      }
+      rest += (double)sum_of(f);
+    }
+  }
+  double s[kMost], away[kMost], sum = 0.0;
+  float top = -kInf, top_d = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    s[u] = 0.0;
+    away[u] = 1.0;
+    if (cls[u] >= 0 && !(xc[u] == -kInf)) {
+      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - (double)base) * kLog2e);
+      if (a.sigmoid) away[u] = sigmoid_64(-xc[u]);
+      sum += s[u];
+      top_d = xc[u] > top ? d[u] : top_d;
+      top = __builtin_fmaxf(top, xc[u]);
+    }
+  }
+  // w_j, and the share R that is not of the choice
+  double inv = 1.0, R = 0.0, from = 0.0, mean = 0.0;
+  if (whole || a.renorm) {
+    sum = lanes_reduce<NT>(sum, add);
+    if (whole) rest = lanes_reduce<NT>(rest, add);
+    inv = sum + rest > 0.0 ? 1.0 / (sum + rest) : 0.0;
+    R = rest * inv;
+    const uint64_t has = __ballot(top == lanes_reduce<NT>(top, larger)) >> first_lane & (~uint64_t(0) >> (64 - NT));
+    const float of_top = __shfl(top_d, first_lane + __ffsll((unsigned long long)has) - 1, 64);
+    from = R < 0.5 ? (double)of_top : 0.0;
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+      s[u] *= inv;
+      mean += s[u] == 0.0 ? 0.0 : s[u] * ((double)d[u] - from);
+    }
+    mean = lanes_reduce<NT>(mean, add);
+  }
+#pragma unroll
+  for (int u = 0; u < kMost; ++u) {
+    const int32_t j = lane + u * NT;
+    if (cls[u] >= 0) {
+      const double t = (double)d[u] - from - mean + from * R;
+      value[j] = (float)(s[u] == 0.0 ? 0.0 : s[u] * away[u] * t * a.scale);
     }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   if (!mine) return;
   Elem* __restrict__ gr = static_cast<Elem*>(a.grad) + i * a.ldg;
-  const float others = (float)(-pull * total);
+  const float others = (float)(-(mean + from * (1.0 - R)) * inv * a.scale);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int32_t e0 = c0 + j * NT * VE;
@@ -405,7 +447,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     if (whole) {
       unpack<DT>(raw[j], f);
 #pragma unroll
-      for (int q = 0; q < VE; ++q) f[q] = exp2_32((in_service(f[q]) - base) * c) * others;
+      for (int q = 0; q < VE; ++q) f[q] = share_32((f[q] - base) * c) * others;
     } else {
 #pragma unroll
       for (int q = 0; q < VE; ++q) f[q] = 0.0f;

@@ -105,3 +105,122 @@ def test_saturated_sigmoids(renormalise, dtype):
         want, size = rref.grad(xh[i], r, c[i], dw[i])
         tol = (ref.EPS[dtype] / 2 + STEP) * np.abs(want) + 2.0 ** -45 * size + TINY[dtype]
         assert np.all(np.abs(got[i] - want) <= tol), (i, got[i], want)
+
+
+def sharp_tolerance(x, r, chosen, dw, want, dtype):
+    """Softmax values as they are.  A sum of FP32 exponentials is off by q = (3 D + 5)
+    STEP: the exponent (difference, constant, product, STEP D each), the exponential (2
+    STEP), three additions; D as far as terms of the mass R outside the choice go, those
+    40 below its largest adding nothing.  So are R and each value s.  What the kernel
+    adds up for a chosen expert: d_j - u, s_i (d_i - u) and u R, u the dweight of the
+    largest chosen score where R is below 1/2, else 0.  Others: their own exponential,
+    two products, and sum s d."""
+    (c, s), R, every = rref.parts(x, r, chosen)
+    d = dw[(chosen >= 0) & (chosen < len(x))].astype(np.float64)
+    s, R, every = s.astype(np.float64), float(R), every.astype(np.float64)
+    top, scale = (int(np.argmax(x[c])) if len(c) else 0), abs(r.scale)
+    fin = np.isfinite(x)
+    D = np.where(fin, x[fin].max() - x, 0.0) if fin.any() else np.zeros(len(x))
+    outside = fin.copy()
+    outside[c] = False
+    far = min(90.0, D[outside].min() + 40.0, D[outside].max()) if outside.any() else 0.0
+    q = 0.0 if r.renormalise else (3 * far + 5) * STEP
+    us = [d[top] if len(c) else 0.0]
+    us = us if r.renormalise or R < 0.499 else [0.0] if R > 0.501 else us + [0.0]
+    tol = (ref.EPS[dtype] / 2 + STEP + q) * np.abs(want)
+    terms = max(np.abs(s * (d - u)).sum() + abs(u) * R for u in us) if len(c) else 0.0
+    mine = max(np.abs(d - u) for u in us) if len(c) == 1 else sum(np.abs(d - u) for u in us) if len(c) else 0.0
+    rest = scale * every * np.abs(s * d).sum() * (q + 2.0 ** -45) + (3 * np.minimum(D, 90.0) + 4) * STEP * np.abs(want)
+    rest[c] = scale * s * (q * terms + 2.0 ** -45 * (mine + terms))
+    return tol + rest + TINY[dtype] * (1 + scale * np.abs(d).sum())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [2, 9, 60, 129, 256, 1000])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_a_router_that_is_sure(E, renormalise, dtype):
+    """One expert far above the others, two experts, and all chosen but a few: 1 - s, and
+    the mass outside the choice, keep their digits."""
+    say("route gradient, sure: %d %s %s" % (E, renormalise, dtype))
+    rng = np.random.default_rng(E)
+    b = rng.normal(0.0, 1.0, (9, E))
+    for i, gap in enumerate((0.0, 3.0, 8.0, 15.0, 25.0, 40.0, 70.0)):
+        b[i, rng.integers(E)] += gap
+    b[7, : 2] += 20.0   # two of them
+    b[8, 0] -= 30.0
+    t = torch.from_numpy(b).to(ref.TYPES[dtype])
+    x, xh = ref.place(t), t.double().numpy()
+    for k in sorted({1, 2, min(E, 8), min(E, 32)}):
+        for same in (False, True):  # (equal dweights: renormalised weights have no gradient, others R alone)
+            r = g.make_routing(k, renormalise=renormalise, scale=2.5)
+            classes, _ = route(x, r)
+            c = classes.cpu().numpy()
+            dw = rng.normal(0.0, 1.0, (len(b), k)).astype(np.float32)
+            dw = np.full_like(dw, 0.75) if same else dw
+            got = gradient(x, r, classes, dw)
+            for i in range(len(b)):
+                want, _ = rref.grad(xh[i], r, c[i], dw[i])
+                tol = sharp_tolerance(xh[i], r, c[i], dw[i], want, dtype)
+                assert np.all(np.abs(got[i] - want) <= tol), (k, i, np.max(np.abs(got[i] - want) / tol), got[i], want)
+
+
+@pytest.mark.parametrize("E", [9, 60, 256])
+def test_experts_of_little_mass(E):
+    """The choice, by a bias, is of experts that the softmax has little of, with dweights
+    of very different sizes: each keeps the digits of its own."""
+    say("route gradient, little mass: %d" % E)
+    rng = np.random.default_rng(E)
+    b = rng.normal(0.0, 1.0, (6, E)).astype(np.float32)
+    b[:, 5:] += np.float32(6.0)
+    b[3:, 0] += np.linspace(4.0, 9.0, 3).astype(np.float32)
+    x, xh = ref.place(torch.from_numpy(b)), b.astype(np.float64)
+    k = 4
+    r = g.make_routing(k, renormalise=False)
+    c = np.tile(np.arange(k, dtype=np.int32), (len(b), 1))
+    dw = (rng.normal(0.0, 1.0, (len(b), k)) * 10.0 ** rng.integers(-8, 1, (len(b), k))).astype(np.float32)
+    got = gradient(x, r, to_dev(c), dw)
+    for i in range(len(b)):
+        want, _ = rref.grad(xh[i], r, c[i], dw[i])
+        tol = sharp_tolerance(xh[i], r, c[i], dw[i], want, "f32")
+        assert np.all(np.abs(got[i] - want) <= tol), (i, np.max(np.abs(got[i] - want) / tol), got[i], want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E", [16, 60, 256, 1000])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_odd_rows(E, renormalise, dtype):
+    """Nothing left, all equal, half out of service, infinities, far apart, the lowest."""
+    say("route gradient, odd rows: %d %s %s" % (E, renormalise, dtype))
+    rng = np.random.default_rng(E)
+    b = np.round(rng.normal(0.0, 1.5, (14, E)))
+    b[0] = -np.inf
+    b[1] = 0.0
+    b[2] = -np.inf
+    b[2, E // 2] = 1.0
+    b[3, : E // 2] = -np.inf
+    b[4, 1:] = -np.inf
+    b[5, rng.random(E) < 0.5] = np.nan
+    b[6] = np.where(rng.random(E) < 0.5, 0.0, -0.0)
+    b[7, [1, 3]] = np.inf
+    b[8] = 200.0 + np.round(rng.normal(0.0, 1.0, E))
+    b[9] = -200.0 + np.round(rng.normal(0.0, 1.0, E))
+    b[10] = -np.inf
+    b[10, [0, E - 1]] = [-300.0, 300.0]
+    b[11] = np.where(np.arange(E) % 5 == 0, 3.0, -np.inf)
+    b[12] = -6.0e4
+    b[13, : E - 3] = np.nan
+    b[13, E - 1] = np.inf
+    t = torch.from_numpy(b).to(ref.TYPES[dtype])
+    x = ref.place(t, E % 5)
+    # (+inf counts as the largest FP32 number)
+    xh = np.minimum(t.double().numpy(), float(np.finfo(np.float32).max))
+    for k in (1, 8):
+        r = g.make_routing(k, renormalise=renormalise, scale=1.5)
+        classes, _ = route(x, r)
+        c = classes.cpu().numpy()
+        dw = rng.normal(0.0, 1.0, (len(b), k)).astype(np.float32)
+        got = gradient(x, r, classes, dw)
+        for i in range(len(b)):
+            want, _ = rref.grad(xh[i], r, c[i], dw[i])
+            tol = sharp_tolerance(xh[i], r, c[i], dw[i], want, dtype)
+            assert np.all(np.abs(got[i] - want) <= tol), (k, i, got[i], want)
