@@ -283,10 +283,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
       s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - top_x) * kLog2e) * inv_total;
     sum += s[u];
   }
-  double by = a.scale;
+  double inv = 1.0;
   if (a.renorm) {
     sum = group_sum<NT>(sum);
-    by = sum > 0.0 ? a.scale / sum : 0.0;
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
   if (mine) {
 #pragma unroll
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
       const int32_t j = lane + u * NT;
       if (j < a.k) {
         a.classes[row * a.k + j] = cls[u];
-        a.weights[row * a.k + j] = (float)(s[u] * by);
+        a.weights[row * a.k + j] = (float)(s[u] * inv * a.scale);  // (scale / sum may overflow)
       }
     }
   }

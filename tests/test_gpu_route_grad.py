@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import histogram_split_finding_amd as g
+import learn_ref as lref
 import route_ref as rref
 import scores_ref as ref
 from gpu_util import DEV, say
@@ -224,3 +225,24 @@ def test_odd_rows(E, renormalise, dtype):
             want, _ = rref.grad(xh[i], r, c[i], dw[i])
             tol = sharp_tolerance(xh[i], r, c[i], dw[i], want, dtype)
             assert np.all(np.abs(got[i] - want) <= tol), (k, i, got[i], want)
+
+
+@pytest.mark.parametrize("scale", [2.5, 1000.0])
+def test_values_next_to_nothing(scale):
+    """Sigmoid values of some e^-700: their quotients are ordinary numbers, and so are the
+    weights and their gradient.  FP64, rounded once; 2^-40 for the functions."""
+    say("route, values next to nothing: %g" % scale)
+    E, k = 12, 4
+    rng = np.random.default_rng(4)
+    b = rng.uniform(-706.9, -706.0, (3, E)).astype(np.float32)
+    x, xh = ref.place(torch.from_numpy(b)), b.astype(np.float64)
+    r = g.make_routing(k, sigmoid=True, scale=scale)
+    classes, weights = route(x, r)
+    dw = rng.normal(0.0, 1.0, (len(b), k)).astype(np.float32)
+    got, c = gradient(x, r, classes, dw), classes.cpu().numpy()
+    for i in range(len(b)):
+        wc, ww = lref.route(xh[i], r, None)
+        assert np.array_equal(c[i], wc)
+        assert np.all(np.abs(weights[i].double().cpu().numpy() - ww) <= (STEP + 2.0 ** -40) * np.abs(ww)), (i, weights[i])
+        want, size = rref.grad(xh[i], r, c[i], dw[i])
+        assert np.all(np.abs(got[i] - want) <= STEP * np.abs(want) + 2.0 ** -40 * size), (i, got[i], want)
