@@ -246,3 +246,27 @@ def test_values_next_to_nothing(scale):
         assert np.all(np.abs(weights[i].double().cpu().numpy() - ww) <= (STEP + 2.0 ** -40) * np.abs(ww)), (i, weights[i])
         want, size = rref.grad(xh[i], r, c[i], dw[i])
         assert np.all(np.abs(got[i] - want) <= STEP * np.abs(want) + 2.0 ** -40 * size), (i, got[i], want)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_dweights_that_are_no_numbers(form, bad):
+    """They reach experts in service; one out of service has gradient 0."""
+    say("route gradient, dweight %g: %s" % (bad, form))
+    E, k = 30, 4
+    b = np.random.default_rng(5).normal(0.0, 1.0, (4, E)).astype(np.float32)
+    b[:, 20:] = -np.inf
+    b[:, [3, 7]] = np.nan
+    x = ref.place(torch.from_numpy(b))
+    r = g.make_routing(k, **form)
+    classes, _ = route(x, r)
+    dw = np.ones((4, k), dtype=np.float32)
+    dw[:2, 1] = bad
+    got, c = gradient(x, r, classes, dw), classes.cpu().numpy()
+    out = ~np.isfinite(b)
+    assert np.all(got[out] == 0)
+    assert np.all(np.isfinite(got[2:]))
+    for i in range(2):
+        assert not np.isfinite(got[i, c[i, 1]])
+        if not r.score and not r.renormalise:
+            assert not np.isfinite(got[i][~out[i]]).any()
