@@ -95,9 +95,10 @@ struct RouteKey<true> {
   }
 };
 
-__device__ __forceinline__ double sigmoid_64(float x) {
+__device__ __forceinline__ double sigmoid_64(float x, double* other = nullptr) {  // other: of -x
   const double e = exp2_64(-(double)__builtin_fabsf(x) * kLog2e);
   const double inv = rcp_64(1.0 + e);
+  if (other != nullptr) *other = x < 0.0f ? inv : e * inv;
   return x < 0.0f ? e * inv : inv;
 }
 
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     if (cls[u] >= 0) d[u] = a.dweights[i * a.k + j];
   }
   Vec16<DT> raw[V];
-  float m = -kInf;
+  float m = -kInf, top_d = 0.0f;
   if (whole) load_vecs<DT, V>(xr, c0, NT * VE, E, raw);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -348,8 +349,16 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
   for (int u = 0; u < kMost; ++u) {
     xc[u] = -kInf;
     if (cls[u] >= 0) xc[u] = in_service(Score<DT>::to_f32(xr[cls[u]]));
+    top_d = xc[u] > m ? d[u] : top_d;
     m = __builtin_fmaxf(m, xc[u]);
   }
+  // of the largest chosen score: the score, and its dweight
+  const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
+  const auto add = [](double p, double q) { return p + q; };
+  const float top = lanes_reduce<NT>(m, larger);
+  const uint64_t has = __ballot(m == top) >> first_lane & (~uint64_t(0) >> (64 - NT));
+  top_d = __shfl(top_d, first_lane + __ffsll((unsigned long long)has) - 1, 64);
+  m = top;
   if (whole) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -358,11 +367,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
 #pragma unroll
       for (int q = 0; q < VE; ++q) m = __builtin_fmaxf(m, f[q]);  // (m is no NaN, so no NaN gets in)
     }
-    m = __builtin_fminf(m, kMaxF32);
+    m = lanes_reduce<NT>(__builtin_fminf(m, kMaxF32), larger);
   }
-  const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
-  const auto add = [](double p, double q) { return p + q; };
-  m = lanes_reduce<NT>(m, larger);
   const float base = m == -kInf ? 0.0f : m, c = (float)kLog2e;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -396,17 +402,13 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
     }
   }
   double s[kMost], away[kMost], sum = 0.0;
-  float top = -kInf, top_d = 0.0f;
 #pragma unroll
   for (int u = 0; u < kMost; ++u) {
     s[u] = 0.0;
     away[u] = 1.0;
     if (cls[u] >= 0 && !(xc[u] == -kInf)) {
-      s[u] = a.sigmoid ? sigmoid_64(xc[u]) : exp2_64(((double)xc[u] - (double)base) * kLog2e);
-      if (a.sigmoid) away[u] = sigmoid_64(-xc[u]);
+      s[u] = a.sigmoid ? sigmoid_64(xc[u], &away[u]) : exp2_64(((double)xc[u] - (double)base) * kLog2e);
       sum += s[u];
-      top_d = xc[u] > top ? d[u] : top_d;
-      top = __builtin_fmaxf(top, xc[u]);
     }
   }
   // w_j, and the share R that is not of the choice
@@ -414,13 +416,12 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a)
   if (whole || a.renorm) {
     sum = lanes_reduce<NT>(sum, add);
     if (whole) rest = lanes_reduce<NT>(rest, add);
-    inv = sum + rest > 0.0 ? 1.0 / (sum + rest) : 0.0;
+    inv = sum + rest > 0.0 ? rcp_64(sum + rest) : 0.0;
     R = rest * inv;
-    const uint64_t has = __ballot(top == lanes_reduce<NT>(top, larger)) >> first_lane & (~uint64_t(0) >> (64 - NT));
-    const float of_top = __shfl(top_d, first_lane + __ffsll((unsigned long long)has) - 1, 64);
-    from = R < 0.5 ? (double)of_top : 0.0;
+    from = R < 0.5 ? (double)top_d : 0.0;
 #pragma unroll
     for (int u = 0; u < kMost; ++u) {
+      if (u * NT >= a.k) break;
       s[u] *= inv;
       mean += s[u] == 0.0 ? 0.0 : s[u] * ((double)d[u] - from);
     }
