@@ -895,8 +895,11 @@ void launch_block(LogpArgs a, hipStream_t s) {
 // that four rows a CU are at different stages (3,355 x 20,000 bf16: 49 us, 65 with
 // 1,024).  Longer rows are read twice, 1,024 threads each, so that the second read
 // finds more of them in the last-level cache.  Where no gradient follows, 256
-// threads: more rows side by side (4,096 x 65,537 bf16: 97 us, 130 with 1,024).  Few
-// long rows are split.
+// threads: more rows side by side (4,096 x 65,537 bf16: 97 us, 130 with 1,024).  A
+// gradient from statistics reads a row once: 256 threads up to 2,500 vectors, 1,024 from
+// there on (f32, 256 / 1,024: 13,421 x 5,000 94 / 120 us, 26,843 x 10,000 426 / 375,
+// 13,421 x 20,000 424 / 390; bf16: 6,710 x 10,000 44 / 57, 13,421 x 20,000 212 / 198,
+// 6,710 x 40,000 213 / 191).  Few long rows are split.
 template <int DT, int FROM>
 int launch_logp(LogpArgs a, hipStream_t s) {
   constexpr int VE = Score<DT>::kVec;
@@ -951,7 +954,7 @@ int launch_logp(LogpArgs a, hipStream_t s) {
     launch_wide<DT, 1024, 8>(a, s);
   } else if (FROM == kSums && !step) {
     launch_block<DT, 256, kSums, false>(a, s);
-  } else if (FROM == kStats && a.C <= 40000) {
+  } else if (FROM == kStats && vecs <= 2500) {
     launch_block<DT, 256, kStats, true>(a, s);
   } else {
     launch_block<DT, 1024, FROM, true>(a, s);
