@@ -1054,11 +1054,14 @@ int check_pairs(const gbdt_pairs* p) {
 // Threads for a pair by its rows in the mean: each of a thread's rows costs latencies
 // (32 pairs of 128: 6 us with 256 threads, 10 with 64), each wave of a pair the pair's own
 // arithmetic, which counts where pairs are many (a step of 9,375 pairs of 64 rows of 3
-// classes: 28 us with 64 threads, 50 with 256).
+// classes: 28 us with 64 threads, 50 with 256).  1,024 threads pay for long pairs that do
+// not fill the CUs (losses over 7 classes, 1,024 / 256 threads: 16 pairs of 1,500 rows
+// 12 / 12 us, of 4,000 14 / 20; 128 of 4,000 19 / 28; 512 of 600 18 / 13, of 3,000
+// 37 / 34; 1,024 of 4,000 79 / 65).
 template <int DT>
 void launch_pairs_of(const PairArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.n_pairs);
-  if (a.n / a.n_pairs > 512) {
+  if (a.n / a.n_pairs > 1500 && a.n_pairs < 512) {
     hipLaunchKernelGGL((k_pairs<DT, 1024>), grid, dim3(1024), 0, s, a);
   } else if (a.n / a.n_pairs <= 128 && a.n_pairs >= 2048) {
     hipLaunchKernelGGL((k_pairs<DT, 64>), grid, dim3(64), 0, s, a);
