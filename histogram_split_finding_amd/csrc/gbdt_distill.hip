@@ -638,14 +638,8 @@ int distill(const gbdt_scores* x, const gbdt_teacher* t, float temperature, cons
   if ((MODE & kLoss) && !loss) return fail(GBDT_E_ARG, "loss is null");
   if (MODE == (kStats | kLoss) && !stats_out) return fail(GBDT_E_ARG, "stats is null");
   if (!(MODE & kStats) && !stats_in) return fail(GBDT_E_ARG, "stats is null");
-  if (MODE & kGrad) {
-    if (!grad) return fail(GBDT_E_ARG, "grad is null");
-    if (x->n_rows > 1 && grad_stride < x->n_classes)
-      return fail(GBDT_E_SHAPE, "grad_stride smaller than n_classes");
-    const uintptr_t es = x->dtype == GBDT_DTYPE_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(grad) % es) return fail(GBDT_E_ARG, "grad is misaligned");
-  }
-  rc = check_scores_ws(*x, ws, ws_bytes);
+  if (MODE & kGrad) rc = check_grad(*x, grad, grad_stride);
+  if (!rc) rc = check_scores_ws(*x, ws, ws_bytes);
   if (rc) return rc;
   DistillArgs a;
   a.x = x->data;
