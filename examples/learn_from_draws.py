@@ -41,6 +41,7 @@ def policy(rows=20000, steps=40, seed=0, device="cuda"):
     for _ in range(steps):
         scores = x @ weights
         u = torch.rand(rows, device=device, generator=gen)
+        # (all classes kept, temperature 1: old is then what the policy's ratio is to)
         g.gbdt_sample_classes(scores, u, None, None, None, None, classes, old, ws)
         reward = (classes == best).float()
         g.gbdt_class_logp(first, classes, 1.0, ref, None, ws)

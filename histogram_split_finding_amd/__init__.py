@@ -737,7 +737,9 @@ def gbdt_policy_loss(scores, classes, temperature, old_logp, ref_logp, advantage
                      loss, logp, dlogp, stats, ws, stream=None):
     """Forward pass of the clipped policy loss with a KL term.  Per row, float32
     [n]: old_logp, ref_logp (or None: no KL term), advantage, weight (or None);
-    out: loss, logp (or None), dlogp = weight times dloss/dlogp, stats [n, 2]."""
+    out: loss, logp (or None), dlogp = weight times dloss/dlogp, stats [n, 2].
+    old_logp and ref_logp are over all classes at `temperature`, as gbdt_class_logp
+    gives them; gbdt_sample_classes does where it keeps all classes."""
     s, dev, n, cp, wp, wb = _rows_of(scores, classes, ws)
     p = _policy(dev, n, old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl)
     f32 = _torch.float32

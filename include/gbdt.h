@@ -773,7 +773,8 @@ int gbdt_distill_step(const gbdt_scores* x /* host */, const gbdt_teacher* t /* 
  * point: the same inputs give the same classes).
  * out[n_rows]: the class, or -1 for a row without a score above -inf;
  * logp[n_rows] (or NULL): log(e_c / sum over the kept ones), -inf with -1.  A score of +inf
- * has e = 1 and leaves all finite ones e = 0.
+ * has e = 1 and leaves all finite ones e = 0.  (logp is the old_logp that gbdt_policy
+ * means only where all classes are kept and T is that of the policy's call.)
  * Per-row parameters (device, [n_rows]); NULL: T = 1, top_k = 0, top_p = 1,
  * min_p = 0.  T finite and >= 0; top_p, min_p in [0, 1]; u in [0, 1): a
  * row that breaks this is recorded as GBDT_E_RANGE and gets -1.  Host struct
@@ -805,6 +806,10 @@ int gbdt_sample_classes(const gbdt_scores* x /* host */, const float* u,
  * whose class is the only one left has logp 0, stats (-inf, 0) and gradient 0.
  * stats may be NULL in gbdt_class_logp.
  *
+ * o is a 64-bit sum of FP32 exponentials: with D the largest (m - x_c) / T, or 40 where
+ * that is less (terms further down add nothing), o is off by up to (3 D + 6) 2^-24 of
+ * it, logp by (1 - p) times that, beside its own rounding to FP32.
+ *
  * gbdt_class_logp_grad: with dlogp[n_rows] the derivative of some loss by each
  * logp, grad = dlogp_i dlogp_i/dx: dlogp_i / T times (1 at the class, else 0) -
  * softmax(x_i / T).  A row of dlogp 0 has gradient 0 whatever its scores.  grad:
@@ -829,7 +834,16 @@ int gbdt_class_logp_grad(const gbdt_scores* x /* host */, const int32_t* classes
  * old_logp, ref_logp, advantage, weight: device, [n_rows]; ref_logp may be NULL (no
  * KL term), weight may be NULL (ones); a row of weight 0 has slope and gradient 0
  * whatever the others.  clip_low in [0, 1], clip_high >= 0, kl finite and >= 0.
+ * On which side of a border a ratio lies is decided from FP64 exponentials.
  * Host struct holding device pointers.
+ *
+ * logp, old_logp and ref_logp are of the same kind of distribution: the softmax over all
+ * classes, at the call's one temperature.  gbdt_sample_classes's logp is that where it
+ * drew at this temperature with nothing cut off (top_k 0, top_p 1, min_p 0: its NULLs).
+ * Of other draws it is over the kept classes alone, larger than what is meant, and would
+ * move ratios down across the border: take old_logp from gbdt_class_logp, with the
+ * scores that were drawn from and the drawn classes.  Rows of different temperatures
+ * go in calls of their own.
  *
  * gbdt_policy_loss writes loss (not weighted), logp (may be NULL), dlogp = weight
  * times slope, and stats: the forward pass; gbdt_class_logp_grad with these is the
