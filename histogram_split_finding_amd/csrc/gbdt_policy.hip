@@ -62,7 +62,10 @@ struct LogpArgs {
   int64_t row0;       // of this launch
 };
 
-// exp(d / T) as a term of a sum, and as a factor of a gradient.
+// exp(d / T) as a term of a sum, and as a factor of a gradient.  In FP32 by choice (each
+// off by some 3 D 2^-24, the sums of them are FP64): FP64 ones bounded all rows of 33 to
+// 2,000 classes (sums of 262,144 x 256 bf16: 62 us, now 33, floor 24).  What they could
+// decide wrongly is taken again in FP64, see next_to_border.
 __device__ __forceinline__ float sum_term(const LogpArgs& a, float d) {
   return exp2_32(__builtin_fmaf(d, a.c_hi, d * a.c_lo));
 }
@@ -233,9 +236,11 @@ __device__ __forceinline__ void set_class(float (&f)[VE], int32_t cls, int32_t c
 // gradients pass through LDS, so that memory sees whole lines: packed rows of an odd
 // length as they lie there, 16 bytes at a time, others (up to 8 classes; longer ones
 // do not come here) in rows of C | 1 words.  Four classes at a time, -inf behind the
-// row's end.  Vector instructions bound it, 432 a wave, some 250 of them the row's FP64
-// (step of 581,012 x 7 f32: 12.8 us, floor 8.3; 19.1 when rows were staged word by word
-// and the exponentials were FP64).
+// row's end.  Step of 581,012 x 7 f32: 12.6 us, floor 8.3 (19.1 when rows were staged word
+// by word and the exponentials were FP64).  Vector instructions, 432 a wave and some 250
+// of them the row's FP64, are 6.6 us of it by the counters: what is left is that a
+// workgroup's loads, work and stores follow each other, and that nearly all workgroups
+// run at once, in phase.
 constexpr int kShortStep = 4;
 template <int DT, int R, int CMAX, int FROM>
 __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
@@ -348,9 +353,11 @@ __global__ void __launch_bounds__(R) k_logp_short(const LogpArgs a) {
 // NT lanes for a row that their V vectors of 16 bytes each hold whole, B rows one
 // after the other in registers.  What is FP64 about a row (some 250 instructions where
 // there is a policy) is done for B rows at once: lane b of the NT has row b.  From some
-// 200 classes on memory bounds it (steps of 67,108 x 1,000 bf16: 53 us, 5.1 TB/s; of
-// 33,537 x 2,001 f32: 100 us, 5.4 TB/s), below that vector instructions, the row's ends
-// and odd tails most (600,000 x 33 bf16: 48 us, floor 17).
+// 200 classes on it is near memory's rate (steps of 67,108 x 1,000 bf16: 51 us, 5.3 TB/s;
+// of 33,537 x 2,001 f32: 101 us, 5.3 TB/s), with 16-bit scores near that of the vector
+// instructions too.  Below that these bound it, the row's ends and odd tails most (600,000
+// x 33 bf16: sums 34 us, floor 9, steps 48 to 55, floor 17; two thirds of the time by the
+// counters).
 template <int DT, int NT, int V, int B, int FROM>
 __global__ void __launch_bounds__(256) k_logp_wave(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -550,7 +557,8 @@ __device__ __forceinline__ RowGrad finish_row(const LogpArgs& a, int64_t i, bool
 // A workgroup of NT threads for a row that their V vectors each hold whole: one read
 // where the gradient follows.  The first wave does what is FP64 about the row.  Memory
 // bounds it: steps of 22,369 x 3,000 bf16 50 us (5.4 TB/s; 122 when each row was read
-// twice by 256 threads), of 8,388 x 8,000 bf16 47 us.
+// twice by 256 threads), of 8,388 x 8,000 bf16 45 us.  A row that fills its registers
+// badly waits for its own end (13,421 x 5,000 bf16, 625 vectors of 1,024: 58 to 65 us).
 template <int DT, int NT, int V>
 __global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -759,7 +767,9 @@ struct PairArgs {
 // count (statistics other than (0, 0)), in FP64 in a fixed order, then the slope of
 // each row.  logp is taken from the statistics again: its FP32 value is off by up to
 // 2^-24 |logp|, some 10 times what o is, and the sums are small differences of many.
-// Latencies bound it: offsets, statistics, score, FP64 (4 pairs of 25 rows: 4.4 us).
+// Latencies bound it: offsets, statistics, score, FP64 (4 pairs of 25 rows: 4.6 us).  A
+// pair has one workgroup however long it is: the loss of one pair of 100,000 rows of 7
+// classes takes 143 us, of two of 50,000 73.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT) k_pairs(const PairArgs a) {
   __shared__ double sh[4][NT / 64];

@@ -108,9 +108,10 @@ __device__ __forceinline__ double sigmoid_64(float x, double* other = nullptr) {
 // a ballot, its first place there by comparisons.  Round j's score is kept by the lane
 // that works out weight j: the key itself, or read again where the key is a value.
 //
-// Vector instructions bound it: 1,584 a wave of four rows of 256 with a bias (16,384
-// rows: 18 us; 40 % of them the rounds, 30 % FP64 sigmoids), 645 a wave of eight rows of
-// 60 without (65,536 rows: 13 us).  More experts a lane save rounds' lane moves and
+// Vector instructions are its largest part, 1,584 a wave of four rows of 256 with a bias
+// (16,384 rows: 19 us, 11 of them by the counters; 40 % of the instructions the rounds,
+// 30 % FP64 sigmoids), 646 a wave of eight rows of 60 without (65,536 rows: 13 us, 8.7 of
+// them); the rest are the rounds' dependent steps at 4 and 8 waves a SIMD.  More experts a lane save rounds' lane moves and
 // lose waves that cover for each other (8 lanes of 32: 20 us; 32 lanes of 8: 20 us).
 // One row takes 5.6 us, with 64 lanes (10 with 16).
 template <int DT, int NT, int EPL, bool BY_VALUE>
@@ -304,8 +305,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
 // NT lanes a row that their V vectors of 16 bytes each hold whole.  A byte per
 // expert in LDS says which place of the list has it: the mass outside the choice is
 // summed by itself (as 1 less the rest it would lose its digits).  65,536 x 128 f32
-// softmax: 14.6 us, 4.8 TB/s; all rows are in flight at once, so reads and writes do not
-// overlap.
+// softmax: 14.3 us, 4.9 TB/s; all rows are in flight at once, so reads and writes do not
+// overlap.  Other forms read the chosen scores alone: 12 us, floor 7.
 template <int DT, int NT, int V>
 __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const RouteArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kCountThreads) k_list_count(const ListArgs a) 
 // lists begin; of those before it: where its own part of each list does), then takes
 // its places in order: a wave's 64 at a time, each behind the places before it of
 // the same expert, which the wave finds by a ballot per bit of the expert.  Latencies
-// bound it (131,072 places of 256 experts: 6.3 us, and 4 us for the counts).
+// bound it (131,072 places of 256 experts: 6.5 us, and 4 us for the counts).
 template <int NT>
 __global__ void __launch_bounds__(NT) k_list_place(const ListArgs a) {
   constexpr int W = NT / 64, EPT = (GBDT_MAX_EXPERTS + NT - 1) / NT;
@@ -833,6 +834,11 @@ int gbdt_route_lists(const int32_t* classes, int64_t n_places, int32_t n_experts
   a.place = place;
   a.err = &static_cast<WsCtrl*>(ws)->err;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  // Up to kAlone places one workgroup does it all (3,000 places of 64 and of 1,024 experts
+  // alone 7.0 and 8.8 us, with counts 10.0 and 9.5; 6,000: 11.7 and 15.1, 9.1 and 10.7).
+  // More go to workgroups of kChunk places or more (65,536 places of 64 and of 1,024
+  // experts with 512, 1,024, 2,048 and 4,096: 9.5, 9.3, 10.0, 13.6 and 15.8, 12.5, 13.2,
+  // 17.5 us), as many as the counts have room for.
   constexpr int64_t kAlone = 4096, kChunk = 1024, kMostBlocks = 256;
   static_assert(kMostBlocks * GBDT_MAX_EXPERTS * 4 <= kScoresPartBytes, "the counts fit the workspace");
   a.blocks = 1;
