@@ -632,11 +632,13 @@ __global__ void __launch_bounds__(NT, 8) k_logp_wide(const LogpArgs a) {
 //
 // Memory bounds it where rows are many: step of 4,096 x 131,072 bf16 419 us (4.9 TB/s of
 // what has to move, the rate of a copy; the second read comes from the last-level
-// cache), gradient of 2,048 x 50,001 f32 148 us (5.2 TB/s), sums of 4,096 x 65,537 bf16
-// 96 us (5.0 TB/s).  Loading the next block before this one is worked on made it
+// cache), gradient of 2,048 x 50,001 f32 148 us (5.5 TB/s), sums of 4,096 x 65,537 bf16
+// 112 to 119 us (4.5 to 4.8 TB/s; 94 in a preference step, which ends on the rows that
+// the next one begins with).  Loading the next block before this one is worked on made it
 // slower (policy loss of 1,000 x 32,003 f16: 19.4 us, 17.6 without): four to eight
 // workgroups a CU cover for each other.  What is left there is the chain of a row of
-// its own: class, scores, joined sums, FP64 (4 us of 17).
+// its own, class, scores, joined sums, FP64 (4 us of 17, floor 10), and 3 us not accounted
+// for.
 template <int DT, int NT, int FROM, bool GRAD>
 __global__ void __launch_bounds__(NT, 8) k_logp_block(const LogpArgs a) {
   using Elem = typename Score<DT>::Elem;
@@ -905,9 +907,9 @@ void launch_block(LogpArgs a, hipStream_t s) {
 // that four rows a CU are at different stages (3,355 x 20,000 bf16: 49 us, 65 with
 // 1,024).  Longer rows are read twice, 1,024 threads each, so that the second read
 // finds more of them in the last-level cache.  Where no gradient follows, 256
-// threads: more rows side by side (4,096 x 65,537 bf16: 97 us, 130 with 1,024).  A
-// gradient from statistics reads a row once: 256 threads up to 2,500 vectors, 1,024 from
-// there on (f32, 256 / 1,024: 13,421 x 5,000 94 / 120 us, 26,843 x 10,000 426 / 375,
+// threads: more rows side by side (4,096 x 65,537 bf16 in a preference step: 94 us, 130
+// with 1,024).  A gradient from statistics reads a row once: 256 threads up to 2,500
+// vectors, 1,024 from there on (f32, 256 / 1,024: 13,421 x 5,000 94 / 120 us, 26,843 x 10,000 426 / 375,
 // 13,421 x 20,000 424 / 390; bf16: 6,710 x 10,000 44 / 57, 13,421 x 20,000 212 / 198,
 // 6,710 x 40,000 213 / 191).  Few long rows are split.
 template <int DT, int FROM>
