@@ -270,3 +270,31 @@ def test_dweights_that_are_no_numbers(form, bad):
         assert not np.isfinite(got[i, c[i, 1]])
         if not r.score and not r.renormalise:
             assert not np.isfinite(got[i][~out[i]]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_odd_sigmoids(renormalise, dtype):
+    """Infinities, NaN, the largest numbers and equal scores under a sigmoid: FP64, rounded
+    once, and 2^-45 as above."""
+    say("route gradient, odd sigmoids: %s %s" % (renormalise, dtype))
+    E, k = 60, 8
+    rng = np.random.default_rng(6)
+    b = np.round(rng.normal(0.0, 1.5, (8, E)))
+    b[0] = -np.inf
+    b[1] = 0.0
+    b[2, rng.random(E) < 0.5] = np.nan
+    b[3, ::2] = np.inf
+    b[4] = np.where(np.arange(E) % 3 == 0, 6.0e4, -6.0e4)
+    b[5, 1:] = -np.inf
+    b[6] = np.nan
+    t = torch.from_numpy(b).to(ref.TYPES[dtype])
+    x, xh = ref.place(t, 3), t.double().numpy()
+    r = g.make_routing(k, sigmoid=True, renormalise=renormalise, scale=0.7)
+    for c in (route(x, r)[0].cpu().numpy(), np.stack([rng.permutation(E)[:k] for _ in b]).astype(np.int32)):
+        dw = rng.normal(0.0, 1.0, (len(b), k)).astype(np.float32)
+        got = gradient(x, r, to_dev(c), dw)
+        for i in range(len(b)):
+            want, size = rref.grad(xh[i], r, c[i], dw[i])
+            tol = (ref.EPS[dtype] / 2 + STEP) * np.abs(want) + 2.0 ** -45 * size + TINY[dtype]
+            assert np.all(np.abs(got[i] - want) <= tol), (i, got[i], want)
